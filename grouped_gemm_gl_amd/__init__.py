@@ -29,11 +29,15 @@ __all__ = [
     "gl_offsets_quantize_mxfp8", "gl_offsets_quantize_mxfp8_rowwise_colwise", "gl_quantize_mxfp8_weights",
     "gl_dgrad_mxfp8", "gl_wgrad_mxfp8", "gl_swiglu_forward", "gl_swiglu_backward",
     "gl_grouped_mlp_forward", "gl_grouped_mlp_backward", "WgradQueue", "gl_forward_noalloc",
-    "NOALLOC_MAX_GROUPS",
+    "NOALLOC_MAX_GROUPS", "gl_rmsnorm_forward", "gl_rmsnorm_workspace_size", "gl_rmsnorm_backward",
+    "GL_SCORE_SOFTMAX", "GL_SCORE_SIGMOID", "gl_route_workspace_size", "gl_route_forward", "gl_route_backward",
+    "gl_moe_few_tokens_workspace_size", "gl_moe_few_tokens", "MOE_MAX_TOKENS",
 ]
 
 GL_F32, GL_BF16, GL_F16, GL_E4M3 = 0, 1, 2, 3
 NOALLOC_MAX_GROUPS = 16384  # GL_NOALLOC_MAX_GROUPS
+GL_SCORE_SOFTMAX, GL_SCORE_SIGMOID = 0, 1
+MOE_MAX_TOKENS = 64  # GL_MOE_MAX_TOKENS
 GL_STATUS_NEGATIVE_SPLIT, GL_STATUS_SUM_MISMATCH, GL_STATUS_WORKSPACE = 1, 2, 4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -95,6 +99,14 @@ def load():
         "gl_wgrad_queue_flush": (I, [P, P]),
         "gl_wgrad_queue_clear": (I, [P]),
         "gl_forward_noalloc": (I, [I, I64, I64, I64, I, I] + [P] * 10 + [I64, P]),
+        "gl_rmsnorm_forward": (I, [I64, I64, I, I, P, P, P, ctypes.c_float, P, P, P, P, P]),
+        "gl_rmsnorm_workspace_size": (ctypes.c_size_t, [I64, I64]),
+        "gl_rmsnorm_backward": (I, [I64, I64, I, I, P, P, P, P, ctypes.c_float, P, I, P, I, P, P]),
+        "gl_route_workspace_size": (ctypes.c_size_t, [I64, I]),
+        "gl_route_forward": (I, [I64, I, I, I, I, I] + [P] * 8),
+        "gl_route_backward": (I, [I64, I, I, I, I, I] + [P] * 5),
+        "gl_moe_few_tokens_workspace_size": (ctypes.c_size_t, [I64, I, I, I64]),
+        "gl_moe_few_tokens": (I, [I, I64, I64, I64, I64, I, I, I] + [P] * 17 + [I64, P, P]),
         "gl_last_error": (ctypes.c_char_p, []),
         "gl_version": (ctypes.c_char_p, []),
     }
@@ -528,6 +540,184 @@ def gl_wgrad_mxfp8(dy_t: Tensor, dy_t_scale: Tensor, x_t: Tensor, x_t_scale: Ten
                                  _stream(stream)))
     del keep
     return dw
+
+
+# -------------------------------------------------------------------- expert block
+
+
+def _on_one_device(first: Tensor, *others) -> None:
+    """Every given tensor (lists of them too) is on ``first``'s GPU."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    for t in others:
+        for u in (t,) if isinstance(t, Tensor) else t or ():
+            if u.device != dev:
+                raise ValueError(f"tensors must be on one device (got {dev} and {u.device})")
+
+
+def _enough(workspace: Optional[Tensor], size: int) -> None:
+    if workspace is None or workspace.numel() * workspace.element_size() < size:
+        raise ValueError(f"workspace must hold {size} bytes")
+
+
+def gl_rmsnorm_forward(x: Tensor, gamma: Tensor, eps: float, *, residual: Optional[Tensor] = None,
+                       h: Optional[Tensor] = None, y: Optional[Tensor] = None, data: Optional[Tensor] = None,
+                       scale: Optional[Tensor] = None, stream=None) -> None:
+    """RMS norm of s = x (+ residual), [T, C]: h = s, y = s rstd gamma, and / or the MXFP8
+    codes of y, data [T, C] / scale [T, C/32].  gamma [C] is fp32 or of x's dtype; h may be
+    ``x`` or ``residual`` itself."""
+    if x.dim() != 2 or gamma.shape != (x.shape[1],):
+        raise ValueError("x must be [T, C] and gamma [C]")
+    T, C = x.shape
+    for t in (residual, h, y):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError("residual, h and y must have x's shape and dtype")
+    if data is not None and (data.shape != x.shape or data.dtype != torch.uint8):
+        raise ValueError("data must be uint8 [T, C]")
+    if scale is not None and (scale.shape != (T, C // 32) or scale.dtype != torch.uint8):
+        raise ValueError("scale must be uint8 [T, C/32]")
+    _on_one_device(x, gamma, residual, h, y, data, scale)
+    _check(load().gl_rmsnorm_forward(T, C, _dtype(x), _dtype(gamma), _ptr(x), _ptr(residual), _ptr(gamma), eps,
+                                     _ptr(h), _ptr(y), _ptr(data), _ptr(scale), _stream(stream)))
+
+
+def gl_rmsnorm_workspace_size(total_rows: int, features: int) -> int:
+    """Bytes of the workspace gl_rmsnorm_backward needs for dgamma."""
+    return int(load().gl_rmsnorm_workspace_size(int(total_rows), int(features)))
+
+
+def gl_rmsnorm_backward(dy: Tensor, h: Tensor, gamma: Tensor, eps: float, dx: Tensor, *,
+                        dh: Optional[Tensor] = None, dgamma: Optional[Tensor] = None, accumulate: bool = False,
+                        workspace: Optional[Tensor] = None, stream=None) -> Tensor:
+    """Gradient of the norm at h, [T, C]: dx (of x and of the residual alike, with dh, the
+    gradient arriving at h, added) and dgamma [C] (fp32 or of h's dtype; added into with
+    ``accumulate``), which needs ``workspace``."""
+    if h.dim() != 2 or gamma.shape != (h.shape[1],):
+        raise ValueError("h must be [T, C] and gamma [C]")
+    T, C = h.shape
+    for t in (dy, dx, dh):
+        if t is not None and (t.shape != h.shape or t.dtype != h.dtype):
+            raise ValueError("dy, dx and dh must have h's shape and dtype")
+    if dgamma is not None:
+        if dgamma.shape != (C,):
+            raise ValueError("dgamma must be [C]")
+        _enough(workspace, gl_rmsnorm_workspace_size(T, C))
+    _on_one_device(h, dy, gamma, dx, dh, dgamma, workspace)
+    _check(load().gl_rmsnorm_backward(T, C, _dtype(h), _dtype(gamma), _ptr(dy), _ptr(dh), _ptr(h), _ptr(gamma), eps,
+                                      _ptr(dx), GL_F32 if dgamma is None else _dtype(dgamma), _ptr(dgamma),
+                                      int(bool(accumulate)), _ptr(workspace), _stream(stream)))
+    return dx
+
+
+
+def _route_args(logits: Tensor, ids: Tensor, weights: Tensor):
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0] or weights.shape != ids.shape:
+        raise ValueError("logits must be [T, E], ids and the weights [T, top_k]")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 and the weights float32")
+    return logits.shape[0], logits.shape[1], ids.shape[1]
+
+
+def gl_route_workspace_size(total_rows: int, num_experts: int) -> int:
+    """Bytes of the workspace a routing plan needs."""
+    return int(load().gl_route_workspace_size(int(total_rows), int(num_experts)))
+
+
+def gl_route_forward(logits: Tensor, ids: Tensor, weights: Tensor, *, score: int = GL_SCORE_SOFTMAX,
+                     renormalize: bool = True, m_splits: Optional[Tensor] = None, row_index: Optional[Tensor] = None,
+                     slot_index: Optional[Tensor] = None, workspace: Optional[Tensor] = None, stream=None):
+    """The top_k experts of each token, ids int32 [T, top_k], and their weights (float32)
+    from logits [T, E]; with m_splits (int64 [E]), row_index (int32 [T, top_k]) and
+    slot_index (int32 [T * top_k]) also the plan that orders the slots by expert."""
+    T, E, k = _route_args(logits, ids, weights)
+    if (m_splits is None) != (row_index is None) or (m_splits is None) != (slot_index is None):
+        raise ValueError("give m_splits, row_index and slot_index, or none of them")
+    if m_splits is not None:
+        if m_splits.shape != (E,) or m_splits.dtype != torch.int64:
+            raise ValueError("m_splits must be int64 [E]")
+        if row_index.shape != (T, k) or slot_index.shape != (T * k,):
+            raise ValueError("row_index must be [T, top_k] and slot_index [T * top_k]")
+        if row_index.dtype != torch.int32 or slot_index.dtype != torch.int32:
+            raise ValueError("row_index and slot_index must be int32")
+        _enough(workspace, gl_route_workspace_size(T, E))
+    _on_one_device(logits, ids, weights, m_splits, row_index, slot_index, workspace)
+    _check(load().gl_route_forward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), _ptr(logits),
+                                   _ptr(ids), _ptr(weights), _ptr(m_splits), _ptr(row_index), _ptr(slot_index),
+                                   _ptr(workspace), _stream(stream)))
+    return ids, weights
+
+
+def gl_route_backward(logits: Tensor, ids: Tensor, dweights: Tensor, dlogits: Tensor, *,
+                      score: int = GL_SCORE_SOFTMAX, renormalize: bool = True, stream=None) -> Tensor:
+    """dlogits [T, E]: the gradient of gl_route_forward's weights at its logits and ids."""
+    T, E, k = _route_args(logits, ids, dweights)
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must have the shape and dtype of logits")
+    _on_one_device(logits, ids, dweights, dlogits)
+    _check(load().gl_route_backward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), _ptr(logits),
+                                    _ptr(ids), _ptr(dweights), _ptr(dlogits), _stream(stream)))
+    return dlogits
+
+
+def gl_moe_few_tokens_workspace_size(total_rows: int, top_k: int, num_experts: int, ffn_features: int) -> int:
+    """Bytes of the workspace gl_moe_few_tokens needs."""
+    return int(load().gl_moe_few_tokens_workspace_size(int(total_rows), int(top_k), int(num_experts),
+                                                       int(ffn_features)))
+
+
+def _each_shape(g: Optional[Grouped], G: int, shape, dtype, what: str) -> None:
+    """Checks a stacked tensor [G, *shape] or a list of G tensors of that shape."""
+    if g is None:
+        return
+    if isinstance(g, Tensor):
+        good = tuple(g.shape) == (G, *shape) and g.dtype == dtype
+    else:
+        good = len(g) == G and all(tuple(t.shape) == tuple(shape) and t.dtype == dtype for t in g)
+    if not good:
+        raise ValueError(f"{what} must be [{G}, {', '.join(map(str, shape))}] or {G} tensors, of {dtype}")
+
+
+def gl_moe_few_tokens(x: Tensor, ids: Tensor, weights: Tensor, w1: Grouped, w2: Grouped, y: Tensor,
+                      workspace: Tensor, *, w1_scale: Optional[Grouped] = None, w2_scale: Optional[Grouped] = None,
+                      b1: Optional[Grouped] = None, b2: Optional[Grouped] = None,
+                      residual: Optional[Tensor] = None, stream=None) -> Tensor:
+    """y[t] = residual[t] + sum_j weights[t, j] (W2_e SwiGLU(W1_e x[t] + b1_e) + b2_e) with
+    e = ids[t, j], for at most MOE_MAX_TOKENS tokens; slots whose id is outside
+    [0, E) take no part.
+
+    x: [T, K]; w1: [E, 2F, K], w2: [E, N, F] stacked or per expert, of x's dtype, or uint8
+    E4M3 codes with ``w1_scale`` [E, 2F, K/32] / ``w2_scale`` [E, N, F/32] and bf16 x."""
+    E = w1.shape[0] if isinstance(w1, Tensor) else len(w1)
+    F2, K = _first(w1).shape[-2:]
+    N, F = _first(w2).shape[-2:]
+    T, k = ids.shape
+    if x.shape != (T, K) or F2 != 2 * F or y.dim() != 2 or y.shape[1] != N:
+        raise ValueError("shapes: x [T, K], ids [T, top_k], w1 [E, 2F, K], w2 [E, N, F], y [rows >= T, N]")
+    if weights.shape != ids.shape or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 and weights float32, both [T, top_k]")
+    if y.dtype != x.dtype or (residual is not None and (residual.shape != (T, N) or residual.dtype != x.dtype)):
+        raise ValueError("y and residual [T, N] must have x's dtype")
+    wd = _first(w1).dtype
+    _each_shape(w1, E, (F2, K), wd, "w1")
+    _each_shape(w2, E, (N, F), wd, "w2")
+    _each_shape(w1_scale, E, (F2, K // 32), torch.uint8, "w1_scale")
+    _each_shape(w2_scale, E, (N, F // 32), torch.uint8, "w2_scale")
+    _each_shape(b1, E, (F2,), x.dtype, "b1")
+    _each_shape(b2, E, (N,), x.dtype, "b2")
+    _enough(workspace, gl_moe_few_tokens_workspace_size(T, k, E, F))
+    _on_one_device(x, ids, weights, w1, w2, y, workspace, w1_scale, w2_scale, b1, b2, residual)
+    p1, pp1, k1 = _grouped(w1, x.device, stream)
+    p2, pp2, k2 = _grouped(w2, x.device, stream)
+    s1, ss1, k3 = _grouped(w1_scale, x.device, stream)
+    s2, ss2, k4 = _grouped(w2_scale, x.device, stream)
+    q1, qq1, k5 = _grouped(b1, x.device, stream)
+    q2, qq2, k6 = _grouped(b2, x.device, stream)
+    _check(load().gl_moe_few_tokens(E, K, F, N, T, k, _dtype(x), _DT[wd] if wd in _DT else -1, _ptr(x), _ptr(ids),
+                                    _ptr(weights), p1, pp1, s1, ss1, q1, qq1, p2, pp2, s2, ss2, q2, qq2,
+                                    _ptr(residual), _ptr(y), y.shape[0], _ptr(workspace), _stream(stream)))
+    del k1, k2, k3, k4, k5, k6
+    return y
 
 
 def _tensors(obj):

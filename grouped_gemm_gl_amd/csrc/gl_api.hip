@@ -6,6 +6,7 @@
 // fuser_forward checks; caller buffers are validated by shape/dtype/contiguity on
 // page "[PyTorch] Add optional caller-provided output/grad-input buffers ...").  On
 // an error nothing is launched and the message is kept per thread.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -62,6 +63,26 @@ hipError_t launch_quantize_mxfp8_weights(const uint16_t *w, int G, int64_t N, in
                                          hipStream_t s);
 hipError_t launch_swiglu_fwd(int el, int64_t T, int64_t F, const void *h, void *a, hipStream_t s);
 hipError_t launch_swiglu_bwd(int el, int64_t T, int64_t F, const void *h, const void *da, void *dh, hipStream_t s);
+hipError_t launch_rmsnorm_fwd(int el, bool g32, int64_t T, int64_t C, const void *x, const void *residual,
+                              const void *gamma, float eps, void *h, void *y, uint8_t *data, uint8_t *scale,
+                              hipStream_t s);
+hipError_t launch_rmsnorm_bwd(int el, bool g32, int64_t T, int64_t C, const void *dy, const void *dh, const void *h,
+                              const void *gamma, float eps, void *dx, int el_dgamma, void *dgamma, int accumulate,
+                              float *part, hipStream_t s);
+int rmsnorm_bwd_blocks(int64_t T);
+size_t route_plan_bytes(int64_t T, int E);
+hipError_t launch_route_fwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits, int32_t *ids,
+                            float *weights, int64_t *m_splits, int32_t *row_index, int32_t *slot_index, void *ws,
+                            hipStream_t s);
+hipError_t launch_route_bwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits,
+                            const int32_t *ids, const float *dweights, void *dlogits, hipStream_t s);
+size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t F);
+hipError_t launch_moe(int el, bool mx, int E, int64_t K, int64_t F, int64_t N, int64_t T, int k, const void *x,
+                      const int32_t *ids, const float *gates, const void *w1, const void *const *w1_ptrs,
+                      const uint8_t *w1_scale, const uint8_t *const *w1_scale_ptrs, const void *b1,
+                      const void *const *b1_ptrs, const void *w2, const void *const *w2_ptrs,
+                      const uint8_t *w2_scale, const uint8_t *const *w2_scale_ptrs, const void *b2,
+                      const void *const *b2_ptrs, const void *residual, void *y, void *ws, hipStream_t s);
 hipError_t launch_wgrad_mxfp8(int G, int64_t K, int64_t N, int64_t T, const uint8_t *dyt, const uint8_t *dyt_s,
                               const uint8_t *xt, const uint8_t *xt_s, int64_t ld, void *dw, void *const *dw_ptrs,
                               int out_f32, int accumulate, const void *ws, hipStream_t s);
@@ -586,7 +607,7 @@ int swiglu_check(const char *who, int64_t T, int64_t F, gl_dtype dtype, const vo
     return fail(GL_ERR_ARG, "%s: buffers must be 16-byte aligned", who);
   return GL_OK;
 }
-int sw_el(gl_dtype d) { return d == GL_F32 ? 1 : d == GL_F16 ? 2 : 0; }
+int el_code(gl_dtype d) { return d == GL_F32 ? 1 : d == GL_F16 ? 2 : 0; }
 }  // namespace
 
 extern "C" {
@@ -594,14 +615,14 @@ extern "C" {
 int gl_swiglu_forward(int64_t total_rows, int64_t F, gl_dtype dtype, const void *h, void *a, hipStream_t stream) {
   GL_TRY(swiglu_check("gl_swiglu_forward", total_rows, F, dtype, h, nullptr, a, false));
   if (total_rows == 0) return ok();
-  return hip_result(gl::launch_swiglu_fwd(sw_el(dtype), total_rows, F, h, a, stream), "gl_swiglu_forward");
+  return hip_result(gl::launch_swiglu_fwd(el_code(dtype), total_rows, F, h, a, stream), "gl_swiglu_forward");
 }
 
 int gl_swiglu_backward(int64_t total_rows, int64_t F, gl_dtype dtype, const void *h, const void *da, void *dh,
                        hipStream_t stream) {
   GL_TRY(swiglu_check("gl_swiglu_backward", total_rows, F, dtype, h, da, dh, true));
   if (total_rows == 0) return ok();
-  return hip_result(gl::launch_swiglu_bwd(sw_el(dtype), total_rows, F, h, da, dh, stream), "gl_swiglu_backward");
+  return hip_result(gl::launch_swiglu_bwd(el_code(dtype), total_rows, F, h, da, dh, stream), "gl_swiglu_backward");
 }
 
 int gl_grouped_mlp_forward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t out_features,
@@ -621,7 +642,7 @@ int gl_grouped_mlp_forward(int num_groups, int64_t in_features, int64_t ffn_feat
   if (T == 0) return ok();
   GL_TRY(forward_impl(G, K, 2 * F, T, dtype, dtype, x, nullptr, w1, w1_ptrs, nullptr, nullptr, b1, b1_ptrs, h, T,
                       workspace, stream, true));
-  GL_TRY(hip_result(gl::launch_swiglu_fwd(sw_el(dtype), T, F, h, a, stream), "gl_grouped_mlp_forward"));
+  GL_TRY(hip_result(gl::launch_swiglu_fwd(el_code(dtype), T, F, h, a, stream), "gl_grouped_mlp_forward"));
   return forward_impl(G, F, N, T, dtype, dtype, a, nullptr, w2, w2_ptrs, nullptr, nullptr, b2, b2_ptrs, y, y_rows,
                       workspace, stream, true);
 }
@@ -658,9 +679,209 @@ int gl_grouped_mlp_backward(int num_groups, int64_t in_features, int64_t ffn_fea
   GL_TRY(fc1_dgrad(false));
   GL_TRY(fc2_wgrad(true));  // also runs for T == 0: empty groups' weight and bias gradients
   GL_TRY(fc2_dgrad(true));
-  if (T > 0) GL_TRY(hip_result(gl::launch_swiglu_bwd(sw_el(dtype), T, F, h, da, dh, stream), "gl_grouped_mlp_backward"));
+  if (T > 0) GL_TRY(hip_result(gl::launch_swiglu_bwd(el_code(dtype), T, F, h, da, dh, stream), "gl_grouped_mlp_backward"));
   GL_TRY(fc1_wgrad(true));
   return fc1_dgrad(true);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- expert block --
+// The RMS norm in front of the experts, the token routing and the expert layer for a
+// few tokens.
+
+namespace {
+int check_norm(const char *who, int64_t T, int64_t C, gl_dtype dtype, gl_dtype gamma_dtype, const void *gamma,
+               float eps) {
+  if (T < 0 || C <= 0) return fail(GL_ERR_ARG, "%s: invalid sizes (T %lld, C %lld)", who, (long long)T, (long long)C);
+  GL_TRY(check_float_dtype(dtype, who));
+  if (gamma_dtype != GL_F32 && gamma_dtype != dtype) return fail(GL_ERR_DTYPE, "%s: gamma is fp32 or of dtype", who);
+  const int v = is16(dtype) ? 8 : 4;
+  if (C % v) return fail(GL_ERR_SHAPE, "%s: C must be a multiple of %d (got %lld)", who, v, (long long)C);
+  if (C > kMaxBf16Dim) return fail(GL_ERR_SHAPE, "%s: C must be at most 2^22", who);
+  if (T > INT32_MAX) return fail(GL_ERR_SHAPE, "%s: at most 2^31 - 1 rows", who);
+  if (!gamma || !aligned16(gamma)) return fail(GL_ERR_ARG, "%s: gamma NULL or not 16-byte aligned", who);
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(GL_ERR_ARG, "%s: eps must be finite and at least 0", who);
+  return GL_OK;
+}
+
+int check_route(const char *who, int64_t T, int E, int k, gl_dtype dtype, int score, int renormalize) {
+  if (T < 0 || E <= 0 || k <= 0)
+    return fail(GL_ERR_ARG, "%s: invalid sizes (T %lld, E %d, top_k %d)", who, (long long)T, E, k);
+  GL_TRY(check_float_dtype(dtype, who));
+  if (E > GL_ROUTE_MAX_EXPERTS) return fail(GL_ERR_SHAPE, "%s: at most %d experts (got %d)", who,
+                                            GL_ROUTE_MAX_EXPERTS, E);
+  if (k > E || k > GL_ROUTE_MAX_TOP_K)
+    return fail(GL_ERR_SHAPE, "%s: top_k is at most %d and the number of experts (got %d)", who, GL_ROUTE_MAX_TOP_K,
+                k);
+  if (T * k > INT32_MAX) return fail(GL_ERR_SHAPE, "%s: T * top_k exceeds 2^31 - 1", who);
+  if (score != GL_SCORE_SOFTMAX && score != GL_SCORE_SIGMOID)
+    return fail(GL_ERR_ARG, "%s: score must be GL_SCORE_SOFTMAX or GL_SCORE_SIGMOID", who);
+  if (renormalize != 0 && renormalize != 1) return fail(GL_ERR_ARG, "%s: renormalize must be 0 or 1", who);
+  return GL_OK;
+}
+
+// Scales of MXFP8 expert weights: in the weights' form, 4-byte aligned.
+int check_scales(const void *w, const void *w_ptrs, const void *scale, const void *scale_ptrs, const char *what) {
+  if ((w != nullptr) != (scale != nullptr) || (w_ptrs != nullptr) != (scale_ptrs != nullptr))
+    return fail(GL_ERR_ARG, "%s: scales must come in the same form as the weights", what);
+  if ((uintptr_t)scale & 3u) return fail(GL_ERR_ARG, "%s: scales not 4-byte aligned", what);
+  if ((uintptr_t)scale_ptrs & 7u) return fail(GL_ERR_ARG, "%s: scale pointer array not 8-byte aligned", what);
+  return GL_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int gl_rmsnorm_forward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_dtype gamma_dtype, const void *x,
+                       const void *residual, const void *gamma, float eps, void *h, void *y, uint8_t *data,
+                       uint8_t *scale, hipStream_t stream) {
+  const char *who = "gl_rmsnorm_forward";
+  const int64_t T = total_rows, C = features;
+  GL_TRY(check_norm(who, T, C, dtype, gamma_dtype, gamma, eps));
+  if ((data && C % 32) || (scale && C % 32))
+    return fail(GL_ERR_SHAPE, "%s: MXFP8 output needs C %% 32 == 0 (got %lld)", who, (long long)C);
+  if (T == 0) return ok();
+  if ((data == nullptr) != (scale == nullptr)) return fail(GL_ERR_ARG, "%s: give both data and scale, or neither", who);
+  if (!y && !data) return fail(GL_ERR_ARG, "%s: neither y nor data is given", who);
+  GL_TRY(check_buf(x, T, "x"));
+  if (!aligned16(residual) || !aligned16(h) || !aligned16(y) || !aligned16(data))
+    return fail(GL_ERR_ARG, "%s: buffers must be 16-byte aligned", who);
+  return hip_result(gl::launch_rmsnorm_fwd(el_code(dtype), gamma_dtype == GL_F32, T, C, x, residual, gamma, eps, h, y,
+                                           data, scale, stream),
+                    who);
+}
+
+size_t gl_rmsnorm_workspace_size(int64_t total_rows, int64_t features) {
+  if (total_rows < 0 || features <= 0) return 0;
+  const size_t bytes = (size_t)gl::rmsnorm_bwd_blocks(total_rows) * (size_t)features * 4;
+  return bytes > 16 ? (bytes + 15) & ~(size_t)15 : 16;
+}
+
+int gl_rmsnorm_backward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_dtype gamma_dtype, const void *dy,
+                        const void *dh, const void *h, const void *gamma, float eps, void *dx,
+                        gl_dtype dgamma_dtype, void *dgamma, int accumulate, void *workspace, hipStream_t stream) {
+  const char *who = "gl_rmsnorm_backward";
+  const int64_t T = total_rows, C = features;
+  GL_TRY(check_norm(who, T, C, dtype, gamma_dtype, gamma, eps));
+  if (accumulate != 0 && accumulate != 1) return fail(GL_ERR_ARG, "accumulate must be 0 or 1");
+  if (dgamma) {
+    if (dgamma_dtype != GL_F32 && dgamma_dtype != dtype)
+      return fail(GL_ERR_DTYPE, "%s: dgamma is fp32 or of dtype", who);
+    if (!aligned16(dgamma)) return fail(GL_ERR_ARG, "%s: dgamma not 16-byte aligned", who);
+    if (!workspace || !aligned16(workspace)) return fail(GL_ERR_ARG, "workspace NULL or not 16-byte aligned");
+  }
+  GL_TRY(check_buf(dy, T, "dy"));
+  GL_TRY(check_buf(h, T, "h"));
+  GL_TRY(check_buf(dx, T, "dx"));
+  if (T > 0 && !aligned16(dh)) return fail(GL_ERR_ARG, "dh not 16-byte aligned");
+  if (T == 0 && !dgamma) return ok();
+  return hip_result(gl::launch_rmsnorm_bwd(el_code(dtype), gamma_dtype == GL_F32, T, C, dy, dh, h, gamma, eps, dx,
+                                           el_code(dgamma_dtype), dgamma, accumulate, (float *)workspace, stream),
+                    who);
+}
+
+size_t gl_route_workspace_size(int64_t total_rows, int num_experts) {
+  if (total_rows < 0 || num_experts <= 0) return 0;
+  return gl::route_plan_bytes(total_rows, num_experts);
+}
+
+int gl_route_forward(int64_t total_rows, int num_experts, int top_k, gl_dtype dtype, int score, int renormalize,
+                     const void *logits, int32_t *ids, float *weights, int64_t *m_splits, int32_t *row_index,
+                     int32_t *slot_index, void *workspace, hipStream_t stream) {
+  const char *who = "gl_route_forward";
+  const int64_t T = total_rows;
+  GL_TRY(check_route(who, T, num_experts, top_k, dtype, score, renormalize));
+  const bool plan = m_splits != nullptr;
+  if (T > 0 && (plan != (row_index != nullptr) || plan != (slot_index != nullptr)))
+    return fail(GL_ERR_ARG, "%s: give m_splits, row_index and slot_index, or none of them", who);
+  if (plan && ((uintptr_t)m_splits & 7u)) return fail(GL_ERR_ARG, "m_splits not 8-byte aligned");
+  if (plan && (!workspace || !aligned16(workspace)))
+    return fail(GL_ERR_ARG, "workspace NULL or not 16-byte aligned");
+  GL_TRY(check_buf(logits, T, "logits"));
+  GL_TRY(check_buf(ids, T, "ids"));
+  GL_TRY(check_buf(weights, T, "weights"));
+  if (plan && (!aligned16(row_index) || !aligned16(slot_index)))
+    return fail(GL_ERR_ARG, "%s: row_index and slot_index must be 16-byte aligned", who);
+  if (T == 0 && !plan) return ok();
+  return hip_result(gl::launch_route_fwd(el_code(dtype), T, num_experts, top_k, score == GL_SCORE_SIGMOID,
+                                         renormalize, logits, ids, weights, m_splits, row_index, slot_index,
+                                         workspace, stream),
+                    who);
+}
+
+int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype dtype, int score, int renormalize,
+                      const void *logits, const int32_t *ids, const float *dweights, void *dlogits,
+                      hipStream_t stream) {
+  const char *who = "gl_route_backward";
+  const int64_t T = total_rows;
+  GL_TRY(check_route(who, T, num_experts, top_k, dtype, score, renormalize));
+  GL_TRY(check_buf(logits, T, "logits"));
+  GL_TRY(check_buf(ids, T, "ids"));
+  GL_TRY(check_buf(dweights, T, "dweights"));
+  GL_TRY(check_buf(dlogits, T, "dlogits"));
+  if (T == 0) return ok();
+  return hip_result(gl::launch_route_bwd(el_code(dtype), T, num_experts, top_k, score == GL_SCORE_SIGMOID,
+                                         renormalize, logits, ids, dweights, dlogits, stream),
+                    who);
+}
+
+size_t gl_moe_few_tokens_workspace_size(int64_t total_rows, int top_k, int num_experts, int64_t ffn_features) {
+  if (total_rows < 0 || top_k <= 0 || num_experts <= 0 || ffn_features <= 0) return 0;
+  return gl::moe_workspace_bytes(total_rows, top_k, num_experts, ffn_features);
+}
+
+int gl_moe_few_tokens(int num_experts, int64_t in_features, int64_t ffn_features, int64_t out_features,
+                      int64_t total_rows, int top_k, gl_dtype dtype, gl_dtype w_dtype, const void *x,
+                      const int32_t *ids, const float *weights, const void *w1, const void *const *w1_ptrs,
+                      const uint8_t *w1_scale, const uint8_t *const *w1_scale_ptrs, const void *b1,
+                      const void *const *b1_ptrs, const void *w2, const void *const *w2_ptrs,
+                      const uint8_t *w2_scale, const uint8_t *const *w2_scale_ptrs, const void *b2,
+                      const void *const *b2_ptrs, const void *residual, void *y, int64_t y_rows, void *workspace,
+                      hipStream_t stream) {
+  const char *who = "gl_moe_few_tokens";
+  const int E = num_experts, k = top_k;
+  const int64_t K = in_features, F = ffn_features, N = out_features, T = total_rows;
+  GL_TRY(check_sizes(E, K, N, T));
+  if (F <= 0) return fail(GL_ERR_ARG, "%s: invalid ffn_features (%lld)", who, (long long)F);
+  if (k <= 0) return fail(GL_ERR_ARG, "%s: invalid top_k (%d)", who, k);
+  GL_TRY(check_float_dtype(dtype, who));
+  const bool mx = w_dtype == GL_E4M3;
+  if (mx ? dtype != GL_BF16 : w_dtype != dtype)
+    return fail(GL_ERR_DTYPE, "%s: the weights are of dtype, or GL_E4M3 with GL_BF16", who);
+  if (T > GL_MOE_MAX_TOKENS)
+    return fail(GL_ERR_SHAPE, "%s: at most %d tokens (got %lld)", who, GL_MOE_MAX_TOKENS, (long long)T);
+  if (k > GL_ROUTE_MAX_TOP_K) return fail(GL_ERR_SHAPE, "%s: top_k is at most %d (got %d)", who, GL_ROUTE_MAX_TOP_K, k);
+  const int v = is16(dtype) ? 8 : 4, vc = mx ? 32 : v;
+  if (K % vc || F % vc || N % v)
+    return fail(GL_ERR_SHAPE, "%s: K and F must be multiples of %d and N of %d (got %lld, %lld, %lld)", who, vc, v,
+                (long long)K, (long long)F, (long long)N);
+  if (K > kMaxBf16Dim || F > kMaxBf16Dim || N > kMaxBf16Dim)
+    return fail(GL_ERR_SHAPE, "%s: K, F and N must be at most 2^22", who);
+  if (T * k * F >= ((int64_t)1 << 29)) return fail(GL_ERR_SHAPE, "%s: T * top_k * F must be below 2^29", who);
+  if (y_rows < T) return fail(GL_ERR_SHAPE, "output buffer has %lld rows, needs at least %lld", (long long)y_rows,
+                              (long long)T);
+  GL_TRY(check_one_form(w1, w1_ptrs, "w1", false));
+  GL_TRY(check_one_form(w2, w2_ptrs, "w2", false));
+  GL_TRY(check_one_form(b1, b1_ptrs, "b1", true));
+  GL_TRY(check_one_form(b2, b2_ptrs, "b2", true));
+  if (mx) {
+    GL_TRY(check_scales(w1, w1_ptrs, w1_scale, w1_scale_ptrs, "w1"));
+    GL_TRY(check_scales(w2, w2_ptrs, w2_scale, w2_scale_ptrs, "w2"));
+  } else if (w1_scale || w1_scale_ptrs || w2_scale || w2_scale_ptrs) {
+    return fail(GL_ERR_ARG, "scales are only for GL_E4M3 weights");
+  }
+  if (T == 0) return ok();
+  GL_TRY(check_buf(x, T, "x"));
+  GL_TRY(check_buf(y, T, "y"));
+  GL_TRY(check_buf(workspace, T, "workspace"));
+  if (!aligned16(residual)) return fail(GL_ERR_ARG, "residual not 16-byte aligned");
+  if (!ids || !weights || ((uintptr_t)ids & 3u) || ((uintptr_t)weights & 3u))
+    return fail(GL_ERR_ARG, "ids or weights NULL or not 4-byte aligned");
+  return hip_result(gl::launch_moe(el_code(dtype), mx, E, K, F, N, T, k, x, ids, weights, w1, w1_ptrs, w1_scale,
+                                   w1_scale_ptrs, b1, b1_ptrs, w2, w2_ptrs, w2_scale, w2_scale_ptrs, b2, b2_ptrs,
+                                   residual, y, workspace, stream),
+                    who);
 }
 
 }  // extern "C"

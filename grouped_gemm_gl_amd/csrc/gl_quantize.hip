@@ -11,24 +11,12 @@
 // so a wave streams 4 KiB of contiguous input.  The scale comes from the exponent
 // bits and multiplies exactly (a power of two); the rounding to E4M3 is the
 // hardware pack conversion, bit-identical to the rule over every value it can see.
+#include "gl_mx.hpp"
 #include "gl_offsets.hpp"
 
 namespace gl {
 
 constexpr int kQThreads = 256;
-
-// E4M3 codes of four finite floats (already scaled into the block's range), packed
-// one per byte: round to nearest even, magnitudes above 448 saturate to 448, the sign
-// bit is kept (also for zero).  gfx950's pack conversion to OCP E4M3 rounds to
-// nearest even and keeps the sign; the clamp first makes overflow saturate.  Over
-// every value the quantizers can pass (8 significant bits, exponents -149 .. 9, both
-// signs) it gives the same bytes as the rule spelled out (checked exhaustively on
-// the device).
-__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
-  const auto sat = [](float v) { return __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f); };
-  uint32_t o = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), (int)o, true);
-}
 
 // One block of 32 bf16 values, given as 16 words of two packed values each (element
 // 2i in the low half of w[i]): 32 E4M3 codes packed four per word, and the scale byte.

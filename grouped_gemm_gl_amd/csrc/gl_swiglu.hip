@@ -9,55 +9,11 @@
 // HBM-bound elementwise work: each thread moves 16 bytes of each operand (8 columns
 // of a 16-bit type, 4 of fp32), math in fp32, one rounding per output.  Per row the
 // forward reads 2F and writes F elements; the backward reads 3F and writes 2F.
-#include "gl_common.hpp"
+#include "gl_vec.hpp"
 
 namespace gl {
 
 constexpr int kSwThreads = 256;
-enum { SW_BF16 = 0, SW_F32 = 1, SW_F16 = 2 };
-
-template <int EL>
-struct Vec;  // 16 bytes of elements <-> fp32 values
-
-template <>
-struct Vec<SW_F32> {
-  static constexpr int n = 4;
-  __device__ static void load(const void *p, float *v) {
-    const float4 q = *(const float4 *)p;
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  }
-  __device__ static void store(void *p, const float *v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
-};
-
-template <int EL>
-struct Vec16 {
-  static constexpr int n = 8;
-  static constexpr bool F16 = EL == SW_F16;
-  __device__ static void load(const void *p, float *v) {
-    const uint4 q = *(const uint4 *)p;
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = h16_to_f32<F16>((uint16_t)(w[i] & 0xffffu));
-      v[2 * i + 1] = h16_to_f32<F16>((uint16_t)(w[i] >> 16));
-    }
-  }
-  __device__ static void store(void *p, const float *v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = pack_h16x2<F16>(v[2 * i], v[2 * i + 1]);
-    *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec<SW_BF16> : Vec16<SW_BF16> {};
-template <>
-struct Vec<SW_F16> : Vec16<SW_F16> {};
-
-constexpr int elem_bytes(int el) { return el == SW_F32 ? 4 : 2; }
-
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
 
 template <int EL>
 __global__ __launch_bounds__(kSwThreads) void swiglu_fwd_kernel(const char *__restrict__ h, int64_t F, int64_t n,
@@ -102,30 +58,30 @@ __global__ __launch_bounds__(kSwThreads) void swiglu_bwd_kernel(const char *__re
 
 // el: 0 bf16, 1 fp32, 2 fp16.  F a multiple of 8 (16-bit) or 4 (fp32).
 hipError_t launch_swiglu_fwd(int el, int64_t T, int64_t F, const void *h, void *a, hipStream_t s) {
-  const int64_t n = T * (F / (el == SW_F32 ? 4 : 8));
+  const int64_t n = T * (F / (el == EL_F32 ? 4 : 8));
   if (n == 0) return hipSuccess;
   const dim3 grid((unsigned)((n + kSwThreads - 1) / kSwThreads)), block(kSwThreads);
-  if (el == SW_F32)
-    hipLaunchKernelGGL(swiglu_fwd_kernel<SW_F32>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
-  else if (el == SW_F16)
-    hipLaunchKernelGGL(swiglu_fwd_kernel<SW_F16>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
+  if (el == EL_F32)
+    hipLaunchKernelGGL(swiglu_fwd_kernel<EL_F32>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
+  else if (el == EL_F16)
+    hipLaunchKernelGGL(swiglu_fwd_kernel<EL_F16>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
   else
-    hipLaunchKernelGGL(swiglu_fwd_kernel<SW_BF16>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
+    hipLaunchKernelGGL(swiglu_fwd_kernel<EL_BF16>, grid, block, 0, s, (const char *)h, F, n, (char *)a);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd(int el, int64_t T, int64_t F, const void *h, const void *da, void *dh, hipStream_t s) {
-  const int64_t n = T * (F / (el == SW_F32 ? 4 : 8));
+  const int64_t n = T * (F / (el == EL_F32 ? 4 : 8));
   if (n == 0) return hipSuccess;
   const dim3 grid((unsigned)((n + kSwThreads - 1) / kSwThreads)), block(kSwThreads);
-  if (el == SW_F32)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<SW_F32>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
+  if (el == EL_F32)
+    hipLaunchKernelGGL(swiglu_bwd_kernel<EL_F32>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
                        (char *)dh);
-  else if (el == SW_F16)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<SW_F16>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
+  else if (el == EL_F16)
+    hipLaunchKernelGGL(swiglu_bwd_kernel<EL_F16>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
                        (char *)dh);
   else
-    hipLaunchKernelGGL(swiglu_bwd_kernel<SW_BF16>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
+    hipLaunchKernelGGL(swiglu_bwd_kernel<EL_BF16>, grid, block, 0, s, (const char *)h, (const char *)da, F, n,
                        (char *)dh);
   return hipGetLastError();
 }

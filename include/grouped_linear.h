@@ -477,6 +477,122 @@ int gl_forward_noalloc(int num_groups, int64_t in_features, int64_t out_features
                        const uint8_t *const *w_scale_ptrs, const void *bias, const void *const *bias_ptrs, void *y,
                        int64_t y_rows, hipStream_t stream);
 
+/*
+ * RMS norm with the residual's addition (the norm in front of the layer's experts and
+ * router; its MXFP8 output is the E4M3 operand of gl_forward):
+ *   s = x + residual,  h = s,  y = s * rstd * gamma,
+ *   rstd = (mean over the row of s^2 + eps)^-1/2
+ * computed in fp32; h, y and the codes are each rounded once from the fp32 values (the
+ * codes from y before its rounding to dtype).
+ *   dtype        GL_F32, GL_BF16 or GL_F16 for x, residual, h and y, all [T, C]
+ *   gamma        [C], gamma_dtype GL_F32 or dtype
+ *   residual     or NULL (s = x)
+ *   h            the new residual stream, or NULL
+ *   y            or NULL; h and y may each be x or residual (not both the same buffer)
+ *   data, scale  MXFP8 of y: codes [T, C] and scales [T, C / 32], by the rule of
+ *                gl_group_quantize_mxfp8 (C % 32 == 0; a block with Inf/NaN likewise),
+ *                or both NULL.  At least one of y and data is given.
+ *   eps          finite, >= 0 (a row of zeros with eps 0 gives NaN)
+ * C a multiple of 8 (16-bit) or 4 (fp32), at most 2^22; every tensor 16-byte aligned
+ * except scale.  No other buffers overlap.
+ */
+int gl_rmsnorm_forward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_dtype gamma_dtype, const void *x,
+                       const void *residual, const void *gamma, float eps, void *h, void *y, uint8_t *data,
+                       uint8_t *scale, hipStream_t stream);
+
+/*
+ * Its backward at the stored h (rstd is taken from h again, so no statistics are kept):
+ *   xh = h * rstd,  v = dy * gamma,  dx = dh + rstd * (v - xh * mean(v * xh)),
+ *   dgamma = sum over rows of dy * xh
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h, dx  [T, C] of dtype; dh [T, C], the gradient that arrives at h through the
+ *              residual stream, or NULL; dx may be dy or dh
+ *   dgamma     [C] of dgamma_dtype (GL_F32 or dtype), or NULL; overwritten, or added to
+ *              with accumulate = 1.  T = 0 writes zeros (accumulate: leaves it).
+ *   workspace  gl_rmsnorm_workspace_size(T, C) bytes, 16-byte aligned; may be NULL where
+ *              dgamma is.  fp32 partial sums, added in a fixed order (deterministic).
+ */
+size_t gl_rmsnorm_workspace_size(int64_t total_rows, int64_t features);
+int gl_rmsnorm_backward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_dtype gamma_dtype, const void *dy,
+                        const void *dh, const void *h, const void *gamma, float eps, void *dx,
+                        gl_dtype dgamma_dtype, void *dgamma, int accumulate, void *workspace, hipStream_t stream);
+
+/*
+ * Token routing: each token's top_k experts by logit with their weights, and the plan
+ * that orders the chosen (token, slot) pairs by expert for the grouped calls.
+ *   logits   [T, E] of dtype (GL_F32, GL_BF16 or GL_F16); E <= GL_ROUTE_MAX_EXPERTS
+ *   ids      int32 [T, top_k], largest logit first, ties to the lowest expert;
+ *            top_k <= min(E, GL_ROUTE_MAX_TOP_K)
+ *   weights  float [T, top_k].  score GL_SCORE_SOFTMAX: the softmax over all E logits at
+ *            the chosen experts; GL_SCORE_SIGMOID: the sigmoid of the chosen logits.
+ *            renormalize = 1: divided by their sum over the token's slots.
+ * A logit of -inf masks its expert: it is chosen only when fewer than top_k others are
+ * left, and weighs 0 then, so a token that is masked everywhere has top_k ids of weight
+ * 0.  NaN counts as -inf, +inf as the largest finite value.
+ * The plan, or m_splits, row_index and slot_index all NULL:
+ *   m_splits    int64 [E], slots of each expert: the input of gl_offsets with
+ *               total_rows = T * top_k
+ *   row_index   int32 [T, top_k], the row of a slot when slots are ordered by expert,
+ *               within an expert by slot (the flat index t * top_k + j)
+ *   slot_index  int32 [T * top_k], its inverse: the slot of each row (its token is
+ *               slot / top_k)
+ *   workspace   gl_route_workspace_size(T, E) bytes, 16-byte aligned; NULL without a plan
+ * Results do not depend on timing (no order of atomics shows).
+ */
+#define GL_ROUTE_MAX_EXPERTS 1024
+#define GL_ROUTE_MAX_TOP_K 32
+enum { GL_SCORE_SOFTMAX = 0, GL_SCORE_SIGMOID = 1 };
+size_t gl_route_workspace_size(int64_t total_rows, int num_experts);
+int gl_route_forward(int64_t total_rows, int num_experts, int top_k, gl_dtype dtype, int score, int renormalize,
+                     const void *logits, int32_t *ids, float *weights, int64_t *m_splits, int32_t *row_index,
+                     int32_t *slot_index, void *workspace, hipStream_t stream);
+
+/*
+ * Gradient of the routing weights: dlogits [T, E] of dtype from dweights float
+ * [T, top_k], at the logits and ids of gl_route_forward (the choice itself has no
+ * gradient).  Masked experts and tokens get 0.  An id outside [0, E) takes no part.
+ */
+int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype dtype, int score, int renormalize,
+                      const void *logits, const int32_t *ids, const float *dweights, void *dlogits,
+                      hipStream_t stream);
+
+/*
+ * The expert layer for a few tokens (decoding): for token t with experts
+ * e_j = ids[t, j] and weights w_j
+ *   y_t = residual_t + sum_j w_j (W2_e SwiGLU(W1_e x_t + b1_e) + b2_e)
+ * straight from the routing, without sorting or gathering rows; two launches, each used
+ * expert's weights read once.  Larger batches take the plan of gl_route_forward and
+ * gl_grouped_mlp_forward.
+ *   T        at most GL_MOE_MAX_TOKENS tokens; top_k <= GL_ROUTE_MAX_TOP_K
+ *   dtype    GL_F32, GL_BF16 or GL_F16 for x [T, K], the biases, residual and y
+ *   w_dtype  dtype, or GL_E4M3 with dtype GL_BF16: the weights are MXFP8 codes with
+ *            scales (gl_quantize_mxfp8_weights), expanded exactly; x stays bf16
+ *   ids      int32 [T, top_k]; a slot whose id is outside [0, E) takes no part (an expert
+ *            held by another device), nor does a slot of weight 0
+ *   weights  float [T, top_k]
+ *   w1, w2   [E, 2F, K] and [E, N, F], stacked or as device pointer arrays, scales in
+ *            the same form [E, rows, cols / 32]; b1 [E, 2F], b2 [E, N] or none.  SwiGLU
+ *            as in gl_swiglu_forward: the first F rows of W1 are the gate's
+ *   residual [T, N], or NULL; may be y itself
+ *   y        [y_rows, N], y_rows >= T; rows >= T are never written.  A token without a
+ *            slot gets its residual, or zeros
+ *   workspace  gl_moe_few_tokens_workspace_size bytes, 16-byte aligned
+ * Sums are fp32 in a fixed order (deterministic), the SwiGLU output between the two
+ * products keeps at least 16 significant bits, y is rounded once.  K, F and N multiples of
+ * 8 (16-bit) or 4 (fp32), for MXFP8 K and F multiples of 32; at most 2^22, and
+ * T * top_k * F < 2^29.
+ */
+#define GL_MOE_MAX_TOKENS 64
+size_t gl_moe_few_tokens_workspace_size(int64_t total_rows, int top_k, int num_experts, int64_t ffn_features);
+int gl_moe_few_tokens(int num_experts, int64_t in_features, int64_t ffn_features, int64_t out_features,
+                      int64_t total_rows, int top_k, gl_dtype dtype, gl_dtype w_dtype, const void *x,
+                      const int32_t *ids, const float *weights, const void *w1, const void *const *w1_ptrs,
+                      const uint8_t *w1_scale, const uint8_t *const *w1_scale_ptrs, const void *b1,
+                      const void *const *b1_ptrs, const void *w2, const void *const *w2_ptrs,
+                      const uint8_t *w2_scale, const uint8_t *const *w2_scale_ptrs, const void *b2,
+                      const void *const *b2_ptrs, const void *residual, void *y, int64_t y_rows, void *workspace,
+                      hipStream_t stream);
+
 /* Message of the last error on this thread ("" if none). */
 const char *gl_last_error(void);
 
