@@ -242,3 +242,18 @@ def test_deterministic_other_stream_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert_bits_equal(y, ref, f"replay {i}")
+
+
+def test_broken_weights_stay_with_their_tokens():
+    """NaN and infinite weights of an expert reach the tokens that name it and no others."""
+    for T in (5, 30, 50):
+        c = case(91, T, 6, 2, 64, 40, 56, BF16)
+        c["ids"][:, 0], c["ids"][:, 1] = 1, 2
+        c["ids"][3, 1] = 4
+        ref = run(c)
+        c["w1"][4, 3, 5] = float("nan")
+        c["w2"][4] = float("inf")
+        y = run(c)
+        keep = [t for t in range(T) if t != 3]
+        assert_bits_equal(y[keep], ref[keep], "other tokens")
+        assert not torch.isfinite(y[3]).any()
