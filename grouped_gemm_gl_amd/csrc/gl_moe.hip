@@ -12,10 +12,10 @@
 //   up    workgroup (expert, 16 columns of a): the expert's tokens, compacted, are the
 //         columns; its waves split the contraction over K and add up through LDS.  Leaves
 //         a = w SwiGLU(W1 x + b1), w the token's weight for the expert, in the workspace.
-//   down  workgroup (16 columns of y): runs over all (expert, piece of F) items of the
-//         call with the tokens themselves as columns, a column without the expert being
-//         zeros, so the sum over a token's experts is the MFMA's own accumulation: one
-//         accumulator a token, no atomics, a fixed order.
+//   down  workgroup (16 columns of y): its waves share the (expert, piece of F) items of
+//         the whole call, an item's columns being the expert's tokens again; each wave
+//         adds its products to its own sum of every token in LDS, and the waves' sums are
+//         added at the end: no atomics, a fixed order.
 //
 // For 16-bit weights a is kept as two values of the weights' type, the rounded value and
 // the rest, each multiplied in its own MFMA step: the products see 16 significant bits
@@ -27,11 +27,16 @@
 
 namespace gl {
 
+enum { EL_MX = 3 };  // weights: E4M3 codes with an E8M0 scale per 32 of a row
 constexpr int kMoeMaxTokens = 64;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
+// Units that a wave takes at a time (an MXFP8 unit holds twice the k values).
+template <int WEL>
+constexpr int up_units() { return WEL == EL_MX ? 1 : 2; }
+template <int WEL>
+constexpr int down_units() { return WEL == EL_MX ? 2 : 4; }
 constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64;
 constexpr int kMoeRows = 16;  // weight rows of a workgroup (per half of W1)
-enum { EL_MX = 3 };           // weights: E4M3 codes with an E8M0 scale per 32 of a row
 
 struct MoeWeight {
   const char *w;
@@ -46,9 +51,9 @@ struct MoeWeight {
 // An expert with its tokens, written by the up kernel: at most one per slot, and one per
 // expert.
 struct MoeEntry {
-  int32_t expert;  // -1: none
-  int32_t pad;
   uint64_t tokens;  // bit t: token t has a slot of it
+  int32_t expert;   // -1: none
+  int32_t first;    // slot_of its first token
 };
 
 struct MoeParams {
@@ -83,10 +88,6 @@ __device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
   return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
-__device__ __forceinline__ float e8m0(uint32_t s) {
-  return __uint_as_float(s == 0xff ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
-}
-
 // A unit is 128 bytes of each of the 16 weight rows: lane l holds bytes 16 (l / 16) and
 // 64 + 16 (l / 16) of row l % 16, two loads that together take whole lines.  Its k values
 // are taken in the order that this gives, the same for both operands, in `steps` pieces:
@@ -100,7 +101,7 @@ struct Unit {  // bf16, fp16 and fp32 weights
   __device__ static uint32_t b_byte(int i, int q) { return i * 64 + q * 16; }
   // row: byte offset of the lane's row, at: byte within it, end: bytes of a row
   __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t, uint32_t row, uint32_t at, uint32_t end,
-                       uint32_t, int q) {
+                       uint32_t, bool, int q) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t b = at + i * 64 + q * 16;
@@ -116,20 +117,35 @@ struct Unit<EL_MX> {
   static constexpr int steps = 4;
   static constexpr int b_bytes = 256;
   i32x4_t r[2];
-  uint8_t s[2];
+  uint32_t s;  // the 4 scales of the unit's codes in the lane's row
+  int q;
   __device__ static uint32_t b_byte(int i, int q) { return (i >> 1) * 128 + q * 32 + (i & 1) * 16; }
   __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, uint32_t row, uint32_t at, uint32_t end,
-                       uint32_t srow, int q) {
+                       uint32_t srow, bool wide, int q_) {
+    q = q_;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t b = at + i * 64 + q * 16;
       r[i] = load16(w, b < end ? row + b : kNowhere);
-      s[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sc, (int)(b < end ? srow + b / 32 : kNowhere), 0, 0);
+    }
+    // whole units (wide): their 4 scales are an aligned word
+    if (wide) {
+      s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sc, (int)(at < end ? srow + at / 32 : kNowhere), 0, 0);
+      return;
+    }
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t b = at + i * 64 + q * 16;
+      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b8(sc, (int)(b < end ? srow + b / 32 : kNowhere), 0, 0);
+      s |= (v & 0xff) << (16 * i + 8 * (q >> 1));
     }
   }
-  // 8 codes as bf16: their values are exact there
+  // 8 codes as bf16: their values are exact there.  The conversion takes the exponent
+  // field of an fp32 scale, which is the E8M0 byte (255, NaN, included).
   __device__ i32x4_t operand(int i) const {
-    const float f = e8m0(s[i >> 1]);
+    const uint32_t byte = (s >> (16 * (i >> 1) + 8 * (q >> 1))) & 0xff;
+    const float f = __uint_as_float(byte << 23);
     i32x4_t o;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -191,20 +207,49 @@ struct UpTokens {
   float gate[kMoeMaxTokens];  // the token's weight for it (all its slots that name it)
 };
 
-// Contraction over K for NT tiles of 16 columns and the gate's and up's rows.
-template <int EL, int WEL, int NT, int U>
-__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
+// The weight side of the up kernel: units wave, wave + kUpWaves, ... of the gate's and the
+// up's 16 rows, U of each at a time.
+template <int WEL>
+struct UpWeights {
+  static constexpr int U = up_units<WEL>();
   using W = Unit<WEL>;
+  __amdgpu_buffer_rsrc_t wg, wu, sg, su;
+  uint32_t row, srow, end;
+  int q;
+  bool wide;
+  __device__ UpWeights(const MoeParams &p, int e, int64_t f0) {
+    const int col = threadIdx.x & 15;
+    const uint32_t wb = (uint32_t)row_bytes<WEL>(p.K);
+    wg = moe_rsrc(weight_row<WEL>(p.w1, e, f0));
+    wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f0));
+    sg = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, f0) : nullptr);
+    su = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, p.F + f0) : nullptr);
+    q = (threadIdx.x >> 4) & 3;
+    row = col * wb;
+    wide = p.K % 128 == 0;
+    srow = col * (uint32_t)(p.K / 32);
+    end = f0 + col < p.F ? wb : 0;  // past the last row: no byte is valid
+  }
+  // units past the end load zeros
+  __device__ void load(W *g, W *u, int c0) const {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t at = (uint32_t)(c0 + i * kUpWaves) * 128;
+      g[i].load(wg, sg, row, at, end, srow, wide, q);
+      u[i].load(wu, su, row, at, end, srow, wide, q);
+    }
+  }
+};
+
+// Contraction over K for up to NT tiles of 16 columns; g and u hold the first units.
+template <int EL, int WEL, int NT>
+__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, const UpWeights<WEL> &weights,
+                                           Unit<WEL> *g, Unit<WEL> *u, float *sums) {
+  using W = Unit<WEL>;
+  constexpr int U = up_units<WEL>();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const uint32_t wb = (uint32_t)row_bytes<WEL>(p.K), xb = (uint32_t)(p.K * elem_bytes(EL));
-  const int e = tok.expert;
-  const auto wg = moe_rsrc(weight_row<WEL>(p.w1, e, f0)), wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f0));
-  const auto sg = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, f0) : nullptr);
-  const auto su = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, p.F + f0) : nullptr);
+  const uint32_t xb = (uint32_t)(p.K * elem_bytes(EL));
   const auto xr = moe_rsrc(p.x);
-  const bool row_ok = f0 + col < p.F;
-  const uint32_t end = row_ok ? wb : 0;  // past the last row: no byte is valid
-  const uint32_t row = col * wb, srow = col * (uint32_t)(p.K / 32);
   uint32_t xrow[NT], xend[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -212,43 +257,46 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
     xend[t] = c < tok.n ? xb : 0;
     xrow[t] = c < tok.n ? (uint32_t)(tok.slot[c] / p.k) * xb : 0;
   }
-  f32x4_t g[NT], u[NT];
+  f32x4_t ag[NT], au[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) g[t] = u[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NT; ++t) ag[t] = au[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   const int units = (int)((p.K + W::kElems - 1) / W::kElems);
   for (int c0 = wave; c0 < units; c0 += kUpWaves * U) {
-    W ug[U], uu[U];
-    i32x4_t b[U][NT][W::steps];
+    W ng[U], nu[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t c = c0 + i * kUpWaves;  // units past the end load zeros
-      ug[i].load(wg, sg, row, c * 128, end, srow, q);
-      uu[i].load(wu, su, row, c * 128, end, srow, q);
+    for (int t = 0; t < NT; ++t) {
+      if (t && t * 16 >= tok.n) break;
+      // the tokens' pieces come from cache, the next weights from memory: issued in this
+      // order, the products wait for the former alone
+      i32x4_t b[U][W::steps];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int s = 0; s < W::steps; ++s) {
-          const uint32_t at = c * W::b_bytes + W::b_byte(s, q);
-          b[i][t][s] = load16(xr, at < xend[t] ? xrow[t] + at : kNowhere);
+          const uint32_t at = (uint32_t)(c0 + i * kUpWaves) * W::b_bytes + W::b_byte(s, q);
+          b[i][s] = load16(xr, at < xend[t] ? xrow[t] + at : kNowhere);
+        }
+      if (t == 0) weights.load(ng, nu, c0 + kUpWaves * U);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int s = 0; s < W::steps; ++s) {
+          ag[t] = mma<EL>(g[i].operand(s), b[i][s], ag[t]);
+          au[t] = mma<EL>(u[i].operand(s), b[i][s], au[t]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int s = 0; s < W::steps; ++s) {
-        const i32x4_t ag = ug[i].operand(s), au = uu[i].operand(s);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          g[t] = mma<EL>(ag, b[i][t][s], g[t]);
-          u[t] = mma<EL>(au, b[i][t][s], u[t]);
-        }
-      }
+    for (int i = 0; i < U; ++i) {
+      g[i] = ng[i];
+      u[i] = nu[i];
+    }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float *o = sums + (((t * kUpWaves + wave) * 2) * 64 + lane) * 4;
-    *(f32x4_t *)o = g[t];
-    *(f32x4_t *)(o + 256) = u[t];
+    *(f32x4_t *)o = ag[t];
+    *(f32x4_t *)(o + 256) = au[t];
   }
 }
 
@@ -260,26 +308,40 @@ __device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
   lo = fabsf(rest) < INFINITY ? f32_to_h16<F16>(rest) : (uint16_t)0;  // hi is not finite
 }
 
-template <int EL, int WEL>
+template <int EL, int WEL, int NT>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
   __shared__ UpTokens tok;
-  __shared__ __align__(16) float sums[4 * kUpWaves * 2 * 64 * 4];
+  __shared__ __align__(16) float sums[NT * kUpWaves * 2 * 64 * 4];
   const int lane = threadIdx.x & 63;
   const int64_t f0 = (int64_t)blockIdx.x * kMoeRows;
+  const bool by_expert = p.E <= p.T * p.k;
+  const int e = by_expert ? (int)blockIdx.y : p.ids[blockIdx.y];
+  const bool valid = e >= 0 && e < p.E;
+  const UpWeights<WEL> weights(p, valid ? e : 0, f0);
+  Unit<WEL> g[up_units<WEL>()], u[up_units<WEL>()];
+  // a slot's expert is almost always read: its first weights are on their way during the
+  // search for its tokens
+  if (valid && !by_expert) weights.load(g, u, threadIdx.x >> 6);
   if (threadIdx.x < 64) {
     // lane t: the slots of token t that name the workgroup's expert
-    const int e = p.E <= p.T * p.k ? (int)blockIdx.y : p.ids[blockIdx.y];
     int first = -1;
     float gate = 0.f;
-    if (lane < p.T && e >= 0 && e < p.E)
-#pragma unroll 4
-      for (int j = 0; j < p.k; ++j) {
-        const int s = lane * p.k + j;
-        const float w = p.gates[s];
-        if (p.ids[s] == e && w != 0.f) {
-          if (first < 0) first = s;
-          gate += w;
+    if (lane < p.T && valid)
+      for (int j0 = 0; j0 < p.k; j0 += 8) {
+        int id[8];
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = lane * p.k + (j0 + i < p.k ? j0 + i : j0);
+          id[i] = p.ids[s];
+          w[i] = p.gates[s];
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j0 + i < p.k && id[i] == e && w[i] != 0.f) {
+            if (first < 0) first = lane * p.k + j0 + i;
+            gate += w[i];
+          }
       }
     const uint64_t mask = __ballot(first >= 0);
     const int rank = __popcll(mask & ((1ull << lane) - 1));
@@ -289,23 +351,22 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
     }
     // one workgroup of several for the same expert goes on: the one of its first slot
     const int lead = mask ? __shfl(first, __ffsll((unsigned long long)mask) - 1) : -1;
-    const bool mine = mask && (p.E <= p.T * p.k || lead == (int)blockIdx.y);
+    const bool mine = mask && (by_expert || lead == (int)blockIdx.y);
     if (lane == 0) {
       tok.expert = mine ? e : -1;
       tok.n = __popcll(mask);
     }
     if (blockIdx.x == 0) {
-      if (lane == 0) p.entries[blockIdx.y] = {mine ? e : -1, 0, mask};
+      if (lane == 0) p.entries[blockIdx.y] = {mask, mine ? e : -1, lead};
       p.slot_of[blockIdx.y * 64 + lane] = (int16_t)first;
     }
   }
   __syncthreads();
   if (tok.expert < 0) return;
-  if (tok.n <= 16) up_product<EL, WEL, 1, WEL == EL_MX ? 2 : 4>(p, tok, f0, sums);
-  else if (tok.n <= 32) up_product<EL, WEL, 2, WEL == EL_MX ? 1 : 2>(p, tok, f0, sums);
-  else up_product<EL, WEL, 4, 1>(p, tok, f0, sums);
+  if (by_expert) weights.load(g, u, threadIdx.x >> 6);
+  up_product<EL, WEL, NT>(p, tok, weights, g, u, sums);
   __syncthreads();
-  const int e = tok.expert, f = threadIdx.x & 15;
+  const int f = threadIdx.x & 15;
   if (f0 + f >= p.F) return;
   const float bg = bias_at<EL>(p.w1, e, f0 + f), bu = bias_at<EL>(p.w1, e, p.F + f0 + f);
   for (int c = threadIdx.x >> 4; c < tok.n; c += 16) {
@@ -332,26 +393,27 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
 
 // LDS of the down kernel: the entries with an expert, in order.
 struct DownEntry {
-  uint64_t tokens;
   int32_t expert;
-  int32_t base;  // its tokens' slots are slots[base ...]
+  int32_t base, n;  // its tokens' slots are slots[base ... base + n)
 };
 
-template <int EL, int WEL, int NT, int U>
+template <int EL, int WEL, int R>
 __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams p) {
   using W = Unit<WEL>;
+  constexpr int U = down_units<WEL>();
   extern __shared__ __align__(16) char lds[];
   __shared__ int wave_n[kDownWaves], wave_m[kDownWaves];
-  float *sums = (float *)lds;  // at the end, over the table
-  DownEntry *ent = (DownEntry *)lds;
+  float *acc = (float *)lds;  // [waves][T][16 rows] sums of a token
+  DownEntry *ent = (DownEntry *)(acc + kDownWaves * p.T * 16);
   int16_t *slots = (int16_t *)(ent + p.n_entries);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * kMoeRows;
+  const int64_t n0 = (int64_t)blockIdx.x * R;
+  for (int i = threadIdx.x; i < kDownWaves * p.T * 4; i += kDownThreads) ((f32x4_t *)acc)[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   // compact the table: running counts of entries and of their tokens
   int n = 0, members = 0;
   for (int d0 = 0; d0 < p.n_entries; d0 += kDownThreads) {
     const int d = d0 + threadIdx.x;
-    MoeEntry t{-1, 0, 0};
+    MoeEntry t{0, -1, 0};
     if (d < p.n_entries) t = p.entries[d];
     const bool on = t.expert >= 0;
     const int mine = on ? __popcll(t.tokens) : 0;
@@ -377,22 +439,23 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
       members += wave_m[w];
     }
     if (on) {
-      ent[at] = {t.tokens, t.expert, base};
-      uint64_t left = t.tokens;
-      for (int i = base; left; ++i, left &= left - 1)
+      ent[at] = {t.expert, base, mine};
+      slots[base] = (int16_t)t.first;
+      uint64_t left = t.tokens & (t.tokens - 1);
+      for (int i = base + 1; left; ++i, left &= left - 1)
         slots[i] = p.slot_of[d * 64 + __ffsll((unsigned long long)left) - 1];
     }
     __syncthreads();
   }
 
   const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = (uint32_t)(p.F * elem_bytes(EL));
-  const uint32_t end = n0 + col < p.N ? wb : 0;
+  const uint32_t end = col < R && n0 + col < p.N ? wb : 0;
   const uint32_t row = col * wb, srow = col * (uint32_t)(p.F / 32);
+  const bool wide = p.F % 128 == 0;
   const auto ar = moe_rsrc(p.a);
-  const auto lr = moe_rsrc(p.a + (int64_t)p.T * p.k * ab);
-  f32x4_t acc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  constexpr int kCols = EL == EL_F32 ? 16 : 8;  // tokens of a step
+  const int token = col & (kCols - 1);
+  const uint32_t part = col < kCols ? 0 : (uint32_t)(p.T * p.k) * ab;  // the second parts' plane
   // items (entry, U units of F), dealt to the waves in turn
   const int pieces = (int)((p.F + W::kElems * U - 1) / (W::kElems * U));
   int i = wave / pieces, c = wave - i * pieces;
@@ -402,7 +465,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
     const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, n0));
     const auto s = moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, n0) : nullptr);
 #pragma unroll
-    for (int j = 0; j < U; ++j) w[j].load(r, s, row, (c * U + j) * 128, end, srow, q);
+    for (int j = 0; j < U; ++j) w[j].load(r, s, row, (c * U + j) * 128, end, srow, wide, q);
   };
   if (i < n) load(cur, i, c);
   while (i < n) {
@@ -411,58 +474,43 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
       nc -= pieces;
       ++ni;
     }
-    i32x4_t hi[NT][U * W::steps], lo[NT][U * W::steps];
-    const uint64_t tokens = ent[i].tokens;
-    const int base = ent[i].base;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int token = t * 16 + col;
-      const bool on = (tokens >> token) & 1;
-      const uint32_t arow =
-          on ? (uint32_t)slots[base + __popcll(tokens & ((1ull << token) - 1))] * ab : 0;
-      const uint32_t aend = on ? ab : 0;
+    const int base = __builtin_amdgcn_readfirstlane(ent[i].base), m = __builtin_amdgcn_readfirstlane(ent[i].n);
+    // the entry's tokens as columns; a 16-bit a's two parts are columns of the same step
+    for (int t = 0; t < m; t += kCols) {
+      const bool on = t + token < m;
+      const int slot = on ? slots[base + t + token] : 0;
+      const uint32_t arow = (uint32_t)slot * ab + part, aend = on ? ab : 0;
+      i32x4_t b[U * W::steps];
 #pragma unroll
       for (int s = 0; s < U * W::steps; ++s) {
         const uint32_t at = (c * U + s / W::steps) * W::b_bytes + W::b_byte(s % W::steps, q);
-        const uint32_t off = at < aend ? arow + at : kNowhere;
-        hi[t][s] = load16(ar, off);
-        if constexpr (EL != EL_F32) lo[t][s] = load16(lr, off);
+        b[s] = load16(ar, at < aend ? arow + at : kNowhere);
+      }
+      if (t == 0 && ni < n) load(nxt, ni, nc);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4_t sum = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < U * W::steps; ++s) sum = mma<EL>(cur[s / W::steps].operand(s % W::steps), b[s], sum);
+      if constexpr (kCols == 8)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] += __shfl_xor(sum[r], 8);
+      if (on && col == token) {  // each column another token: no lane shares a sum
+        f32x4_t *o = (f32x4_t *)(acc + (wave * p.T + slot / p.k) * 16 + q * 4);
+        *o += sum;
       }
     }
-    if (ni < n) load(nxt, ni, nc);
-    f32x4_t sum[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sum[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < U * W::steps; ++s) {
-      const i32x4_t a = cur[s / W::steps].operand(s % W::steps);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        sum[t] = mma<EL>(a, hi[t][s], sum[t]);
-        if constexpr (EL != EL_F32) sum[t] = mma<EL>(a, lo[t][s], sum[t]);
-      }
-    }
-    // only tokens that name the expert: an infinite weight times the zeros of another
-    // token's column is NaN
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if ((tokens >> (t * 16 + col)) & 1) acc[t] += sum[t];
 #pragma unroll
     for (int j = 0; j < U; ++j) cur[j] = nxt[j];
     i = ni;
     c = nc;
   }
-  __syncthreads();  // every wave is done with the table
-#pragma unroll
-  for (int t = 0; t < NT; ++t) *(f32x4_t *)(sums + ((t * kDownWaves + wave) * 64 + lane) * 4) = acc[t];
   __syncthreads();
-  const int r = threadIdx.x & 15;
-  if (n0 + r >= p.N) return;
-  for (int t = threadIdx.x >> 4; t < p.T; t += kDownThreads / 16) {
-    const float *s = sums + ((t >> 4) * kDownWaves * 64 + ((r >> 2) * 16 + (t & 15))) * 4 + (r & 3);
+  for (int o = threadIdx.x; o < p.T * 16; o += kDownThreads) {
+    const int r = o & 15, t = o >> 4;
+    if (r >= R || n0 + r >= p.N) continue;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) y += s[w * 256];
+    for (int w = 0; w < kDownWaves; ++w) y += acc[w * p.T * 16 + o];
     if (p.w2.bias || p.w2.bias_ptrs)
       for (int j = 0; j < p.k; ++j) {
         const int e = p.ids[t * p.k + j];
@@ -482,20 +530,18 @@ size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t F) {
 
 template <int EL, int WEL>
 static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((moe_up_kernel<EL, WEL>), dim3((unsigned)((p.F + kMoeRows - 1) / kMoeRows), p.n_entries),
-                     dim3(kUpThreads), 0, s, p);
-  const dim3 grid((unsigned)((p.N + kMoeRows - 1) / kMoeRows)), block(kDownThreads);
-  const size_t table = (size_t)p.n_entries * sizeof(DownEntry) + (size_t)p.T * p.k * 2;  // at most 36 KiB
-  const auto lds = [&](int tiles) {
-    const size_t sums = (size_t)tiles * kDownWaves * 64 * 16;
-    return table > sums ? (table + 15) & ~(size_t)15 : sums;
-  };
+  const dim3 up((unsigned)((p.F + kMoeRows - 1) / kMoeRows), p.n_entries);
   if (p.T <= 16)
-    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 1, WEL == EL_MX ? 1 : 2>), grid, block, lds(1), s, p);
-  else if (p.T <= 32)
-    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 2, 1>), grid, block, lds(2), s, p);
+    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, 1>), up, dim3(kUpThreads), 0, s, p);
   else
-    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 4, 1>), grid, block, lds(4), s, p);
+    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, 4>), up, dim3(kUpThreads), 0, s, p);
+  // LDS: at most 4 KiB of sums a wave, 24 KiB of entries and 4 KiB of slots
+  const size_t lds = (size_t)kDownWaves * p.T * 64 + (size_t)p.n_entries * sizeof(DownEntry) + (size_t)p.T * p.k * 2;
+  if (p.N / 16 < 256)
+    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 8>), dim3((unsigned)((p.N + 7) / 8)), dim3(kDownThreads), lds, s, p);
+  else
+    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 16>), dim3((unsigned)((p.N + 15) / 16)), dim3(kDownThreads), lds, s,
+                       p);
 }
 
 hipError_t launch_moe(int el, bool mx, int E, int64_t K, int64_t F, int64_t N, int64_t T, int k, const void *x,

@@ -566,7 +566,8 @@ int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype d
  *   T        at most GL_MOE_MAX_TOKENS tokens; top_k <= GL_ROUTE_MAX_TOP_K
  *   dtype    GL_F32, GL_BF16 or GL_F16 for x [T, K], the biases, residual and y
  *   w_dtype  dtype, or GL_E4M3 with dtype GL_BF16: the weights are MXFP8 codes with
- *            scales (gl_quantize_mxfp8_weights), expanded exactly; x stays bf16
+ *            scales (gl_quantize_mxfp8_weights), expanded to bf16, which is exact but for
+ *            weights below 2^-126 (bf16's subnormals, or 0); x stays bf16
  *   ids      int32 [T, top_k]; a slot whose id is outside [0, E) takes no part (an expert
  *            held by another device), nor does a slot of weight 0
  *   weights  float [T, top_k]

@@ -129,6 +129,39 @@ def test_mxfp8_scales_at_the_ends_of_their_range():
     assert torch.isnan(y[1, 3]) and not torch.isnan(y[1, :3]).any() and not torch.isnan(y[1, 4:]).any()
 
 
+@pytest.mark.parametrize("F", [32, 128])
+def test_mxfp8_weights_expand_exactly(F):
+    """Every code under scales over their range, read off one at a time: token t has a = 2^m
+    in column t of a and zeros elsewhere (g = 64 makes silu(g) = g), so y is code * scale *
+    2^m, exact in bf16; a weight below 2^-126, bf16's smallest normal value, may lose bits
+    there or count as 0: it is within its own size; one of 2^128 or more is infinite (times
+    the zeros of the one-hot row NaN), as in fp32."""
+    T, K = 32, 32
+    scales = torch.tensor([0, 1, 2, 60, 126, 127, 128, 200, 253, 254], dtype=torch.uint8)
+    w1 = torch.zeros(10, 2 * F, K, dtype=BF16)
+    x = torch.eye(T, K).to(BF16)
+    for e, s in enumerate(scales.tolist()):
+        m = max(-100, min(100, 127 - s))
+        for t in range(T):
+            w1[e, t, t] = 64.0
+            w1[e, F + t, t] = 2.0 ** (m - 6)
+    q = [oracle.quantize_mxfp8(to64(w1[e])) for e in range(10)]
+    w2 = torch.arange(256, dtype=torch.uint8).view(1, 256, 1).expand(10, 256, F).contiguous()
+    c = dict(x=x, w1=torch.from_numpy(np.stack([d for d, _ in q])), w1_scale=torch.from_numpy(np.stack([d for _, d in q])),
+             w2=w2, w2_scale=scales.view(10, 1, 1).expand(10, 256, F // 32).contiguous(), b1=None, b2=None, residual=None,
+             weights=torch.ones(T, 1))
+    for e, s in enumerate(scales.tolist()):
+        c["ids"] = torch.full((T, 1), e, dtype=torch.int32)
+        y = to64(run(c))
+        m = max(-100, min(100, 127 - s))
+        ref = oracle.e4m3_decode(np.arange(256, dtype=np.uint8)) * 2.0 ** (s - 127 + m)
+        small = np.abs(ref) < 2.0 ** (m - 126)
+        ref = np.where(small[None] & (np.abs(y - ref) <= np.abs(ref)), y, ref)
+        large = np.broadcast_to(np.abs(ref) >= 2.0 ** (m + 128), y.shape)
+        assert not np.isfinite(y[large]).any()
+        assert np.array_equal(y[~large], ref[~large], equal_nan=True), s
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_per_expert_lists_match_stacked(mx):
     c = case(11, 9, 5, 2, 96, 64, 72, BF16, mx=mx, bias=True, residual=True)
