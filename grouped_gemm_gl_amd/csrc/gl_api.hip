@@ -69,7 +69,7 @@ hipError_t launch_rmsnorm_fwd(int el, bool g32, int64_t T, int64_t C, const void
 hipError_t launch_rmsnorm_bwd(int el, bool g32, int64_t T, int64_t C, const void *dy, const void *dh, const void *h,
                               const void *gamma, float eps, void *dx, int el_dgamma, void *dgamma, int accumulate,
                               float *part, hipStream_t s);
-int rmsnorm_bwd_blocks(int64_t T);
+int rmsnorm_bwd_blocks(int64_t T, int64_t C);
 size_t route_plan_bytes(int64_t T, int E);
 hipError_t launch_route_fwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits, int32_t *ids,
                             float *weights, int64_t *m_splits, int32_t *row_index, int32_t *slot_index, void *ws,
@@ -754,7 +754,7 @@ int gl_rmsnorm_forward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_
 
 size_t gl_rmsnorm_workspace_size(int64_t total_rows, int64_t features) {
   if (total_rows < 0 || features <= 0) return 0;
-  const size_t bytes = (size_t)gl::rmsnorm_bwd_blocks(total_rows) * (size_t)features * 4;
+  const size_t bytes = (size_t)gl::rmsnorm_bwd_blocks(total_rows, features) * (size_t)features * 4;
   return bytes > 16 ? (bytes + 15) & ~(size_t)15 : 16;
 }
 
