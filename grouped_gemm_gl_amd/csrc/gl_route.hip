@@ -7,23 +7,25 @@
 // all experts, or the sigmoid of each logit; renormalised, a token's weights are its
 // chosen scores divided by their sum (for softmax: a softmax over the chosen logits).
 // A token whose experts are all masked gets weights 0.
+#include <type_traits>
+
 #include "gl_vec.hpp"
 
 namespace gl {
 
-constexpr int kRouteThreads = 256, kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteMaxExperts = 1024;
-constexpr int kPlanTokens = 64;  // tokens of a plan block: one bit each of a 64-bit mask
+constexpr int kChunk = 64;  // tokens of a workgroup: one bit each of a 64-bit mask
+constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
+
+__device__ __forceinline__ float as_logit(float v) {
+  // NaN counts as masked; +inf as the largest finite value, so that sums stay finite
+  return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
+}
 
 template <int EL>
 __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
-  float v;
-  if constexpr (EL == EL_F32)
-    v = ((const float *)p)[i];
-  else
-    v = h16_to_f32<EL == EL_F16>(((const uint16_t *)p)[i]);
-  // NaN counts as masked; +inf as the largest finite value, so that sums stay finite
-  return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
+  if constexpr (EL == EL_F32) return as_logit(((const float *)p)[i]);
+  else return as_logit(h16_to_f32<EL == EL_F16>(((const uint16_t *)p)[i]));
 }
 
 // Unsigned order of floats without NaN, -0 equal to +0; every value maps above 0.
@@ -32,271 +34,419 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One wave a token: lane l holds experts l, l + 64, ....
-template <int EL>
-__global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const void *__restrict__ logits, int64_t T, int E,
-                                                                    int k, int sigm, int renorm,
-                                                                    int32_t *__restrict__ ids,
-                                                                    float *__restrict__ weights) {
-  constexpr int kPer = kRouteMaxExperts / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
-  float l[kPer];
-  uint32_t key[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 64 + lane;
-    l[i] = e < E ? load_logit<EL>(logits, t * E + e) : -INFINITY;
-    key[i] = e < E ? order_key(l[i]) : 0;
+// A token's row is held by LPR lanes, PER consecutive experts each: 16 lanes (four tokens a
+// wave, reductions by four rotations within 16 lanes) up to 256 experts, else the wave.
+template <int LPR_, int PER_>
+struct RowLanes {
+  static constexpr int LPR = LPR_, PER = PER_, rows = 64 / LPR_;  // rows of a wave
+};
+
+template <int ror>
+__device__ __forceinline__ uint32_t rotate16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ror, 0xf, 0xf, true);
+}
+
+// f over the LPR lanes of the row, in every lane of it
+template <int LPR, class F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
+  v = f(v, rotate16<8>(v));
+  v = f(v, rotate16<4>(v));
+  v = f(v, rotate16<2>(v));
+  v = f(v, rotate16<1>(v));
+  if constexpr (LPR == 64) {
+    v = f(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = f(v, (uint32_t)__shfl_xor((int)v, 32));
   }
-  int my_id = 0;
-  float my_l = -INFINITY;  // lane j keeps the j-th choice
-  for (int j = 0; j < k; ++j) {
-    uint64_t best = 0;
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  return __uint_as_float(row_reduce<LPR>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+// The lane's PER logits of row t from expert e0 on, -inf past the experts.  whole: rows
+// start on a multiple of the loads' 16 (or, 4 values of 16 bits, 8) bytes.
+template <int EL, int PER>
+__device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, int e0, bool whole, float *l) {
+  constexpr int V = EL == EL_F32 ? 4 : PER < 8 ? 4 : 8;  // values of a load
+  if (whole) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint64_t c = ((uint64_t)key[i] << 32) | (uint32_t)~(i * 64 + lane);
-      best = c > best ? c : best;
-    }
+    for (int i = 0; i < PER; i += V) {
+      if (e0 + i >= E) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d);
-      best = o > best ? o : best;
-    }
-    const int e = (int)~(uint32_t)best;
+        for (int j = 0; j < V; ++j) l[i + j] = -INFINITY;
+        continue;
+      }
+      if constexpr (EL == EL_F32) {
+        const float4 q = *(const float4 *)((const float *)logits + t * E + e0 + i);
+        l[i] = as_logit(q.x); l[i + 1] = as_logit(q.y); l[i + 2] = as_logit(q.z); l[i + 3] = as_logit(q.w);
+      } else {
+        uint32_t w[V / 2];
+        const uint16_t *at = (const uint16_t *)logits + t * E + e0 + i;
+        if constexpr (V == 8) __builtin_memcpy(w, __builtin_assume_aligned(at, 16), 16);
+        else __builtin_memcpy(w, __builtin_assume_aligned(at, 8), 8);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (e == i * 64 + lane) key[i] = 0;  // taken
-    if (lane == j) {
-      const uint32_t b = (uint32_t)(best >> 32);
-      my_id = e;
-      my_l = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+        for (int j = 0; j < V; ++j)
+          l[i + j] = as_logit(h16_to_f32<EL == EL_F16>((uint16_t)(w[j / 2] >> (16 * (j & 1)))));
+      }
     }
-  }
-  float w;
-  if (sigm) {
-    w = 1.f / (1.f + expf(-my_l));
   } else {
-    const float top = __shfl(my_l, 0);
-    w = top == -INFINITY ? 0.f : expf(my_l - top);
-    if (!renorm) {
-      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += top == -INFINITY ? 0.f : expf(l[i] - top);
-#pragma unroll
-      for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-      w = sum > 0.f ? w / sum : 0.f;
-    }
-  }
-  if (renorm) {
-    float sum = lane < k ? w : 0.f;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    w = sum > 0.f ? w / sum : 0.f;
-  }
-  if (lane < k) {
-    ids[t * k + lane] = my_id;
-    weights[t * k + lane] = w;
+    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? load_logit<EL>(logits, t * E + e0 + i) : -INFINITY;
   }
 }
 
-// Plan.  A token names an expert at most once, so within a block of 64 tokens the
-// tokens of an expert are one 64-bit mask, and a slot's rank among them is the number
-// of bits below its token's.
-__global__ __launch_bounds__(kRouteThreads) void route_masks_kernel(const int32_t *__restrict__ ids, int64_t T, int E,
-                                                                    int k, unsigned long long *__restrict__ masks) {
-  __shared__ unsigned long long m[kRouteMaxExperts];
-  const int64_t t0 = (int64_t)blockIdx.x * kPlanTokens;
-  const int n = (int)min64(kPlanTokens, T - t0) * k;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) m[e] = 0;
+// Inclusive sums over the wave's lanes, and over a workgroup of kRouteThreads.
+__device__ __forceinline__ int wave_scan(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if ((int)(threadIdx.x & 63) >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ int block_scan(int v) {
+  __shared__ int waves[kRouteWaves];
+  v = wave_scan(v);
+  if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int s = threadIdx.x; s < n; s += kRouteThreads) atomicOr(&m[ids[t0 * k + s]], 1ull << (s / k));
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) masks[(int64_t)blockIdx.x * E + e] = m[e];
+  for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) v += waves[w];
+  return v;
 }
 
-// One workgroup: thread e runs over the blocks of expert e, then the experts' totals
-// are scanned.
-__global__ __launch_bounds__(kRouteMaxExperts) void route_scan_kernel(const unsigned long long *__restrict__ masks,
-                                                                      int64_t blocks, int E,
-                                                                      int32_t *__restrict__ base,
-                                                                      int32_t *__restrict__ start,
-                                                                      int64_t *__restrict__ m_splits) {
-  __shared__ int32_t tot[kRouteMaxExperts];
-  const int e = threadIdx.x;
-  int32_t sum = 0;
-  if (e < E)
-    for (int64_t b = 0; b < blocks; ++b) {
-      base[b * E + e] = sum;
-      sum += __popcll(masks[b * E + e]);
-    }
-  tot[e] = e < E ? sum : 0;
-  __syncthreads();
-  for (int d = 1; d < kRouteMaxExperts; d <<= 1) {
-    const int32_t v = e >= d ? tot[e - d] : 0;
-    __syncthreads();
-    tot[e] += v;
+struct RouteForward {
+  const void *logits;
+  int32_t *ids;
+  float *weights;
+  unsigned long long *masks;  // [chunks][E] tokens of the chunk that chose the expert, or null
+  int64_t *m_splits;
+  int32_t *row_index, *slot_index;
+  int64_t T;
+  int E, k, sigm, renorm, whole;
+};
+
+// Gates of a chunk of 64 tokens, and the chunk's part of the plan.  A token names an
+// expert at most once, so the chunk's tokens of an expert are one 64-bit mask, and a
+// slot's rank among them is the number of bits below its token's.  A call of one chunk
+// makes its whole plan here.
+//
+// Bound by instructions and, for few tokens, latency.  k rounds, each the row's largest
+// key and then the lowest expert that has it; the lane that held it drops it and takes
+// its next.
+template <int EL, class R>
+__global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteForward p) {
+  constexpr int LPR = R::LPR, PER = R::PER;
+  __shared__ unsigned long long mask[kRouteMaxExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, pos = lane % LPR;
+  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  const int e0 = pos * PER, k = p.k;
+  if (p.m_splits) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = 0;
     __syncthreads();
   }
-  if (e < E) {
-    start[e] = tot[e] - sum;
-    m_splits[e] = sum;
+  for (int r = wave * R::rows + sub; r < kChunk; r += kRouteWaves * R::rows) {
+    const int64_t t = t0 + r;
+    if (t >= p.T) break;
+    float l[PER];
+    load_row<EL, PER>(p.logits, t, p.E, e0, p.whole, l);
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = e0 + i < p.E ? order_key(l[i]) : 0;
+    float top = 0.f, w[2] = {0.f, 0.f}, sum = 0.f;
+    int id[2] = {0, 0};  // the row's lane j keeps choices j and LPR + j
+    for (int j = 0; j < k; ++j) {
+      uint32_t best = 0, at = 0;  // the lane's largest key left, at its lowest expert
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        at = key[i] > best ? e0 + i : at;
+        best = key[i] > best ? key[i] : best;
+      }
+      const uint32_t m = row_max<LPR>(best);
+      const int e = (int)row_min<LPR>(best == m ? at : 0xffffffffu);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = e == e0 + i ? 0 : key[i];
+      const float v = __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
+      if (j == 0) top = v;
+      const float s = p.sigm ? 1.f / (1.f + expf(-v)) : top == -INFINITY ? 0.f : expf(v - top);
+      sum += s;
+      const bool mine = pos == j % LPR;
+      if (LPR == 64 || j < LPR) {
+        id[0] = mine ? e : id[0];
+        w[0] = mine ? s : w[0];
+      } else {
+        id[1] = mine ? e : id[1];
+        w[1] = mine ? s : w[1];
+      }
+      if (p.m_splits && pos == 0) atomicOr(&mask[e], 1ull << r);
+    }
+    if (!p.renorm) {
+      if (p.sigm) {
+        sum = 1.f;
+      } else {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sum += top == -INFINITY ? 0.f : expf(l[i] - top);
+        sum = row_sum<LPR>(sum);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < (LPR == 64 ? 1 : 2); ++h) {
+      const int j = h * LPR + pos;
+      if (j < k) {
+        p.ids[t * k + j] = id[h];
+        p.weights[t * k + j] = sum > 0.f ? w[h] / sum : 0.f;
+      }
+    }
+  }
+  if (!p.m_splits) return;
+  __syncthreads();
+  if (p.T > kChunk) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.masks[(int64_t)blockIdx.x * p.E + e] = mask[e];
+    return;
+  }
+  // the only chunk: an expert's rows start at the sum of the counts before it
+  __shared__ int start[kRouteMaxExperts];
+  const int e = threadIdx.x, n = e < p.E ? __popcll(mask[e]) : 0;
+  start[e] = block_scan(n) - n;
+  if (e < p.E) p.m_splits[e] = n;
+  __syncthreads();
+  for (int s = threadIdx.x; s < (int)p.T * k; s += kRouteThreads) {
+    const int e = p.ids[s];
+    const int row = start[e] + __popcll(mask[e] & ((1ull << (s / k)) - 1));
+    p.row_index[s] = row;
+    p.slot_index[row] = s;
   }
 }
 
+// Where a chunk's slots of an expert start among the expert's: one wave an expert, lane l
+// taking chunks l, l + 64, ...
+__global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(const unsigned long long *__restrict__ masks,
+                                                                   int64_t chunks, int E, int32_t *__restrict__ base,
+                                                                   int64_t *__restrict__ m_splits) {
+  const int e = blockIdx.x * kRouteWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (e >= E) return;
+  int before = 0;
+  for (int64_t c0 = 0; c0 < chunks; c0 += 64) {
+    const int64_t c = c0 + lane;
+    const int n = c < chunks ? __popcll(masks[c * E + e]) : 0;
+    const int upto = wave_scan(n);
+    if (c < chunks) base[c * E + e] = before + upto - n;
+    before += __shfl(upto, 63);
+  }
+  if (lane == 0) m_splits[e] = before;
+}
+
+// The rows of a chunk's slots: the experts' starts (a scan of the totals, made by every
+// workgroup), the chunk's within the expert, and the rank within the chunk.
 __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t *__restrict__ ids, int64_t T, int E,
                                                                    int k, const unsigned long long *__restrict__ masks,
                                                                    const int32_t *__restrict__ base,
-                                                                   const int32_t *__restrict__ start,
+                                                                   const int64_t *__restrict__ m_splits,
                                                                    int32_t *__restrict__ row_index,
                                                                    int32_t *__restrict__ slot_index) {
-  const int64_t t0 = (int64_t)blockIdx.x * kPlanTokens;
-  const int n = (int)min64(kPlanTokens, T - t0) * k;
+  __shared__ int start[kRouteMaxExperts];
+  __shared__ unsigned long long mask[kRouteMaxExperts];
+  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  const int n = (int)min64(kChunk, T - t0) * k;
+  const int e = threadIdx.x;
+  int total = 0, here = 0;
+  if (e < E) {
+    total = (int)m_splits[e];
+    here = base[(int64_t)blockIdx.x * E + e];
+    mask[e] = masks[(int64_t)blockIdx.x * E + e];
+  }
+  start[e] = block_scan(total) - total + here;
+  __syncthreads();
   for (int s = threadIdx.x; s < n; s += kRouteThreads) {
     const int e = ids[t0 * k + s];
-    const int64_t at = (int64_t)blockIdx.x * E + e;
-    const int row = start[e] + base[at] + __popcll(masks[at] & ((1ull << (s / k)) - 1));
+    const int row = start[e] + __popcll(mask[e] & ((1ull << (s / k)) - 1));
     row_index[t0 * k + s] = row;
     slot_index[row] = (int32_t)(t0 * k + s);
   }
 }
 
-// Gradient of the weights, one wave a token.  With s the scores before any division
-// and w = s / sum(s) where renormalised:
+struct RouteBackward {
+  const void *logits;
+  const int32_t *ids;
+  const float *dweights;
+  void *dlogits;
+  int64_t T;
+  int E, k, sigm, renorm, whole;
+};
+
+// Gradient of the weights.  With s the scores before any division and w = s / sum(s) where
+// renormalised:
 //   softmax             dl_e = p_e (dw_e - sum_j dw_j p_j)        (dw_e 0 if not chosen)
 //   softmax, renorm.    dl_j = w_j (dw_j - sum_i dw_i w_i)        (chosen only)
 //   sigmoid             dl_j = dw_j s_j (1 - s_j)
 //   sigmoid, renorm.    dl_j = (1 - s_j) w_j (dw_j - sum_i dw_i w_i)
-template <int EL>
-__global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void *__restrict__ logits, int64_t T, int E,
-                                                                  int k, int sigm, int renorm,
-                                                                  const int32_t *__restrict__ ids,
-                                                                  const float *__restrict__ dweights,
-                                                                  void *__restrict__ dlogits) {
-  constexpr int kPer = kRouteMaxExperts / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const auto sum = [](float v) {
+template <int EL, class R>
+__global__ __launch_bounds__(256) void route_bwd_kernel(const RouteBackward p) {
+  constexpr int LPR = R::LPR, PER = R::PER, H = LPR == 64 ? 1 : 2;
+  const int lane = threadIdx.x & 63, sub = lane / LPR, pos = lane % LPR, e0 = pos * PER, k = p.k;
+  const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * R::rows + sub;
+  const bool in = t < p.T;  // (every lane stays for the row's reductions)
+  float l[PER], top = -INFINITY;
+  if (in) {
+    load_row<EL, PER>(p.logits, t, p.E, e0, p.whole, l);
+  } else {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-  };
-  float l[kPer], top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 64 + lane;
-    l[i] = e < E ? load_logit<EL>(logits, t * E + e) : -INFINITY;
-    top = fmaxf(top, l[i]);
+    for (int i = 0; i < PER; ++i) l[i] = -INFINITY;
   }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  // lane j holds slot j; an id outside the experts takes no part
-  int id = -1;
-  float dw = 0.f, s = 0.f, slope = 1.f;
-  if (lane < k) {
-    id = ids[t * k + lane];
-    if (id < 0 || id >= E) id = -1;
-    dw = dweights[t * k + lane];
-  }
-  if (id >= 0) {
-    const float v = load_logit<EL>(logits, t * E + id);
-    if (sigm) {
-      s = 1.f / (1.f + expf(-v));
-      slope = 1.f - s;
-    } else {
-      s = top == -INFINITY ? 0.f : expf(v - top);
+  for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
+  top = __uint_as_float(row_reduce<LPR>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+  // the row's lane j holds slots j and LPR + j; an id outside the experts takes no part
+  int id[H];
+  float dw[H], s[H], slope[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int j = h * LPR + pos;
+    id[h] = -1;
+    dw[h] = s[h] = 0.f;
+    slope[h] = 1.f;
+    if (in && j < k) {
+      const int e = p.ids[t * k + j];
+      if (e >= 0 && e < p.E) {
+        id[h] = e;
+        dw[h] = p.dweights[t * k + j];
+        const float v = load_logit<EL>(p.logits, t * p.E + e);
+        if (p.sigm) {
+          s[h] = 1.f / (1.f + expf(-v));
+          slope[h] = 1.f - s[h];
+        } else {
+          s[h] = top == -INFINITY ? 0.f : expf(v - top);
+        }
+      }
     }
   }
-  float total = 1.f;
-  if (renorm)
-    total = sum(s);
-  else if (!sigm) {
+  const bool dense = !p.sigm && !p.renorm;  // every expert has a share
+  float x[PER], total = 1.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = 0.f;
+  if (p.renorm) {
     total = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) total += top == -INFINITY ? 0.f : expf(l[i] - top);
-    total = sum(total);
-  }
-  const float w = total > 0.f ? s / total : 0.f;
-  const float mean = !sigm || renorm ? sum(id >= 0 ? dw * w : 0.f) : 0.f;
-  const float mine = id >= 0 ? slope * w * (dw - mean) : 0.f;
-  // every expert's value: chosen from its slot, others 0 or their share of the softmax
-  const bool dense = !sigm && !renorm;
-  float o[kPer];
+    for (int h = 0; h < H; ++h) total += s[h];
+    total = row_sum<LPR>(total);
+  } else if (dense) {
+    total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    o[i] = dense && total > 0.f ? -mean * (expf(l[i] - top) / total) : 0.f;
+    for (int i = 0; i < PER; ++i) {
+      x[i] = top == -INFINITY ? 0.f : expf(l[i] - top);
+      total += x[i];
+    }
+    total = row_sum<LPR>(total);
+  }
+  float mean = 0.f, mine[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    s[h] = total > 0.f ? s[h] / total : 0.f;
+    mean += dw[h] * s[h];
+  }
+  mean = p.sigm && !p.renorm ? 0.f : row_sum<LPR>(mean);
+#pragma unroll
+  for (int h = 0; h < H; ++h) mine[h] = id[h] >= 0 ? slope[h] * s[h] * (dw[h] - mean) : 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = dense && total > 0.f ? -mean * (x[i] / total) : 0.f;
   for (int j = 0; j < k; ++j) {
-    const int e = __shfl(id, j);
-    const float v = __shfl(mine, j);
+    const int src = sub * LPR + j % LPR;
+    const int e = __shfl(H == 2 && j >= LPR ? id[H - 1] : id[0], src);
+    const float v = __shfl(H == 2 && j >= LPR ? mine[H - 1] : mine[0], src);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (e == i * 64 + lane) o[i] = v;
+    for (int i = 0; i < PER; ++i) x[i] = e == e0 + i ? v : x[i];
   }
+  if (!in) return;
+  const int64_t at = t * p.E + e0;
+  if (p.whole) {
+    constexpr int V = EL == EL_F32 ? 4 : PER < 8 ? 4 : 8;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 64 + lane;
-    if (e >= E) break;
-    if constexpr (EL == EL_F32)
-      ((float *)dlogits)[t * E + e] = o[i];
-    else
-      ((uint16_t *)dlogits)[t * E + e] = f32_to_h16<EL == EL_F16>(o[i]);
+    for (int i = 0; i < PER; i += V) {
+      if (e0 + i >= p.E) continue;
+      if constexpr (EL == EL_F32) {
+        *(float4 *)((float *)p.dlogits + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int j = 0; j < V; j += 2) w[j / 2] = pack_h16x2<EL == EL_F16>(x[i + j], x[i + j + 1]);
+        uint16_t *o = (uint16_t *)p.dlogits + at + i;
+        if constexpr (V == 8) __builtin_memcpy(__builtin_assume_aligned(o, 16), w, 16);
+        else __builtin_memcpy(__builtin_assume_aligned(o, 8), w, 8);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (e0 + i >= p.E) continue;
+      if constexpr (EL == EL_F32) ((float *)p.dlogits)[at + i] = x[i];
+      else ((uint16_t *)p.dlogits)[at + i] = f32_to_h16<EL == EL_F16>(x[i]);
+    }
   }
 }
-
-struct RoutePlan {
-  unsigned long long *masks;  // [blocks][E]
-  int32_t *base;              // [blocks][E]
-  int32_t *start;             // [E]
-};
 
 size_t route_plan_bytes(int64_t T, int E) {
-  const int64_t blocks = (T + kPlanTokens - 1) / kPlanTokens;
-  return (size_t)(blocks * E * 12 + E * 4 + 15) & ~(size_t)15;
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  return (size_t)(chunks * E * 12 + 31) & ~(size_t)15;
 }
+
+// f(element type, lanes and experts a lane of a row)
+template <class F>
+static void each_route(int el, int E, F f) {
+  const auto rows = [&](auto e) {
+    if (E <= 64) f(e, RowLanes<16, 4>());
+    else if (E <= 128) f(e, RowLanes<16, 8>());
+    else if (E <= 256) f(e, RowLanes<16, 16>());
+    else f(e, RowLanes<64, 16>());
+  };
+  if (el == EL_F32) rows(std::integral_constant<int, EL_F32>());
+  else if (el == EL_F16) rows(std::integral_constant<int, EL_F16>());
+  else rows(std::integral_constant<int, EL_BF16>());
+}
+
+// Whether load_row's loads are aligned in every row.
+static int whole_rows(int el, int E) { return E % (el == EL_F32 || E <= 64 ? 4 : 8) == 0; }
 
 hipError_t launch_route_fwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits, int32_t *ids,
                             float *weights, int64_t *m_splits, int32_t *row_index, int32_t *slot_index, void *ws,
                             hipStream_t s) {
-  const int64_t blocks = (T + kPlanTokens - 1) / kPlanTokens;
-  const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteThreads);
-  if (T > 0) {
-    if (el == EL_F32)
-      hipLaunchKernelGGL(route_gates_kernel<EL_F32>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, weights);
-    else if (el == EL_F16)
-      hipLaunchKernelGGL(route_gates_kernel<EL_F16>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, weights);
-    else
-      hipLaunchKernelGGL(route_gates_kernel<EL_BF16>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, weights);
-  }
-  if (m_splits) {
-    RoutePlan r;
-    r.masks = (unsigned long long *)ws;
-    r.base = (int32_t *)(r.masks + blocks * E);
-    r.start = r.base + blocks * E;
-    if (T > 0)
-      hipLaunchKernelGGL(route_masks_kernel, dim3((unsigned)blocks), block, 0, s, ids, T, E, k, r.masks);
-    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kRouteMaxExperts), 0, s, r.masks, blocks, E, r.base, r.start,
-                       m_splits);
-    if (T > 0)
-      hipLaunchKernelGGL(route_rows_kernel, dim3((unsigned)blocks), block, 0, s, ids, T, E, k, r.masks, r.base,
-                         r.start, row_index, slot_index);
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  const RouteForward p{logits, ids, weights, (unsigned long long *)ws, m_splits, row_index, slot_index,
+                       T, E, k, sigm, renorm, whole_rows(el, E)};
+  // (no tokens: one workgroup writes the counts)
+  const dim3 grid((unsigned)(chunks ? chunks : 1)), block(kRouteThreads);
+  each_route(el, E, [&](auto e, auto r) {
+    hipLaunchKernelGGL((route_gates_kernel<e(), decltype(r)>), grid, block, 0, s, p);
+  });
+  if (m_splits && chunks > 1) {
+    int32_t *base = (int32_t *)(p.masks + chunks * E);
+    hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + kRouteWaves - 1) / kRouteWaves)), block, 0, s, p.masks,
+                       chunks, E, base, m_splits);
+    hipLaunchKernelGGL(route_rows_kernel, grid, block, 0, s, ids, T, E, k, p.masks, base, m_splits, row_index,
+                       slot_index);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_route_bwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits,
                             const int32_t *ids, const float *dweights, void *dlogits, hipStream_t s) {
-  const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteThreads);
-  if (el == EL_F32)
-    hipLaunchKernelGGL(route_bwd_kernel<EL_F32>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, dweights,
-                       dlogits);
-  else if (el == EL_F16)
-    hipLaunchKernelGGL(route_bwd_kernel<EL_F16>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, dweights,
-                       dlogits);
-  else
-    hipLaunchKernelGGL(route_bwd_kernel<EL_BF16>, grid, block, 0, s, logits, T, E, k, sigm, renorm, ids, dweights,
-                       dlogits);
+  const RouteBackward p{logits, ids, dweights, dlogits, T, E, k, sigm, renorm, whole_rows(el, E)};
+  each_route(el, E, [&](auto e, auto r) {
+    const int64_t rows = 4 * decltype(r)::rows;
+    hipLaunchKernelGGL((route_bwd_kernel<e(), decltype(r)>), dim3((unsigned)((T + rows - 1) / rows)), dim3(256), 0, s,
+                       p);
+  });
   return hipGetLastError();
 }
 
