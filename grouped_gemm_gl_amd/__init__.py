@@ -124,6 +124,8 @@ def _check(rc: int):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized():  # the same handle, without a Stream object (2.4 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -547,13 +549,16 @@ def gl_wgrad_mxfp8(dy_t: Tensor, dy_t_scale: Tensor, x_t: Tensor, x_t_scale: Ten
 
 def _on_one_device(first: Tensor, *others) -> None:
     """Every given tensor (lists of them too) is on ``first``'s GPU."""
-    dev = first.device
-    if dev.type != "cuda":
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on the GPU")
     for t in others:
-        for u in (t,) if isinstance(t, Tensor) else t or ():
-            if u.device != dev:
-                raise ValueError(f"tensors must be on one device (got {dev} and {u.device})")
+        if t is None:
+            continue
+        if not isinstance(t, Tensor):
+            _on_one_device(first, *t)
+        elif t.get_device() != dev:
+            raise ValueError(f"tensors must be on one device (got {first.device} and {t.device})")
 
 
 def _enough(workspace: Optional[Tensor], size: int) -> None:

@@ -261,8 +261,7 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
 #pragma unroll
   for (int t = 0; t < NT; ++t) ag[t] = au[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   const int units = (int)((p.K + W::kElems - 1) / W::kElems);
-  for (int c0 = wave; c0 < units; c0 += kUpWaves * U) {
-    W ng[U], nu[U];
+  const auto step = [&](int c0, const W *g, const W *u, W *ng, W *nu) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (t && t * 16 >= tok.n) break;
@@ -285,12 +284,15 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
           ag[t] = mma<EL>(g[i].operand(s), b[i][s], ag[t]);
           au[t] = mma<EL>(u[i].operand(s), b[i][s], au[t]);
         }
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      g[i] = ng[i];
-      u[i] = nu[i];
-    }
+  };
+  // two register sets in turn: copying one to the other would wait for its loads
+  W ng[U], nu[U];
+  for (int c0 = wave; c0 < units; c0 += 2 * kUpWaves * U) {
+    step(c0, g, u, ng, nu);
+    if (c0 + kUpWaves * U >= units) break;
+    step(c0 + kUpWaves * U, ng, nu, g, u);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -317,25 +319,31 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
   const bool by_expert = p.E <= p.T * p.k;
   const int e = by_expert ? (int)blockIdx.y : p.ids[blockIdx.y];
   const bool valid = e >= 0 && e < p.E;
+  // lane t of the first wave: the slots of token t, 8 at a time, loaded ahead of the weights
+  const bool search = threadIdx.x < 64 && lane < p.T && valid;
+  int id[8];
+  float w[8];
+  const auto slots = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = lane * p.k + (j0 + i < p.k ? j0 + i : j0);
+      id[i] = p.ids[s];
+      w[i] = p.gates[s];
+    }
+  };
+  if (search) slots(0);
   const UpWeights<WEL> weights(p, valid ? e : 0, f0);
   Unit<WEL> g[up_units<WEL>()], u[up_units<WEL>()];
   // a slot's expert is almost always read: its first weights are on their way during the
   // search for its tokens
   if (valid && !by_expert) weights.load(g, u, threadIdx.x >> 6);
   if (threadIdx.x < 64) {
-    // lane t: the slots of token t that name the workgroup's expert
+    // the slots of token t that name the workgroup's expert
     int first = -1;
     float gate = 0.f;
-    if (lane < p.T && valid)
+    if (search)
       for (int j0 = 0; j0 < p.k; j0 += 8) {
-        int id[8];
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int s = lane * p.k + (j0 + i < p.k ? j0 + i : j0);
-          id[i] = p.ids[s];
-          w[i] = p.gates[s];
-        }
+        if (j0) slots(j0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (j0 + i < p.k && id[i] == e && w[i] != 0.f) {
@@ -458,8 +466,6 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
   const uint32_t part = col < kCols ? 0 : (uint32_t)(p.T * p.k) * ab;  // the second parts' plane
   // items (entry, U units of F), dealt to the waves in turn
   const int pieces = (int)((p.F + W::kElems * U - 1) / (W::kElems * U));
-  int i = wave / pieces, c = wave - i * pieces;
-  W cur[U], nxt[U];
   const auto load = [&](W *w, int i, int c) {
     const int e = __builtin_amdgcn_readfirstlane(ent[i].expert);
     const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, n0));
@@ -467,8 +473,9 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
 #pragma unroll
     for (int j = 0; j < U; ++j) w[j].load(r, s, row, (c * U + j) * 128, end, srow, wide, q);
   };
-  if (i < n) load(cur, i, c);
-  while (i < n) {
+  int i = wave / pieces, c = wave - i * pieces;
+  // one item with its weights in `cur`; moves on to the next, whose weights go to `nxt`
+  const auto step = [&](const W *cur, W *nxt) {
     int ni = i, nc = c + kDownWaves;
     while (nc >= pieces) {
       nc -= pieces;
@@ -499,10 +506,16 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
         *o += sum;
       }
     }
-#pragma unroll
-    for (int j = 0; j < U; ++j) cur[j] = nxt[j];
     i = ni;
     c = nc;
+  };
+  // two register sets in turn: copying one to the other would wait for its loads
+  W w0[U], w1[U];
+  if (i < n) load(w0, i, c);
+  while (i < n) {
+    step(w0, w1);
+    if (i >= n) break;
+    step(w1, w0);
   }
   __syncthreads();
   for (int o = threadIdx.x; o < p.T * 16; o += kDownThreads) {

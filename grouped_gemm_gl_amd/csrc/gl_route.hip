@@ -236,12 +236,20 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(const unsigne
   const int e = blockIdx.x * kRouteWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (e >= E) return;
   int before = 0;
-  for (int64_t c0 = 0; c0 < chunks; c0 += 64) {
-    const int64_t c = c0 + lane;
-    const int n = c < chunks ? __popcll(masks[c * E + e]) : 0;
-    const int upto = wave_scan(n);
-    if (c < chunks) base[c * E + e] = before + upto - n;
-    before += __shfl(upto, 63);
+  for (int64_t c0 = 0; c0 < chunks; c0 += 64 * 8) {
+    int n[8];  // loaded together: the scans wait once
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + i * 64 + lane;
+      n[i] = c < chunks ? __popcll(masks[c * E + e]) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + i * 64 + lane;
+      const int upto = wave_scan(n[i]);
+      if (c < chunks) base[c * E + e] = before + upto - n[i];
+      before += __shfl(upto, 63);
+    }
   }
   if (lane == 0) m_splits[e] = before;
 }
