@@ -207,6 +207,216 @@ struct UpTokens {
   float gate[kMoeMaxTokens];  // the token's weight for it (all its slots that name it)
 };
 
+// ------------------------------------------------------------------ few columns --
+// Few tokens of an expert go without MFMA.  The A operand's layout makes a
+// load touch 16 rows, 64 bytes each; the same loads taking 1 KiB of one row at a time
+// stream half as fast again (67 MB over 512 workgroups: 15.9 and 11.1 us).  So a wave
+// takes 1 KiB blocks of 8 rows, with 16 bytes of each row in a lane, the tokens' values
+// of the same places beside them, and dot products in the lane; the lanes' sums are added
+// at the end of a row.
+constexpr int kVecRows = 8;
+
+template <int WEL>
+constexpr int block_elems() { return WEL == EL_MX ? 1024 : 1024 / elem_bytes(WEL); }
+
+// The lane's 16 bytes of each of 8 rows.
+template <int WEL>
+struct VecRows {
+  i32x4_t r[kVecRows];
+  uint8_t s[WEL == EL_MX ? kVecRows : 1];
+  // row byte offsets from the resource's base are i * wb; a row not < rows is not read
+  __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, int first, int n, uint32_t at, uint32_t wb,
+                       int rows) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool ok = at < wb && i < rows;
+      r[first + i] = load16(w, ok ? i * wb + at : kNowhere);
+      if constexpr (WEL == EL_MX)
+        s[first + i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sc, (int)(ok ? (i * wb + at) / 32 : kNowhere), 0, 0);
+    }
+  }
+};
+
+// A lane's values of one token at the places of its 16 weight bytes: 16 bytes of the
+// activations' type, or 32 beside MXFP8 codes.
+template <int WEL>
+struct VecToken {
+  static constexpr int parts = WEL == EL_MX ? 2 : 1;
+  i32x4_t v[parts];
+  __device__ void load(__amdgpu_buffer_rsrc_t x, uint32_t row, uint32_t at, uint32_t xb) {
+#pragma unroll
+    for (int i = 0; i < parts; ++i) v[i] = load16(x, at + 16 * i < xb ? row + at + 16 * i : kNowhere);
+  }
+};
+
+template <int EL>
+__device__ __forceinline__ float dot2(int a, int b, float c) {
+  if constexpr (EL == EL_F16) {
+    typedef __attribute__((ext_vector_type(2))) _Float16 h2;
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
+  } else {
+    typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, a), __builtin_bit_cast(b2, b), c, false);
+  }
+}
+
+// acc[r][c] += row r . token c over the lane's places, for n tokens whose values are the
+// sum of P parts
+template <int EL, int WEL, int NV, int P>
+__device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<WEL> (*x)[P], int n, float (*acc)[NV]) {
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r) {
+    if constexpr (WEL == EL_MX) {
+      const float f = __uint_as_float((uint32_t)w.s[r] << 23);
+      int q[8];  // 16 codes as bf16 pairs, exact there
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = w.r[r][i];
+        q[2 * i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, false));
+        q[2 * i + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, true));
+      }
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        if (c < n)
+#pragma unroll
+          for (int d = 0; d < P; ++d)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[r][c] = dot2<EL>(q[i], x[c][d].v[i >> 2][i & 3], acc[r][c]);
+      __builtin_amdgcn_sched_barrier(0);  // one row's expanded codes in registers at a time
+    } else {
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        if (c < n)
+#pragma unroll
+          for (int d = 0; d < P; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int a = w.r[r][i], b = x[c][d].v[0][i];
+              if constexpr (EL == EL_F32) acc[r][c] = fmaf(__int_as_float(a), __int_as_float(b), acc[r][c]);
+              else acc[r][c] = dot2<EL>(a, b, acc[r][c]);
+            }
+    }
+  }
+}
+
+// Sums over the wave's lanes of 8 values: lane l gets that of value vec_row(l).  Each of
+// the first steps adds two values' halves of the lanes, so the values halve with it.
+__device__ __forceinline__ int vec_row(int lane) { return (lane >> 5) * 4 + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1); }
+template <int dpp>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), dpp, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float vec_sum(const float *v, int stride) {
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i * stride]), __float_as_uint(v[(i + 4) * stride]),
+                                                    false, false);
+    a[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(a[i + 2]), false, false);
+    b[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  const bool high = threadIdx.x & 8;
+  float s = (high ? b[1] : b[0]) + dpp_move<0x128>(high ? b[0] : b[1]);  // rotate by 8 within 16
+  s += dpp_move<0xb1>(s);   // quad_perm [1, 0, 3, 2]
+  s += dpp_move<0x4e>(s);   // quad_perm [2, 3, 0, 1]
+  s += dpp_move<0x141>(s);  // mirrored within 8: the other quad
+  return s;
+}
+
+// Rounds v to the weights' 16-bit type in two parts: v ~ hi + lo.
+template <bool F16>
+__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
+  hi = f32_to_h16<F16>(v);
+  const float rest = v - h16_to_f32<F16>(hi);
+  lo = fabsf(rest) < INFINITY ? f32_to_h16<F16>(rest) : (uint16_t)0;  // hi is not finite
+}
+
+// Token's value a for slot's row of the workspace, column f.
+template <int EL>
+__device__ __forceinline__ void store_a(const MoeParams &p, int slot, int64_t f, float a) {
+  const int64_t at = slot * p.F + f;
+  if constexpr (EL == EL_F32) {
+    ((float *)p.a)[at] = a;
+  } else {
+    uint16_t *hi = (uint16_t *)p.a, *lo = hi + (int64_t)p.T * p.k * p.F;
+    split<EL == EL_F16>(a, hi[at], lo[at]);
+  }
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
+
+// The 8 rows of W1 behind 4 columns of a, a wave's share of the workgroup's 16.
+template <int WEL>
+struct UpRows {
+  __amdgpu_buffer_rsrc_t wg, wu, sg, su;
+  int64_t f0;
+  uint32_t wb;
+  int n;  // columns below F
+  __device__ UpRows(const MoeParams &p, int e, int64_t f) : f0(f), wb((uint32_t)row_bytes<WEL>(p.K)) {
+    n = (int)(p.F - f < 4 ? p.F - f : 4);
+    wg = moe_rsrc(weight_row<WEL>(p.w1, e, f));
+    wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f));
+    sg = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, f) : nullptr);
+    su = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, p.F + f) : nullptr);
+  }
+  __device__ void load(VecRows<WEL> &w, int block) const {
+    const uint32_t at = (block * 64 + (threadIdx.x & 63)) * 16;
+    w.load(wg, sg, 0, 4, at, wb, n);
+    w.load(wu, su, 4, 4, at, wb, n);
+  }
+};
+
+// a of 4 columns f0 ... f0 + 3 for up to NV tokens, by one wave: rows 0-3 are the gate's,
+// 4-7 the up's.
+template <int EL, int WEL, int NV>
+__device__ __forceinline__ void up_vector(const MoeParams &p, const UpTokens &tok, const UpRows<WEL> &rows,
+                                          VecRows<WEL> &w0) {
+  const int lane = threadIdx.x & 63;
+  constexpr uint32_t kX = 16 * VecToken<WEL>::parts;
+  const uint32_t xb = (uint32_t)(p.K * elem_bytes(EL));
+  const auto xr = moe_rsrc(p.x);
+  uint32_t xrow[NV];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) xrow[c] = __builtin_amdgcn_readfirstlane(tok.slot[c < tok.n ? c : 0] / p.k) * xb;
+  float acc[kVecRows][NV] = {};
+  const int blocks = (int)((p.K + block_elems<WEL>() - 1) / block_elems<WEL>());
+  VecToken<WEL> x0[NV][1], x1[NV][1];
+  const auto load_x = [&](VecToken<WEL> (*x)[1], int b) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      if (c < tok.n) x[c][0].load(xr, xrow[c], (b * 64 + lane) * kX, xb);
+  };
+  VecRows<WEL> w1;
+  load_x(x0, 0);
+  for (int b = 0; b < blocks; b += 2) {  // two register sets in turn
+    load_x(x1, b + 1);
+    rows.load(w1, b + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    vec_dots<EL, WEL, NV, 1>(w0, x0, tok.n, acc);
+    if (b + 1 >= blocks) break;
+    __builtin_amdgcn_sched_barrier(0);
+    load_x(x0, b + 2);
+    rows.load(w0, b + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    vec_dots<EL, WEL, NV, 1>(w1, x1, tok.n, acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  const int64_t f = rows.f0 + (vec_row(lane) & 3);
+  const bool mine = lane < 32 && f < p.F;
+  const float bg = mine ? bias_at<EL>(p.w1, tok.expert, f) : 0.f, bu = mine ? bias_at<EL>(p.w1, tok.expert, p.F + f) : 0.f;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    if (c >= tok.n) break;
+    const float g = vec_sum(&acc[0][c], NV), u = __shfl_xor(g, 32);
+    if (mine && (lane & 7) == 0) store_a<EL>(p, tok.slot[c], f, tok.gate[c] * swiglu(g + bg, u + bu));
+  }
+}
+
+// ----------------------------------------------------------------- many columns --
 // The weight side of the up kernel: units wave, wave + kUpWaves, ... of the gate's and the
 // up's 16 rows, U of each at a time.
 template <int WEL>
@@ -241,12 +451,14 @@ struct UpWeights {
   }
 };
 
-// Contraction over K for up to NT tiles of 16 columns; g and u hold the first units.
+// Contraction over K for up to NT tiles of 16 columns.
 template <int EL, int WEL, int NT>
-__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, const UpWeights<WEL> &weights,
-                                           Unit<WEL> *g, Unit<WEL> *u, float *sums) {
+__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
   using W = Unit<WEL>;
   constexpr int U = up_units<WEL>();
+  const UpWeights<WEL> weights(p, tok.expert, f0);
+  W g[U], u[U];
+  weights.load(g, u, threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const uint32_t xb = (uint32_t)(p.K * elem_bytes(EL));
   const auto xr = moe_rsrc(p.x);
@@ -302,18 +514,35 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
   }
 }
 
-// Rounds v to the weights' 16-bit type in two parts: v ~ hi + lo.
-template <bool F16>
-__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
-  hi = f32_to_h16<F16>(v);
-  const float rest = v - h16_to_f32<F16>(hi);
-  lo = fabsf(rest) < INFINITY ? f32_to_h16<F16>(rest) : (uint16_t)0;  // hi is not finite
+// a of the workgroup's 16 columns for all of the expert's tokens.
+template <int EL, int WEL, int NT>
+__device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
+  up_product<EL, WEL, NT>(p, tok, f0, sums);
+  __syncthreads();
+  const int f = threadIdx.x & 15;
+  if (f0 + f >= p.F) return;
+  const float bg = bias_at<EL>(p.w1, tok.expert, f0 + f), bu = bias_at<EL>(p.w1, tok.expert, p.F + f0 + f);
+  for (int c = threadIdx.x >> 4; c < tok.n; c += 16) {
+    // row f, column c of a 16 x 16 result is value f % 4 of lane 16 (f / 4) + c % 16
+    const float *s = sums + ((c >> 4) * kUpWaves * 2 * 64 + ((f >> 2) * 16 + (c & 15))) * 4 + (f & 3);
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < kUpWaves; ++w) {
+      g += s[w * 512];
+      u += s[w * 512 + 256];
+    }
+    g += bg;
+    u += bu;
+    store_a<EL>(p, tok.slot[c], f0 + f, tok.gate[c] * swiglu(g, u));
+  }
 }
 
-template <int EL, int WEL, int NT>
+// NV: experts of up to that many tokens go by up_vector, the others by up_product in at
+// most NT tiles (NT 0: the call has no more than NV tokens).
+template <int EL, int WEL, int NV, int NT>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
   __shared__ UpTokens tok;
-  __shared__ __align__(16) float sums[NT * kUpWaves * 2 * 64 * 4];
+  __shared__ __align__(16) float sums[NT ? NT * kUpWaves * 2 * 64 * 4 : 4];
   const int lane = threadIdx.x & 63;
   const int64_t f0 = (int64_t)blockIdx.x * kMoeRows;
   const bool by_expert = p.E <= p.T * p.k;
@@ -332,11 +561,11 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
     }
   };
   if (search) slots(0);
-  const UpWeights<WEL> weights(p, valid ? e : 0, f0);
-  Unit<WEL> g[up_units<WEL>()], u[up_units<WEL>()];
-  // a slot's expert is almost always read: its first weights are on their way during the
+  const UpRows<WEL> rows(p, valid ? e : 0, f0 + (threadIdx.x >> 6) * 4);
+  VecRows<WEL> r;
+  // a slot's expert is almost always read: its first rows are on their way during the
   // search for its tokens
-  if (valid && !by_expert) weights.load(g, u, threadIdx.x >> 6);
+  if (NV > 0 && valid && !by_expert) rows.load(r, 0);
   if (threadIdx.x < 64) {
     // the slots of token t that name the workgroup's expert
     int first = -1;
@@ -371,32 +600,14 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
   }
   __syncthreads();
   if (tok.expert < 0) return;
-  if (by_expert) weights.load(g, u, threadIdx.x >> 6);
-  up_product<EL, WEL, NT>(p, tok, weights, g, u, sums);
-  __syncthreads();
-  const int f = threadIdx.x & 15;
-  if (f0 + f >= p.F) return;
-  const float bg = bias_at<EL>(p.w1, e, f0 + f), bu = bias_at<EL>(p.w1, e, p.F + f0 + f);
-  for (int c = threadIdx.x >> 4; c < tok.n; c += 16) {
-    // row f, column c of a 16 x 16 result is value f % 4 of lane 16 (f / 4) + c % 16
-    const float *s = sums + ((c >> 4) * kUpWaves * 2 * 64 + ((f >> 2) * 16 + (c & 15))) * 4 + (f & 3);
-    float g = 0.f, u = 0.f;
-#pragma unroll
-    for (int w = 0; w < kUpWaves; ++w) {
-      g += s[w * 512];
-      u += s[w * 512 + 256];
-    }
-    g += bg;
-    u += bu;
-    const float a = tok.gate[c] * (g * sigmoid(g) * u);
-    const int64_t at = tok.slot[c] * p.F + f0 + f;
-    if constexpr (EL == EL_F32) {
-      ((float *)p.a)[at] = a;
-    } else {
-      uint16_t *hi = (uint16_t *)p.a, *lo = hi + (int64_t)p.T * p.k * p.F;
-      split<EL == EL_F16>(a, hi[at], lo[at]);
+  if constexpr (NV > 0) {
+    if (NT == 0 || tok.n <= NV) {
+      if (by_expert) rows.load(r, 0);
+      up_vector<EL, WEL, NV>(p, tok, rows, r);
+      return;
     }
   }
+  if constexpr (NT > 0) up_many<EL, WEL, NT>(p, tok, f0, sums);
 }
 
 // LDS of the down kernel: the entries with an expert, in order.
@@ -405,71 +616,100 @@ struct DownEntry {
   int32_t base, n;  // its tokens' slots are slots[base ... base + n)
 };
 
+// A workgroup's place in the down kernel: its first row of W2, and its tables in LDS.
+struct DownPlace {
+  int64_t n0;
+  const DownEntry *ent;  // n_vec entries of few tokens from the front, the others from the back
+  const int16_t *slots;
+  float *acc;  // [waves][T][16 rows] sums of a token
+  int n_vec, n_many;
+};
+
+// Entries of up to NV tokens: items (entry, 8 rows, 1 KiB block of F), dealt to the waves
+// in turn.
+template <int EL, int WEL, int R, int NV>
+__device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace &o) {
+  constexpr int parts = EL == EL_F32 ? 1 : 2;  // of a
+  constexpr uint32_t kX = 16 * VecToken<WEL>::parts;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = (uint32_t)(p.F * elem_bytes(EL));
+  const uint32_t plane = (uint32_t)(p.T * p.k) * ab;
+  const auto ar = moe_rsrc(p.a);
+  const int blocks = (int)((p.F + block_elems<WEL>() - 1) / block_elems<WEL>()), per = blocks * (R / 8);
+  int i = wave / per, c = wave - i * per;
+  const auto load = [&](VecRows<WEL> &w, VecToken<WEL> (*x)[parts], int i, int c) {
+    const int h = c / blocks, b = c - h * blocks;
+    const DownEntry t = o.ent[i];
+    const int e = __builtin_amdgcn_readfirstlane(t.expert), n = __builtin_amdgcn_readfirstlane(t.n);
+    const int base = __builtin_amdgcn_readfirstlane(t.base);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (k < n) {
+        const uint32_t row = (uint32_t)__builtin_amdgcn_readfirstlane(o.slots[base + k]) * ab;
+#pragma unroll
+        for (int d = 0; d < parts; ++d) x[k][d].load(ar, row + d * plane, (b * 64 + lane) * kX, ab);
+      }
+    const int64_t r0 = o.n0 + h * 8;
+    w.load(moe_rsrc(weight_row<WEL>(p.w2, e, r0)), moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, r0) : nullptr), 0, 8,
+           (uint32_t)(b * 64 + lane) * 16, wb, (int)min64(p.N - r0, 8));
+  };
+  const auto step = [&](const VecRows<WEL> &w, const VecToken<WEL> (*x)[parts], VecRows<WEL> &nw,
+                        VecToken<WEL> (*nx)[parts]) {
+    int ni = i, nc = c + kDownWaves;
+    while (nc >= per) {
+      nc -= per;
+      ++ni;
+    }
+    if (ni < o.n_vec) load(nw, nx, ni, nc);
+    __builtin_amdgcn_sched_barrier(0);
+    const int n = __builtin_amdgcn_readfirstlane(o.ent[i].n), base = __builtin_amdgcn_readfirstlane(o.ent[i].base);
+    float acc[kVecRows][NV] = {};
+    vec_dots<EL, WEL, NV, parts>(w, x, n, acc);
+    // lanes 0 ... 7 of a row's 8 hold the same sum: the k-th adds token k's
+    const int k = lane & 7;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j < n) {
+        const float v = vec_sum(&acc[0][j], NV);
+        sum = k == j ? v : sum;
+      }
+    if (k < n) o.acc[(wave * p.T + o.slots[base + k] / p.k) * 16 + (c / blocks) * 8 + vec_row(lane)] += sum;
+    __builtin_amdgcn_sched_barrier(0);
+    i = ni;
+    c = nc;
+  };
+  VecRows<WEL> w0, w1;
+  VecToken<WEL> x0[NV][parts], x1[NV][parts];
+  if (i < o.n_vec) load(w0, x0, i, c);
+  while (i < o.n_vec) {  // two register sets in turn
+    step(w0, x0, w1, x1);
+    if (i >= o.n_vec) break;
+    step(w1, x1, w0, x0);
+  }
+}
+
+// The other entries: items (entry, U units of F), dealt to the waves in turn, 16 rows by
+// the entry's tokens in MFMA steps.
 template <int EL, int WEL, int R>
-__global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams p) {
+__device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o) {
   using W = Unit<WEL>;
   constexpr int U = down_units<WEL>();
-  extern __shared__ __align__(16) char lds[];
-  __shared__ int wave_n[kDownWaves], wave_m[kDownWaves];
-  float *acc = (float *)lds;  // [waves][T][16 rows] sums of a token
-  DownEntry *ent = (DownEntry *)(acc + kDownWaves * p.T * 16);
-  int16_t *slots = (int16_t *)(ent + p.n_entries);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * R;
-  for (int i = threadIdx.x; i < kDownWaves * p.T * 4; i += kDownThreads) ((f32x4_t *)acc)[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  // compact the table: running counts of entries and of their tokens
-  int n = 0, members = 0;
-  for (int d0 = 0; d0 < p.n_entries; d0 += kDownThreads) {
-    const int d = d0 + threadIdx.x;
-    MoeEntry t{0, -1, 0};
-    if (d < p.n_entries) t = p.entries[d];
-    const bool on = t.expert >= 0;
-    const int mine = on ? __popcll(t.tokens) : 0;
-    const uint64_t ons = __ballot(on);
-    int upto = mine;  // inclusive sum over the wave's lanes
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int o = __shfl_up(upto, s);
-      if (lane >= s) upto += o;
-    }
-    if (lane == 63) {
-      wave_n[wave] = __popcll(ons);
-      wave_m[wave] = upto;
-    }
-    __syncthreads();
-    int at = n + __popcll(ons & ((1ull << lane) - 1)), base = members + upto - mine;
-    for (int w = 0; w < kDownWaves; ++w) {
-      if (w < wave) {
-        at += wave_n[w];
-        base += wave_m[w];
-      }
-      n += wave_n[w];
-      members += wave_m[w];
-    }
-    if (on) {
-      ent[at] = {t.expert, base, mine};
-      slots[base] = (int16_t)t.first;
-      uint64_t left = t.tokens & (t.tokens - 1);
-      for (int i = base + 1; left; ++i, left &= left - 1)
-        slots[i] = p.slot_of[d * 64 + __ffsll((unsigned long long)left) - 1];
-    }
-    __syncthreads();
-  }
-
+  const auto entry = [&](int i) { return o.ent[p.n_entries - 1 - i]; };
   const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = (uint32_t)(p.F * elem_bytes(EL));
-  const uint32_t end = col < R && n0 + col < p.N ? wb : 0;
+  const uint32_t end = col < R && o.n0 + col < p.N ? wb : 0;
   const uint32_t row = col * wb, srow = col * (uint32_t)(p.F / 32);
   const bool wide = p.F % 128 == 0;
   const auto ar = moe_rsrc(p.a);
   constexpr int kCols = EL == EL_F32 ? 16 : 8;  // tokens of a step
   const int token = col & (kCols - 1);
   const uint32_t part = col < kCols ? 0 : (uint32_t)(p.T * p.k) * ab;  // the second parts' plane
-  // items (entry, U units of F), dealt to the waves in turn
   const int pieces = (int)((p.F + W::kElems * U - 1) / (W::kElems * U));
   const auto load = [&](W *w, int i, int c) {
-    const int e = __builtin_amdgcn_readfirstlane(ent[i].expert);
-    const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, n0));
-    const auto s = moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, n0) : nullptr);
+    const int e = __builtin_amdgcn_readfirstlane(entry(i).expert);
+    const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, o.n0));
+    const auto s = moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, o.n0) : nullptr);
 #pragma unroll
     for (int j = 0; j < U; ++j) w[j].load(r, s, row, (c * U + j) * 128, end, srow, wide, q);
   };
@@ -481,11 +721,11 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
       nc -= pieces;
       ++ni;
     }
-    const int base = __builtin_amdgcn_readfirstlane(ent[i].base), m = __builtin_amdgcn_readfirstlane(ent[i].n);
+    const int base = __builtin_amdgcn_readfirstlane(entry(i).base), m = __builtin_amdgcn_readfirstlane(entry(i).n);
     // the entry's tokens as columns; a 16-bit a's two parts are columns of the same step
     for (int t = 0; t < m; t += kCols) {
       const bool on = t + token < m;
-      const int slot = on ? slots[base + t + token] : 0;
+      const int slot = on ? o.slots[base + t + token] : 0;
       const uint32_t arow = (uint32_t)slot * ab + part, aend = on ? ab : 0;
       i32x4_t b[U * W::steps];
 #pragma unroll
@@ -493,7 +733,7 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
         const uint32_t at = (c * U + s / W::steps) * W::b_bytes + W::b_byte(s % W::steps, q);
         b[s] = load16(ar, at < aend ? arow + at : kNowhere);
       }
-      if (t == 0 && ni < n) load(nxt, ni, nc);
+      if (t == 0 && ni < o.n_many) load(nxt, ni, nc);
       __builtin_amdgcn_sched_barrier(0);
       f32x4_t sum = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -502,8 +742,8 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[r] += __shfl_xor(sum[r], 8);
       if (on && col == token) {  // each column another token: no lane shares a sum
-        f32x4_t *o = (f32x4_t *)(acc + (wave * p.T + slot / p.k) * 16 + q * 4);
-        *o += sum;
+        f32x4_t *at = (f32x4_t *)(o.acc + (wave * p.T + slot / p.k) * 16 + q * 4);
+        *at += sum;
       }
     }
     i = ni;
@@ -511,12 +751,67 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams 
   };
   // two register sets in turn: copying one to the other would wait for its loads
   W w0[U], w1[U];
-  if (i < n) load(w0, i, c);
-  while (i < n) {
+  if (i < o.n_many) load(w0, i, c);
+  while (i < o.n_many) {
     step(w0, w1);
-    if (i >= n) break;
+    if (i >= o.n_many) break;
     step(w1, w0);
   }
+}
+
+template <int EL, int WEL, int R, int NV, bool MANY>
+__global__ __launch_bounds__(kDownThreads) void moe_down_kernel(const MoeParams p) {
+  extern __shared__ __align__(16) char lds[];
+  __shared__ int3 wave_n[kDownWaves];
+  float *acc = (float *)lds;  // [waves][T][16 rows] sums of a token
+  DownEntry *ent = (DownEntry *)(acc + kDownWaves * p.T * 16);
+  int16_t *slots = (int16_t *)(ent + p.n_entries);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * R;
+  for (int i = threadIdx.x; i < kDownWaves * p.T * 4; i += kDownThreads) ((f32x4_t *)acc)[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  // compact the table: running counts of the entries of few tokens, the others, and of all
+  // their tokens
+  int n_vec = 0, n_many = 0, members = 0;
+  for (int d0 = 0; d0 < p.n_entries; d0 += kDownThreads) {
+    const int d = d0 + threadIdx.x;
+    MoeEntry t{0, -1, 0};
+    if (d < p.n_entries) t = p.entries[d];
+    const int mine = t.expert >= 0 ? __popcll(t.tokens) : 0;
+    const bool few = mine > 0 && (!MANY || mine <= NV);
+    const uint64_t vec = __ballot(few), many = __ballot(mine > 0 && !few), below = (1ull << lane) - 1;
+    int upto = mine;  // inclusive sum over the wave's lanes
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(upto, s);
+      if (lane >= s) upto += o;
+    }
+    if (lane == 63) wave_n[wave] = make_int3(__popcll(vec), __popcll(many), upto);
+    __syncthreads();
+    int at_vec = n_vec + __popcll(vec & below), at_many = n_many + __popcll(many & below);
+    int base = members + upto - mine;
+    for (int w = 0; w < kDownWaves; ++w) {
+      const int3 n = wave_n[w];
+      if (w < wave) {
+        at_vec += n.x;
+        at_many += n.y;
+        base += n.z;
+      }
+      n_vec += n.x;
+      n_many += n.y;
+      members += n.z;
+    }
+    if (mine) {
+      ent[few ? at_vec : p.n_entries - 1 - at_many] = {t.expert, base, mine};
+      slots[base] = (int16_t)t.first;
+      uint64_t left = t.tokens & (t.tokens - 1);
+      for (int i = base + 1; left; ++i, left &= left - 1)
+        slots[i] = p.slot_of[d * 64 + __ffsll((unsigned long long)left) - 1];
+    }
+    __syncthreads();
+  }
+  const DownPlace place{n0, ent, slots, acc, n_vec, n_many};
+  if constexpr (NV > 0) down_vector<EL, WEL, R, NV>(p, place);
+  if constexpr (MANY) down_many<EL, WEL, R>(p, place);
   __syncthreads();
   for (int o = threadIdx.x; o < p.T * 16; o += kDownThreads) {
     const int r = o & 15, t = o >> 4;
@@ -544,17 +839,44 @@ size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t F) {
 template <int EL, int WEL>
 static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   const dim3 up((unsigned)((p.F + kMoeRows - 1) / kMoeRows), p.n_entries);
-  if (p.T <= 16)
-    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, 1>), up, dim3(kUpThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, 4>), up, dim3(kUpThreads), 0, s, p);
+  const auto go_up = [&](auto nv, auto nt) {
+    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, nv(), nt()>), up, dim3(kUpThreads), 0, s, p);
+  };
+  using std::integral_constant;
+  using Zero = integral_constant<int, 0>;
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  using Four = integral_constant<int, 4>;
+  // Experts of one or two tokens by dot products up to 16 tokens (8 tokens over 32 experts of
+  // 4096/2048: bf16 124 us, without 130; MXFP8 74 and 85); beyond, MFMA alone, whose fewer
+  // registers keep more loads in flight (32 tokens: MXFP8 132 us, with dot products 134).
+  if (p.T == 1) go_up(One(), Zero());
+  else if (p.T == 2) go_up(Two(), Zero());
+  else if (p.T <= 4) go_up(Four(), Zero());
+  else if (p.T <= 16) go_up(Two(), One());
+  else go_up(Zero(), Four());
+
   // LDS: at most 4 KiB of sums a wave, 24 KiB of entries and 4 KiB of slots
   const size_t lds = (size_t)kDownWaves * p.T * 64 + (size_t)p.n_entries * sizeof(DownEntry) + (size_t)p.T * p.k * 2;
-  if (p.N / 16 < 256)
-    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 8>), dim3((unsigned)((p.N + 7) / 8)), dim3(kDownThreads), lds, s, p);
-  else
-    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, 16>), dim3((unsigned)((p.N + 15) / 16)), dim3(kDownThreads), lds, s,
-                       p);
+  const auto go_down = [&](auto r, auto nv, auto many) {
+    hipLaunchKernelGGL((moe_down_kernel<EL, WEL, r(), nv(), many()>), dim3((unsigned)((p.N + r() - 1) / r())),
+                       dim3(kDownThreads), lds, s, p);
+  };
+  // Rows of a workgroup: 16, or 8 where 16 would leave CUs without one.  With 16 rows the
+  // MFMA steps of 16-bit weights do as well for one token as dot products (5 tokens fp16, 8
+  // experts of 14336: 140 us, with dot products 152); with 8 rows half of their operand is
+  // empty (8 tokens over 64 experts of 768: 24.2 us, with dot products 20.5), and beside
+  // MXFP8 codes they load twice the activations (17 tokens over 32 experts of 2048: 52 us,
+  // with dot products 46.6).
+  const auto by_tokens = [&](auto r) {
+    constexpr bool half = decltype(r)() == 8;
+    if (p.T == 1) go_down(r, One(), std::false_type());
+    else if (p.T == 2) go_down(r, Two(), std::false_type());
+    else if (WEL == EL_MX || (half && p.T <= 16)) go_down(r, integral_constant<int, WEL == EL_MX || half ? 2 : 0>(), std::true_type());
+    else go_down(r, Zero(), std::true_type());
+  };
+  if (p.N / 16 < 256) by_tokens(integral_constant<int, 8>());
+  else by_tokens(integral_constant<int, 16>());
 }
 
 hipError_t launch_moe(int el, bool mx, int E, int64_t K, int64_t F, int64_t N, int64_t T, int k, const void *x,

@@ -108,6 +108,25 @@ def test_forward(T, E, k, K, F, N, dtype):
     check(c, run(c))
 
 
+# outputs of 4096 and more (another workgroup shape), contractions over several blocks
+WIDE = [(1, 5, 3, 2600, 1112, 4104), (2, 4, 2, 1544, 520, 4096), (4, 6, 2, 1032, 200, 4104), (9, 5, 2, 520, 1096, 4200),
+        (16, 3, 2, 264, 72, 4096), (24, 6, 2, 136, 264, 4104), (64, 9, 3, 72, 136, 4096)]
+
+
+@pytest.mark.parametrize("T,E,k,K,F,N", WIDE)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_forward_wide(T, E, k, K, F, N, dtype):
+    c = case(T * 5 + E, T, E, k, K, F, N, dtype, bias=T % 2 == 0, residual=T % 3 == 1)
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("T,E,k,K,F,N", [(1, 5, 3, 2080, 1120, 4104), (2, 4, 2, 1056, 2176, 4096), (4, 6, 2, 1152, 224, 4104),
+                                         (9, 5, 2, 544, 1088, 4200), (40, 6, 2, 128, 256, 4104)])
+def test_mxfp8_weights_wide(T, E, k, K, F, N):
+    c = case(T * 7 + E, T, E, k, K, F, N, BF16, mx=True, bias=T % 2 == 0, residual=T % 3 == 1)
+    check(c, run(c))
+
+
 @pytest.mark.parametrize("T,E,k,K,F,N", [(1, 4, 2, 32, 32, 8), (3, 8, 2, 96, 64, 40), (5, 40, 4, 160, 96, 136),
                                          (17, 6, 3, 544, 32, 64), (40, 3, 2, 64, 288, 72), (64, 20, 4, 128, 160, 96)])
 def test_mxfp8_weights(T, E, k, K, F, N):
