@@ -60,6 +60,13 @@ __device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
   return v;
 }
 template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  return __uint_as_float(row_reduce<LPR>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
@@ -67,12 +74,54 @@ template <int LPR>
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
   return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-  return __uint_as_float(row_reduce<LPR>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
+
+// The lane's experts as keys in the order of choice, and a round of it: the row's best
+// expert still there, which its lane drops.  No key but a missing expert's is 0.
+template <int EL, int LPR, int PER>
+struct Choices {
+  uint32_t key[PER];
+  int e0;
+  __device__ Choices(const float *l, int e0_, int E) : e0(e0_) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      uint32_t k;
+      if constexpr (EL == EL_F32) {
+        k = order_key(l[i]);
+      } else {
+        // the value's own 16 bits in order, and below them a larger number for a lower
+        // expert: all keys of a row differ
+        const uint32_t b = f32_to_h16<EL == EL_F16>(l[i] + 0.f);
+        k = ((b & 0x8000u ? ~b & 0xffffu : b | 0x8000u) << 16) | (uint32_t)(0xffff - e0 - i);
+      }
+      key[i] = e0 + i < E ? k : 0;
+    }
+  }
+  // every lane of the row gets the choice's key and expert
+  __device__ void next(uint32_t &m, int &e) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) best = key[i] > best ? key[i] : best;
+    m = row_max<LPR>(best);
+    if constexpr (EL == EL_F32) {  // the lowest expert of that key
+      uint32_t at = 0xffffffffu;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i) at = key[i] == m ? e0 + i : at;
+      e = (int)row_min<LPR>(at);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = e == e0 + i ? 0 : key[i];
+    } else {
+      e = 0xffff - (int)(m & 0xffff);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = key[i] == m ? 0 : key[i];
+    }
+  }
+  // the logit of a choice's key
+  __device__ static float logit(uint32_t m) {
+    if constexpr (EL == EL_F32) return __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
+    const uint32_t b = m >> 16;
+    return as_logit(h16_to_f32<EL == EL_F16>((uint16_t)(b & 0x8000u ? b & 0x7fffu : ~b)));
+  }
+};
 
 // The lane's PER logits of row t from expert e0 on, -inf past the experts.  whole: rows
 // start on a multiple of the loads' 16 (or, 4 values of 16 bits, 8) bytes.
@@ -140,12 +189,12 @@ struct RouteForward {
 // slot's rank among them is the number of bits below its token's.  A call of one chunk
 // makes its whole plan here.
 //
-// Bound by instructions and, for few tokens, latency.  k rounds, each the row's largest
-// key and then the lowest expert that has it; the lane that held it drops it and takes
-// its next.
+// Bound by instructions and, for few tokens, latency: k rounds over the keys that the
+// row's lanes hold.  (Sorting each lane's keys first, so that a round looks at one, took
+// four times as long: the keys that sort need 64 bits.)
 template <int EL, class R>
 __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteForward p) {
-  constexpr int LPR = R::LPR, PER = R::PER;
+  constexpr int LPR = R::LPR, PER = R::PER, H = LPR == 64 ? 1 : 2;
   __shared__ unsigned long long mask[kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, pos = lane % LPR;
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
@@ -159,52 +208,46 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
     if (t >= p.T) break;
     float l[PER];
     load_row<EL, PER>(p.logits, t, p.E, e0, p.whole, l);
-    uint32_t key[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = e0 + i < p.E ? order_key(l[i]) : 0;
-    float top = 0.f, w[2] = {0.f, 0.f}, sum = 0.f;
-    int id[2] = {0, 0};  // the row's lane j keeps choices j and LPR + j
+    Choices<EL, LPR, PER> choices(l, e0, p.E);
+    uint32_t key[H] = {};
+    int id[H] = {};  // the row's lane j keeps choices j and, of 16 lanes, 16 + j
     for (int j = 0; j < k; ++j) {
-      uint32_t best = 0, at = 0;  // the lane's largest key left, at its lowest expert
+      uint32_t m;
+      int e;
+      choices.next(m, e);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        at = key[i] > best ? e0 + i : at;
-        best = key[i] > best ? key[i] : best;
-      }
-      const uint32_t m = row_max<LPR>(best);
-      const int e = (int)row_min<LPR>(best == m ? at : 0xffffffffu);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = e == e0 + i ? 0 : key[i];
-      const float v = __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
-      if (j == 0) top = v;
-      const float s = p.sigm ? 1.f / (1.f + expf(-v)) : top == -INFINITY ? 0.f : expf(v - top);
-      sum += s;
-      const bool mine = pos == j % LPR;
-      if (LPR == 64 || j < LPR) {
-        id[0] = mine ? e : id[0];
-        w[0] = mine ? s : w[0];
-      } else {
-        id[1] = mine ? e : id[1];
-        w[1] = mine ? s : w[1];
-      }
-      if (p.m_splits && pos == 0) atomicOr(&mask[e], 1ull << r);
-    }
-    if (!p.renorm) {
-      if (p.sigm) {
-        sum = 1.f;
-      } else {
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) sum += top == -INFINITY ? 0.f : expf(l[i] - top);
-        sum = row_sum<LPR>(sum);
+      for (int h = 0; h < H; ++h) {
+        const bool mine = j == h * LPR + pos;
+        key[h] = mine ? m : key[h];
+        id[h] = mine ? e : id[h];
       }
     }
+    // scores of the choices, and of all where they are divided by their sum
+    const float top = choices.logit((uint32_t)__shfl((int)key[0], sub * LPR));
+    float w[H], sum = 0.f;
 #pragma unroll
-    for (int h = 0; h < (LPR == 64 ? 1 : 2); ++h) {
+    for (int h = 0; h < H; ++h) {
+      const float v = choices.logit(key[h]);
+      w[h] = h * LPR + pos >= k ? 0.f : p.sigm ? 1.f / (1.f + expf(-v)) : top == -INFINITY ? 0.f : expf(v - top);
+      sum += w[h];
+    }
+    if (p.renorm) {
+      sum = row_sum<LPR>(sum);
+    } else if (p.sigm) {
+      sum = 1.f;
+    } else {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += top == -INFINITY ? 0.f : expf(l[i] - top);
+      sum = row_sum<LPR>(sum);
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
       const int j = h * LPR + pos;
       if (j < k) {
         p.ids[t * k + j] = id[h];
         p.weights[t * k + j] = sum > 0.f ? w[h] / sum : 0.f;
+        if (p.m_splits) atomicOr(&mask[id[h]], 1ull << r);
       }
     }
   }
@@ -228,30 +271,32 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
   }
 }
 
-// Where a chunk's slots of an expert start among the expert's: one wave an expert, lane l
-// taking chunks l, l + 64, ...
+// Where a chunk's slots of an expert start among the expert's.  A workgroup takes 16
+// experts, neighbours in every chunk's masks, and splits the chunks into 64 runs: thread
+// (run, expert) adds up its run, the runs' sums are scanned, and it goes over its run again.
 __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(const unsigned long long *__restrict__ masks,
                                                                    int64_t chunks, int E, int32_t *__restrict__ base,
                                                                    int64_t *__restrict__ m_splits) {
-  const int e = blockIdx.x * kRouteWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (e >= E) return;
-  int before = 0;
-  for (int64_t c0 = 0; c0 < chunks; c0 += 64 * 8) {
-    int n[8];  // loaded together: the scans wait once
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = c0 + i * 64 + lane;
-      n[i] = c < chunks ? __popcll(masks[c * E + e]) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = c0 + i * 64 + lane;
-      const int upto = wave_scan(n[i]);
-      if (c < chunks) base[c * E + e] = before + upto - n[i];
-      before += __shfl(upto, 63);
-    }
+  static_assert(kRouteWaves == 16, "a wave scans one of the workgroup's experts");
+  __shared__ int sums[64][17];
+  const int col = threadIdx.x & 15, run = threadIdx.x >> 4, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 16 + col;
+  const int64_t per = (chunks + 63) / 64, c0 = run * per, c1 = e < E ? min64(c0 + per, chunks) : 0;
+  int n = 0;
+#pragma unroll 8
+  for (int64_t c = c0; c < c1; ++c) n += __popcll(masks[c * E + e]);
+  sums[run][col] = n;
+  __syncthreads();
+  const int v = sums[lane][wave], upto = wave_scan(v);
+  sums[lane][wave] = upto - v;
+  if (lane == 63 && blockIdx.x * 16 + wave < E) m_splits[blockIdx.x * 16 + wave] = upto;
+  __syncthreads();
+  n = sums[run][col];
+#pragma unroll 8
+  for (int64_t c = c0; c < c1; ++c) {
+    base[c * E + e] = n;
+    n += __popcll(masks[c * E + e]);
   }
-  if (lane == 0) m_splits[e] = before;
 }
 
 // The rows of a chunk's slots: the experts' starts (a scan of the totals, made by every
@@ -439,7 +484,7 @@ hipError_t launch_route_fwd(int el, int64_t T, int E, int k, int sigm, int renor
   });
   if (m_splits && chunks > 1) {
     int32_t *base = (int32_t *)(p.masks + chunks * E);
-    hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + kRouteWaves - 1) / kRouteWaves)), block, 0, s, p.masks,
+    hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + 15) / 16)), block, 0, s, p.masks,
                        chunks, E, base, m_splits);
     hipLaunchKernelGGL(route_rows_kernel, grid, block, 0, s, ids, T, E, k, p.masks, base, m_splits, row_index,
                        slot_index);
