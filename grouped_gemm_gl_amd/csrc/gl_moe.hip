@@ -4,37 +4,51 @@
 // in two kernels, without sorting or gathering rows.  A slot whose id is no expert of
 // this call, or whose weight is 0, takes no part.
 //
-// Both are bound by reading the used experts' weights once from HBM, so both stream
-// weight rows straight from global memory into the A operand of 16-row MFMA steps (no
-// LDS in between: no workgroup shares a weight with another) and take the few tokens as
-// the B operand's columns from cache.
+// Both are bound by reading the used experts' weights once from HBM, and what a load
+// instruction touches decides how near they come: one that takes 16 rows by 64 bytes, the
+// layout of the MFMA's operand, streams 4.2 TB/s where one that takes 1 KiB of a row streams
+// 5.9 (67 MB over 512 workgroups; 16 rows of 8 would cost the same again).  So every weight
+// goes straight from memory to the registers of the one wave that uses it, no load takes less
+// than whole 128-byte lines, and the next loads are in flight during the products:
 //
-//   up    workgroup (expert, 16 columns of a): the expert's tokens, compacted, are the
-//         columns; its waves split the contraction over K and add up through LDS.  Leaves
+//   - experts of many tokens by MFMA steps of 16 weight rows by 16 columns, the columns being
+//     the expert's tokens, compacted; loads of 8 rows by 128 bytes and a rotation of 8 lanes
+//     give the operand's layout (RowPair);
+//   - experts of one or two tokens (up to four) by dot products in the lane over 1 KiB blocks
+//     of 8 rows, the lanes' sums added at the end (vec_sum).
+//
+//   up    workgroup (expert, 16 columns of a): its waves split the contraction over K and add
+//         up through LDS, or, by dot products, take 4 columns each.  Leaves
 //         a = w SwiGLU(W1 x + b1), w the token's weight for the expert, in the workspace.
-//   down  workgroup (16 columns of y): its waves share the (expert, piece of F) items of
-//         the whole call, an item's columns being the expert's tokens again; each wave
-//         adds its products to its own sum of every token in LDS, and the waves' sums are
-//         added at the end: no atomics, a fixed order.
+//   down  workgroup (16 or 8 columns of y): its waves share the (expert, piece of F) items of
+//         the whole call; each wave adds its products to its own sum of every token in LDS,
+//         and the waves' sums are added at the end: no atomics, a fixed order.
 //
 // For 16-bit weights a is kept as two values of the weights' type, the rounded value and
-// the rest, each multiplied in its own MFMA step: the products see 16 significant bits
-// of a (22 for fp16) where one value would add its own rounding, of the output's size,
-// to the result.  The extra step is free beside the weight read.
+// the rest, which share a step as two columns: the products see 16 significant bits of a
+// (22 for fp16) where one value would add its own rounding, of the output's size, to the
+// result.
+//
+// Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.83 ms (7.1
+// TB/s of weights), down 1.11 ms (5.9 TB/s: 448 workgroups over 256 CUs); one token, 8 of 64
+// experts of 2048/768: up 12.4 us, down 8.4 us, half of it latency.
 #include <type_traits>
 
 #include "gl_vec.hpp"
 
 namespace gl {
 
-enum { EL_MX = 3 };  // weights: E4M3 codes with an E8M0 scale per 32 of a row
+// Weights as E4M3 codes with an E8M0 scale per 32 of a row; EL_MX: K and F are multiples of
+// 128, so that four scales of a row are an aligned word, EL_MX_RAGGED: of 32.
+enum { EL_MX = 3, EL_MX_RAGGED = 4 };
+constexpr bool is_mx(int wel) { return wel >= EL_MX; }
 constexpr int kMoeMaxTokens = 64;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
 // Units that a wave takes at a time (an MXFP8 unit holds twice the k values).
 template <int WEL>
-constexpr int up_units() { return WEL == EL_MX ? 1 : 2; }
+constexpr int up_units() { return is_mx(WEL) ? 1 : 2; }
 template <int WEL>
-constexpr int down_units() { return WEL == EL_MX ? 2 : 4; }
+constexpr int down_units() { return is_mx(WEL) ? 2 : 4; }
 constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64;
 constexpr int kMoeRows = 16;  // weight rows of a workgroup (per half of W1)
 
@@ -84,60 +98,95 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t moe_rsrc(const void *base) {
                                            0x00020000);
 }
 
+// Weights are read once, whole lines at a time: non-temporal loads (the up kernel at 64
+// tokens, 256 experts of 7168/2048, 13.1 GB: 1.83 ms, 2.04 without).
+__device__ __forceinline__ i32x4_t load_weight(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));
+}
 __device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
-// A unit is 128 bytes of each of the 16 weight rows: lane l holds bytes 16 (l / 16) and
-// 64 + 16 (l / 16) of row l % 16, two loads that together take whole lines.  Its k values
-// are taken in the order that this gives, the same for both operands, in `steps` pieces:
-// piece i contracts the 16 bytes that b_byte(i) names of each token's row.
-template <int WEL>
+// 16 rows of an MFMA operand (weight rows, or the tokens that are its columns), 128 bytes
+// of each: lane (r, q) = (l % 16, l / 16) needs two 16-byte chunks of row r, which the two
+// loads would each take as 16 rows by 64 bytes.  Instead `low` takes rows 0-7 and `high`
+// rows 8-15, whole 128-byte lines, the lanes of r and r + 8 sharing a row, and one rotation
+// of 8 lanes a register gives either chunk to its lane.
+struct RowPair {
+  i32x4_t low, high;
+  // chunk `h` (0 or 1) of the lane's row; the lanes r loaded theirs as chunk r / 8
+  __device__ __forceinline__ i32x4_t chunk(int h) const {
+    i32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // row_ror:8 into the lanes of rows 8-15, or 0-7
+      o[i] = h == 0 ? __builtin_amdgcn_update_dpp(low[i], high[i], 0x128, 0xf, 0xc, false)
+                    : __builtin_amdgcn_update_dpp(high[i], low[i], 0x128, 0xf, 0x3, false);
+    return o;
+  }
+};
+
+// Where the lane's weight rows are: offsets from the first of the workgroup's R rows.
+struct WeightLane {
+  uint32_t row, end_low, end_high, step, chunk;  // step: from row r to r + 8
+  uint32_t srow, send;                           // scales of row l % 16
+  int q;
+  // rows: how many of the 16 there are; wb: bytes of one
+  __device__ WeightLane(int64_t rows, uint32_t wb, int64_t cols) {
+    const int lane = threadIdx.x & 63, r = lane & 15;
+    q = lane >> 4;
+    row = (r & 7) * wb;
+    step = 8 * wb;
+    end_low = (r & 7) < rows ? wb : 0;  // past the last row no byte is valid
+    end_high = (r & 7) + 8 < rows ? wb : 0;
+    chunk = (r >> 3) * 64 + q * 16;
+    srow = r * (uint32_t)(cols / 32);
+    send = r < rows ? wb : 0;
+  }
+};
+
+// A unit is 128 bytes of each of R = 16 or 8 weight rows; its k values are taken in the
+// order that the lanes' chunks give, the same for both operands, in `steps` pieces: piece i
+// contracts the 16 bytes that b_byte(i) names of each token's row.
+template <int WEL, int R>
 struct Unit {  // bf16, fp16 and fp32 weights
   static constexpr int kElems = 128 / elem_bytes(WEL);
   static constexpr int steps = 2;
   static constexpr int b_bytes = 128;  // of a token's row
-  i32x4_t r[2];
+  RowPair r;
   __device__ static uint32_t b_byte(int i, int q) { return i * 64 + q * 16; }
-  // row: byte offset of the lane's row, at: byte within it, end: bytes of a row
-  __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t, uint32_t row, uint32_t at, uint32_t end,
-                       uint32_t, bool, int q) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b = at + i * 64 + q * 16;
-      r[i] = load16(w, b < end ? row + b : kNowhere);
-    }
+  __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t, const WeightLane &o, uint32_t at) {
+    const uint32_t b = at + o.chunk;
+    r.low = load_weight(w, b < o.end_low ? o.row + b : kNowhere);
+    r.high = (i32x4_t){0, 0, 0, 0};
+    if constexpr (R == 16) r.high = load_weight(w, b < o.end_high ? o.row + o.step + b : kNowhere);
   }
-  __device__ i32x4_t operand(int i) const { return r[i]; }
+  __device__ i32x4_t operand(int i) const { return r.chunk(i); }
 };
 
-template <>
-struct Unit<EL_MX> {
+template <int WEL, int R>
+struct CodeUnit {  // MXFP8 weights
   static constexpr int kElems = 128;
   static constexpr int steps = 4;
   static constexpr int b_bytes = 256;
-  i32x4_t r[2];
-  uint32_t s;  // the 4 scales of the unit's codes in the lane's row
+  RowPair r;
+  uint32_t s;  // the 4 scales of the unit's codes in row l % 16
   int q;
   __device__ static uint32_t b_byte(int i, int q) { return (i >> 1) * 128 + q * 32 + (i & 1) * 16; }
-  __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, uint32_t row, uint32_t at, uint32_t end,
-                       uint32_t srow, bool wide, int q_) {
-    q = q_;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t b = at + i * 64 + q * 16;
-      r[i] = load16(w, b < end ? row + b : kNowhere);
-    }
-    // whole units (wide): their 4 scales are an aligned word
-    if (wide) {
-      s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sc, (int)(at < end ? srow + at / 32 : kNowhere), 0, 0);
+  __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, const WeightLane &o, uint32_t at) {
+    q = o.q;
+    const uint32_t b = at + o.chunk;
+    r.low = load_weight(w, b < o.end_low ? o.row + b : kNowhere);
+    r.high = (i32x4_t){0, 0, 0, 0};
+    if constexpr (R == 16) r.high = load_weight(w, b < o.end_high ? o.row + o.step + b : kNowhere);
+    if constexpr (WEL == EL_MX) {
+      s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sc, (int)(at < o.send ? o.srow + at / 32 : kNowhere), 0, 0);
       return;
     }
     s = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t b = at + i * 64 + q * 16;
-      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b8(sc, (int)(b < end ? srow + b / 32 : kNowhere), 0, 0);
+      const uint32_t c = at + i * 64 + q * 16;
+      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b8(sc, (int)(c < o.send ? o.srow + c / 32 : kNowhere), 0, 0);
       s |= (v & 0xff) << (16 * i + 8 * (q >> 1));
     }
   }
@@ -146,15 +195,43 @@ struct Unit<EL_MX> {
   __device__ i32x4_t operand(int i) const {
     const uint32_t byte = (s >> (16 * (i >> 1) + 8 * (q >> 1))) & 0xff;
     const float f = __uint_as_float(byte << 23);
+    const i32x4_t codes = r.chunk(i >> 1);
     i32x4_t o;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int c = r[i >> 1][(i & 1) * 2 + w];
+      const int c = codes[(i & 1) * 2 + w];
       o[2 * w] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, false));
       o[2 * w + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, true));
     }
     return o;
   }
+};
+
+template <int R>
+struct Unit<EL_MX, R> : CodeUnit<EL_MX, R> {};
+template <int R>
+struct Unit<EL_MX_RAGGED, R> : CodeUnit<EL_MX_RAGGED, R> {};
+
+// The tokens' side of U units: pair j holds pieces 2 j and 2 j + 1 of the columns.
+// row_low / row_high: byte offsets of the lane's rows among columns 0-7 and 8-15, each
+// valid up to its end; HIGH: whether columns 8-15 hold any token.  (Decided here and not at
+// run time: a branch around loads makes the compiler wait for those before it.)
+template <class W, int U, bool HIGH>
+struct Columns {
+  RowPair b[U * W::steps / 2];
+  __device__ void load(__amdgpu_buffer_rsrc_t x, uint32_t row_low, uint32_t end_low, uint32_t row_high,
+                       uint32_t end_high, const uint32_t *unit_at) {
+    const int lane = threadIdx.x & 63, h = (lane >> 3) & 1, q = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < U * W::steps / 2; ++j) {
+      const int i = (2 * j) % W::steps;  // piece of the unit
+      const uint32_t at = unit_at[2 * j / W::steps] + (h ? W::b_byte(i + 1, q) : W::b_byte(i, q));
+      b[j].low = load16(x, at < end_low ? row_low + at : kNowhere);
+      b[j].high = (i32x4_t){0, 0, 0, 0};
+      if constexpr (HIGH) b[j].high = load16(x, at < end_high ? row_high + at : kNowhere);
+    }
+  }
+  __device__ i32x4_t operand(int piece) const { return b[piece / 2].chunk(piece & 1); }
 };
 
 // acc[weight row][column] += A B over the k values of one 16-byte piece of each lane
@@ -187,7 +264,7 @@ __device__ __forceinline__ float bias_at(const MoeWeight &m, int e, int64_t r) {
 }
 
 template <int WEL>
-__device__ __forceinline__ int64_t row_bytes(int64_t cols) { return WEL == EL_MX ? cols : cols * elem_bytes(WEL); }
+__device__ __forceinline__ int64_t row_bytes(int64_t cols) { return is_mx(WEL) ? cols : cols * elem_bytes(WEL); }
 
 // First row r of expert e's matrix, and of its scales.
 template <int WEL>
@@ -208,30 +285,26 @@ struct UpTokens {
 };
 
 // ------------------------------------------------------------------ few columns --
-// Few tokens of an expert go without MFMA.  The A operand's layout makes a
-// load touch 16 rows, 64 bytes each; the same loads taking 1 KiB of one row at a time
-// stream half as fast again (67 MB over 512 workgroups: 15.9 and 11.1 us).  So a wave
-// takes 1 KiB blocks of 8 rows, with 16 bytes of each row in a lane, the tokens' values
-// of the same places beside them, and dot products in the lane; the lanes' sums are added
-// at the end of a row.
+// One wave takes 1 KiB blocks of 8 rows, 16 bytes of each row in a lane, and the tokens'
+// values of the same places beside them.
 constexpr int kVecRows = 8;
 
 template <int WEL>
-constexpr int block_elems() { return WEL == EL_MX ? 1024 : 1024 / elem_bytes(WEL); }
+constexpr int block_elems() { return is_mx(WEL) ? 1024 : 1024 / elem_bytes(WEL); }
 
 // The lane's 16 bytes of each of 8 rows.
 template <int WEL>
 struct VecRows {
   i32x4_t r[kVecRows];
-  uint8_t s[WEL == EL_MX ? kVecRows : 1];
+  uint8_t s[is_mx(WEL) ? kVecRows : 1];
   // row byte offsets from the resource's base are i * wb; a row not < rows is not read
   __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, int first, int n, uint32_t at, uint32_t wb,
                        int rows) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const bool ok = at < wb && i < rows;
-      r[first + i] = load16(w, ok ? i * wb + at : kNowhere);
-      if constexpr (WEL == EL_MX)
+      r[first + i] = load_weight(w, ok ? i * wb + at : kNowhere);
+      if constexpr (is_mx(WEL))
         s[first + i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sc, (int)(ok ? (i * wb + at) / 32 : kNowhere), 0, 0);
     }
   }
@@ -241,7 +314,7 @@ struct VecRows {
 // activations' type, or 32 beside MXFP8 codes.
 template <int WEL>
 struct VecToken {
-  static constexpr int parts = WEL == EL_MX ? 2 : 1;
+  static constexpr int parts = is_mx(WEL) ? 2 : 1;
   i32x4_t v[parts];
   __device__ void load(__amdgpu_buffer_rsrc_t x, uint32_t row, uint32_t at, uint32_t xb) {
 #pragma unroll
@@ -266,7 +339,7 @@ template <int EL, int WEL, int NV, int P>
 __device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<WEL> (*x)[P], int n, float (*acc)[NV]) {
 #pragma unroll
   for (int r = 0; r < kVecRows; ++r) {
-    if constexpr (WEL == EL_MX) {
+    if constexpr (is_mx(WEL)) {
       const float f = __uint_as_float((uint32_t)w.s[r] << 23);
       int q[8];  // 16 codes as bf16 pairs, exact there
 #pragma unroll
@@ -360,8 +433,8 @@ struct UpRows {
     n = (int)(p.F - f < 4 ? p.F - f : 4);
     wg = moe_rsrc(weight_row<WEL>(p.w1, e, f));
     wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f));
-    sg = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, f) : nullptr);
-    su = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, p.F + f) : nullptr);
+    sg = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, f) : nullptr);
+    su = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, p.F + f) : nullptr);
   }
   __device__ void load(VecRows<WEL> &w, int block) const {
     const uint32_t at = (block * 64 + (threadIdx.x & 63)) * 16;
@@ -417,90 +490,66 @@ __device__ __forceinline__ void up_vector(const MoeParams &p, const UpTokens &to
 }
 
 // ----------------------------------------------------------------- many columns --
-// The weight side of the up kernel: units wave, wave + kUpWaves, ... of the gate's and the
-// up's 16 rows, U of each at a time.
-template <int WEL>
-struct UpWeights {
-  static constexpr int U = up_units<WEL>();
-  using W = Unit<WEL>;
-  __amdgpu_buffer_rsrc_t wg, wu, sg, su;
-  uint32_t row, srow, end;
-  int q;
-  bool wide;
-  __device__ UpWeights(const MoeParams &p, int e, int64_t f0) {
-    const int col = threadIdx.x & 15;
-    const uint32_t wb = (uint32_t)row_bytes<WEL>(p.K);
-    wg = moe_rsrc(weight_row<WEL>(p.w1, e, f0));
-    wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f0));
-    sg = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, f0) : nullptr);
-    su = moe_rsrc(WEL == EL_MX ? scale_row(p.w1, e, p.F + f0) : nullptr);
-    q = (threadIdx.x >> 4) & 3;
-    row = col * wb;
-    wide = p.K % 128 == 0;
-    srow = col * (uint32_t)(p.K / 32);
-    end = f0 + col < p.F ? wb : 0;  // past the last row: no byte is valid
-  }
+// Contraction over K for up to NT tiles of 16 columns (HIGH false: one of 8): wave w takes units w, w + kUpWaves,
+// ... of the gate's and the up's 16 rows, U of each at a time.
+template <int EL, int WEL, int NT, bool HIGH>
+__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
+  using W = Unit<WEL, kMoeRows>;
+  constexpr int U = up_units<WEL>();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = tok.expert;
+  const WeightLane rows(p.F - f0, (uint32_t)row_bytes<WEL>(p.K), p.K);
+  const auto wg = moe_rsrc(weight_row<WEL>(p.w1, e, f0)), wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f0));
+  const auto sg = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, f0) : nullptr);
+  const auto su = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, p.F + f0) : nullptr);
   // units past the end load zeros
-  __device__ void load(W *g, W *u, int c0) const {
+  const auto load = [&](W *g, W *u, int c0) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t at = (uint32_t)(c0 + i * kUpWaves) * 128;
-      g[i].load(wg, sg, row, at, end, srow, wide, q);
-      u[i].load(wu, su, row, at, end, srow, wide, q);
+      g[i].load(wg, sg, rows, at);
+      u[i].load(wu, su, rows, at);
     }
-  }
-};
-
-// Contraction over K for up to NT tiles of 16 columns.
-template <int EL, int WEL, int NT>
-__device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
-  using W = Unit<WEL>;
-  constexpr int U = up_units<WEL>();
-  const UpWeights<WEL> weights(p, tok.expert, f0);
-  W g[U], u[U];
-  weights.load(g, u, threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
+  };
+  W g[U], u[U], ng[U], nu[U];
+  load(g, u, wave);
   const uint32_t xb = (uint32_t)(p.K * elem_bytes(EL));
   const auto xr = moe_rsrc(p.x);
-  uint32_t xrow[NT], xend[NT];
+  uint32_t xrow[NT][2], xend[NT][2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + col;
-    xend[t] = c < tok.n ? xb : 0;
-    xrow[t] = c < tok.n ? (uint32_t)(tok.slot[c] / p.k) * xb : 0;
-  }
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = t * 16 + h * 8 + (lane & 7);
+      xend[t][h] = c < tok.n ? xb : 0;
+      xrow[t][h] = c < tok.n ? (uint32_t)(tok.slot[c] / p.k) * xb : 0;
+    }
   f32x4_t ag[NT], au[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) ag[t] = au[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   const int units = (int)((p.K + W::kElems - 1) / W::kElems);
   const auto step = [&](int c0, const W *g, const W *u, W *ng, W *nu) {
+    uint32_t at[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) at[i] = (uint32_t)(c0 + i * kUpWaves) * W::b_bytes;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (t && t * 16 >= tok.n) break;
       // the tokens' pieces come from cache, the next weights from memory: issued in this
       // order, the products wait for the former alone
-      i32x4_t b[U][W::steps];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int s = 0; s < W::steps; ++s) {
-          const uint32_t at = (uint32_t)(c0 + i * kUpWaves) * W::b_bytes + W::b_byte(s, q);
-          b[i][s] = load16(xr, at < xend[t] ? xrow[t] + at : kNowhere);
-        }
-      if (t == 0) weights.load(ng, nu, c0 + kUpWaves * U);
+      Columns<W, U, HIGH> b;
+      b.load(xr, xrow[t][0], xend[t][0], xrow[t][1], xend[t][1], at);
+      if (t == 0) load(ng, nu, c0 + kUpWaves * U);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int s = 0; s < W::steps; ++s) {
-          ag[t] = mma<EL>(g[i].operand(s), b[i][s], ag[t]);
-          au[t] = mma<EL>(u[i].operand(s), b[i][s], au[t]);
-        }
+      for (int i = 0; i < U * W::steps; ++i) {
+        const i32x4_t x = b.operand(i);
+        ag[t] = mma<EL>(g[i / W::steps].operand(i % W::steps), x, ag[t]);
+        au[t] = mma<EL>(u[i / W::steps].operand(i % W::steps), x, au[t]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   // two register sets in turn: copying one to the other would wait for its loads
-  W ng[U], nu[U];
   for (int c0 = wave; c0 < units; c0 += 2 * kUpWaves * U) {
     step(c0, g, u, ng, nu);
     if (c0 + kUpWaves * U >= units) break;
@@ -517,7 +566,8 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
 // a of the workgroup's 16 columns for all of the expert's tokens.
 template <int EL, int WEL, int NT>
 __device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
-  up_product<EL, WEL, NT>(p, tok, f0, sums);
+  if (tok.n <= 8) up_product<EL, WEL, 1, false>(p, tok, f0, sums);
+  else up_product<EL, WEL, NT, true>(p, tok, f0, sums);
   __syncthreads();
   const int f = threadIdx.x & 15;
   if (f0 + f >= p.F) return;
@@ -650,7 +700,7 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
         for (int d = 0; d < parts; ++d) x[k][d].load(ar, row + d * plane, (b * 64 + lane) * kX, ab);
       }
     const int64_t r0 = o.n0 + h * 8;
-    w.load(moe_rsrc(weight_row<WEL>(p.w2, e, r0)), moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, r0) : nullptr), 0, 8,
+    w.load(moe_rsrc(weight_row<WEL>(p.w2, e, r0)), moe_rsrc(is_mx(WEL) ? scale_row(p.w2, e, r0) : nullptr), 0, 8,
            (uint32_t)(b * 64 + lane) * 16, wb, (int)min64(p.N - r0, 8));
   };
   const auto step = [&](const VecRows<WEL> &w, const VecToken<WEL> (*x)[parts], VecRows<WEL> &nw,
@@ -693,25 +743,22 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
 // the entry's tokens in MFMA steps.
 template <int EL, int WEL, int R>
 __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o) {
-  using W = Unit<WEL>;
+  using W = Unit<WEL, R>;
   constexpr int U = down_units<WEL>();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const auto entry = [&](int i) { return o.ent[p.n_entries - 1 - i]; };
-  const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = (uint32_t)(p.F * elem_bytes(EL));
-  const uint32_t end = col < R && o.n0 + col < p.N ? wb : 0;
-  const uint32_t row = col * wb, srow = col * (uint32_t)(p.F / 32);
-  const bool wide = p.F % 128 == 0;
+  const uint32_t ab = (uint32_t)(p.F * elem_bytes(EL));
+  const WeightLane rows(min64(p.N - o.n0, R), (uint32_t)row_bytes<WEL>(p.F), p.F);
   const auto ar = moe_rsrc(p.a);
   constexpr int kCols = EL == EL_F32 ? 16 : 8;  // tokens of a step
-  const int token = col & (kCols - 1);
-  const uint32_t part = col < kCols ? 0 : (uint32_t)(p.T * p.k) * ab;  // the second parts' plane
+  const uint32_t plane = (uint32_t)(p.T * p.k) * ab;  // from a's first parts to the second
   const int pieces = (int)((p.F + W::kElems * U - 1) / (W::kElems * U));
   const auto load = [&](W *w, int i, int c) {
     const int e = __builtin_amdgcn_readfirstlane(entry(i).expert);
     const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, o.n0));
-    const auto s = moe_rsrc(WEL == EL_MX ? scale_row(p.w2, e, o.n0) : nullptr);
+    const auto s = moe_rsrc(is_mx(WEL) ? scale_row(p.w2, e, o.n0) : nullptr);
 #pragma unroll
-    for (int j = 0; j < U; ++j) w[j].load(r, s, row, (c * U + j) * 128, end, srow, wide, q);
+    for (int j = 0; j < U; ++j) w[j].load(r, s, rows, (c * U + j) * 128);
   };
   int i = wave / pieces, c = wave - i * pieces;
   // one item with its weights in `cur`; moves on to the next, whose weights go to `nxt`
@@ -722,28 +769,27 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
       ++ni;
     }
     const int base = __builtin_amdgcn_readfirstlane(entry(i).base), m = __builtin_amdgcn_readfirstlane(entry(i).n);
+    uint32_t at[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) at[j] = (c * U + j) * W::b_bytes;
     // the entry's tokens as columns; a 16-bit a's two parts are columns of the same step
     for (int t = 0; t < m; t += kCols) {
-      const bool on = t + token < m;
-      const int slot = on ? o.slots[base + t + token] : 0;
-      const uint32_t arow = (uint32_t)slot * ab + part, aend = on ? ab : 0;
-      i32x4_t b[U * W::steps];
-#pragma unroll
-      for (int s = 0; s < U * W::steps; ++s) {
-        const uint32_t at = (c * U + s / W::steps) * W::b_bytes + W::b_byte(s % W::steps, q);
-        b[s] = load16(ar, at < aend ? arow + at : kNowhere);
-      }
+      const int lo = t + (lane & 7), hi = kCols == 16 ? lo + 8 : lo;
+      const uint32_t row_lo = lo < m ? (uint32_t)o.slots[base + lo] * ab : 0;
+      const uint32_t row_hi = kCols == 8 ? row_lo + plane : hi < m ? (uint32_t)o.slots[base + hi] * ab : 0;
+      Columns<W, U, true> b;
+      b.load(ar, row_lo, lo < m ? ab : 0, row_hi, hi < m ? ab : 0, at);
       if (t == 0 && ni < o.n_many) load(nxt, ni, nc);
       __builtin_amdgcn_sched_barrier(0);
       f32x4_t sum = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < U * W::steps; ++s) sum = mma<EL>(cur[s / W::steps].operand(s % W::steps), b[s], sum);
+      for (int s = 0; s < U * W::steps; ++s) sum = mma<EL>(cur[s / W::steps].operand(s % W::steps), b.operand(s), sum);
       if constexpr (kCols == 8)
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[r] += __shfl_xor(sum[r], 8);
-      if (on && col == token) {  // each column another token: no lane shares a sum
-        f32x4_t *at = (f32x4_t *)(o.acc + (wave * p.T + slot / p.k) * 16 + q * 4);
-        *at += sum;
+      if (col < kCols && t + col < m) {  // each column another token: no lane shares a sum
+        f32x4_t *to = (f32x4_t *)(o.acc + (wave * p.T + o.slots[base + t + col] / p.k) * 16 + q * 4);
+        *to += sum;
       }
     }
     i = ni;
@@ -847,14 +893,18 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
   using Four = integral_constant<int, 4>;
-  // Experts of one or two tokens by dot products up to 16 tokens (8 tokens over 32 experts of
-  // 4096/2048: bf16 124 us, without 130; MXFP8 74 and 85); beyond, MFMA alone, whose fewer
-  // registers keep more loads in flight (32 tokens: MXFP8 132 us, with dot products 134).
+  // Dot products where the whole call has as few tokens: up to four of 16-bit or fp32 weights
+  // in the up kernel (4 tokens over 8 experts of 4096/8192: 127 us, by MFMA 136), two
+  // otherwise (down kernel, 2 tokens there: 63 us, by MFMA 85).  In larger calls only beside
+  // MXFP8 codes, for the experts of one or two tokens, where the MFMA's columns would load
+  // 256 bytes of activations for every 128 of codes (8 tokens over 32 experts of 4096/2048:
+  // up 72 us, all by MFMA 81, down 40 and 50; bf16 does as well by MFMA, 116 and 117 us).
+  using Few = integral_constant<int, is_mx(WEL) ? 2 : 0>;
   if (p.T == 1) go_up(One(), Zero());
   else if (p.T == 2) go_up(Two(), Zero());
-  else if (p.T <= 4) go_up(Four(), Zero());
-  else if (p.T <= 16) go_up(Two(), One());
-  else go_up(Zero(), Four());
+  else if (p.T <= 4 && !is_mx(WEL)) go_up(integral_constant<int, is_mx(WEL) ? 2 : 4>(), Zero());
+  else if (p.T <= 16) go_up(Few(), One());
+  else go_up(Few(), Four());
 
   // LDS: at most 4 KiB of sums a wave, 24 KiB of entries and 4 KiB of slots
   const size_t lds = (size_t)kDownWaves * p.T * 64 + (size_t)p.n_entries * sizeof(DownEntry) + (size_t)p.T * p.k * 2;
@@ -862,18 +912,12 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
     hipLaunchKernelGGL((moe_down_kernel<EL, WEL, r(), nv(), many()>), dim3((unsigned)((p.N + r() - 1) / r())),
                        dim3(kDownThreads), lds, s, p);
   };
-  // Rows of a workgroup: 16, or 8 where 16 would leave CUs without one.  With 16 rows the
-  // MFMA steps of 16-bit weights do as well for one token as dot products (5 tokens fp16, 8
-  // experts of 14336: 140 us, with dot products 152); with 8 rows half of their operand is
-  // empty (8 tokens over 64 experts of 768: 24.2 us, with dot products 20.5), and beside
-  // MXFP8 codes they load twice the activations (17 tokens over 32 experts of 2048: 52 us,
-  // with dot products 46.6).
+  // Rows of a workgroup: 16, or 8 where 16 would leave CUs without one (one token, 8 experts
+  // of 768 into 2048: 9.3 us, with 16 rows 10.6)
   const auto by_tokens = [&](auto r) {
-    constexpr bool half = decltype(r)() == 8;
     if (p.T == 1) go_down(r, One(), std::false_type());
     else if (p.T == 2) go_down(r, Two(), std::false_type());
-    else if (WEL == EL_MX || (half && p.T <= 16)) go_down(r, integral_constant<int, WEL == EL_MX || half ? 2 : 0>(), std::true_type());
-    else go_down(r, Zero(), std::true_type());
+    else go_down(r, Few(), std::true_type());
   };
   if (p.N / 16 < 256) by_tokens(integral_constant<int, 8>());
   else by_tokens(integral_constant<int, 16>());
@@ -905,7 +949,8 @@ hipError_t launch_moe(int el, bool mx, int E, int64_t K, int64_t F, int64_t N, i
   p.entries = (MoeEntry *)ws;
   p.slot_of = (int16_t *)(p.entries + p.n_entries);
   p.a = (char *)ws + moe_table_bytes(p.n_entries);
-  if (mx) launch_moe_typed<EL_BF16, EL_MX>(p, s);
+  if (mx && K % 128 == 0 && F % 128 == 0) launch_moe_typed<EL_BF16, EL_MX>(p, s);
+  else if (mx) launch_moe_typed<EL_BF16, EL_MX_RAGGED>(p, s);
   else if (el == EL_F32) launch_moe_typed<EL_F32, EL_F32>(p, s);
   else if (el == EL_F16) launch_moe_typed<EL_F16, EL_F16>(p, s);
   else launch_moe_typed<EL_BF16, EL_BF16>(p, s);

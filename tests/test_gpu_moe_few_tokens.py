@@ -121,7 +121,9 @@ def test_forward_wide(T, E, k, K, F, N, dtype):
 
 
 @pytest.mark.parametrize("T,E,k,K,F,N", [(1, 5, 3, 2080, 1120, 4104), (2, 4, 2, 1056, 2176, 4096), (4, 6, 2, 1152, 224, 4104),
-                                         (9, 5, 2, 544, 1088, 4200), (40, 6, 2, 128, 256, 4104)])
+                                         (9, 5, 2, 544, 1088, 4200), (40, 6, 2, 128, 256, 4104),
+                                         (1, 5, 3, 2048, 1152, 4104), (2, 4, 2, 1280, 2048, 80), (5, 9, 2, 512, 1152, 4104),
+                                         (12, 3, 2, 384, 128, 72), (30, 4, 2, 1152, 384, 4096), (64, 3, 3, 256, 128, 40)])
 def test_mxfp8_weights_wide(T, E, k, K, F, N):
     c = case(T * 7 + E, T, E, k, K, F, N, BF16, mx=True, bias=T % 2 == 0, residual=T % 3 == 1)
     check(c, run(c))
