@@ -547,18 +547,23 @@ def gl_wgrad_mxfp8(dy_t: Tensor, dy_t_scale: Tensor, x_t: Tensor, x_t_scale: Ten
 # -------------------------------------------------------------------- expert block
 
 
-def _on_one_device(first: Tensor, *others) -> None:
-    """Every given tensor (lists of them too) is on ``first``'s GPU."""
+def _addresses(first: Tensor, *others: Optional[Tensor]):
+    """Addresses of ``first`` and of the others (None for None), which must be contiguous and
+    on ``first``'s GPU."""
     dev = first.get_device()
     if dev < 0:
         raise ValueError("tensors must be on the GPU")
-    for t in others:
+    out = []
+    for t in (first, *others):
         if t is None:
+            out.append(None)
             continue
-        if not isinstance(t, Tensor):
-            _on_one_device(first, *t)
-        elif t.get_device() != dev:
+        if t.get_device() != dev:
             raise ValueError(f"tensors must be on one device (got {first.device} and {t.device})")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the library must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _enough(workspace: Optional[Tensor], size: int) -> None:
@@ -582,9 +587,8 @@ def gl_rmsnorm_forward(x: Tensor, gamma: Tensor, eps: float, *, residual: Option
         raise ValueError("data must be uint8 [T, C]")
     if scale is not None and (scale.shape != (T, C // 32) or scale.dtype != torch.uint8):
         raise ValueError("scale must be uint8 [T, C/32]")
-    _on_one_device(x, gamma, residual, h, y, data, scale)
-    _check(load().gl_rmsnorm_forward(T, C, _dtype(x), _dtype(gamma), _ptr(x), _ptr(residual), _ptr(gamma), eps,
-                                     _ptr(h), _ptr(y), _ptr(data), _ptr(scale), _stream(stream)))
+    px, pr, pg, ph, py, pd, ps = _addresses(x, residual, gamma, h, y, data, scale)
+    _check(load().gl_rmsnorm_forward(T, C, _dtype(x), _dtype(gamma), px, pr, pg, eps, ph, py, pd, ps, _stream(stream)))
 
 
 def gl_rmsnorm_workspace_size(total_rows: int, features: int) -> int:
@@ -608,10 +612,10 @@ def gl_rmsnorm_backward(dy: Tensor, h: Tensor, gamma: Tensor, eps: float, dx: Te
         if dgamma.shape != (C,):
             raise ValueError("dgamma must be [C]")
         _enough(workspace, gl_rmsnorm_workspace_size(T, C))
-    _on_one_device(h, dy, gamma, dx, dh, dgamma, workspace)
-    _check(load().gl_rmsnorm_backward(T, C, _dtype(h), _dtype(gamma), _ptr(dy), _ptr(dh), _ptr(h), _ptr(gamma), eps,
-                                      _ptr(dx), GL_F32 if dgamma is None else _dtype(dgamma), _ptr(dgamma),
-                                      int(bool(accumulate)), _ptr(workspace), _stream(stream)))
+    ph, py, pd, pg, px, pw, ws = _addresses(h, dy, dh, gamma, dx, dgamma, workspace)
+    _check(load().gl_rmsnorm_backward(T, C, _dtype(h), _dtype(gamma), py, pd, ph, pg, eps, px,
+                                      GL_F32 if dgamma is None else _dtype(dgamma), pw, int(bool(accumulate)), ws,
+                                      _stream(stream)))
     return dx
 
 
@@ -646,10 +650,8 @@ def gl_route_forward(logits: Tensor, ids: Tensor, weights: Tensor, *, score: int
         if row_index.dtype != torch.int32 or slot_index.dtype != torch.int32:
             raise ValueError("row_index and slot_index must be int32")
         _enough(workspace, gl_route_workspace_size(T, E))
-    _on_one_device(logits, ids, weights, m_splits, row_index, slot_index, workspace)
-    _check(load().gl_route_forward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), _ptr(logits),
-                                   _ptr(ids), _ptr(weights), _ptr(m_splits), _ptr(row_index), _ptr(slot_index),
-                                   _ptr(workspace), _stream(stream)))
+    at = _addresses(logits, ids, weights, m_splits, row_index, slot_index, workspace)
+    _check(load().gl_route_forward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), *at, _stream(stream)))
     return ids, weights
 
 
@@ -659,9 +661,8 @@ def gl_route_backward(logits: Tensor, ids: Tensor, dweights: Tensor, dlogits: Te
     T, E, k = _route_args(logits, ids, dweights)
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must have the shape and dtype of logits")
-    _on_one_device(logits, ids, dweights, dlogits)
-    _check(load().gl_route_backward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), _ptr(logits),
-                                    _ptr(ids), _ptr(dweights), _ptr(dlogits), _stream(stream)))
+    at = _addresses(logits, ids, dweights, dlogits)
+    _check(load().gl_route_backward(T, E, k, _dtype(logits), int(score), int(bool(renormalize)), *at, _stream(stream)))
     return dlogits
 
 
@@ -711,16 +712,19 @@ def gl_moe_few_tokens(x: Tensor, ids: Tensor, weights: Tensor, w1: Grouped, w2: 
     _each_shape(b1, E, (F2,), x.dtype, "b1")
     _each_shape(b2, E, (N,), x.dtype, "b2")
     _enough(workspace, gl_moe_few_tokens_workspace_size(T, k, E, F))
-    _on_one_device(x, ids, weights, w1, w2, y, workspace, w1_scale, w2_scale, b1, b2, residual)
+    px, pi, pw, pr, py, ws = _addresses(x, ids, weights, residual, y, workspace)
+    for g in (w1, w2, w1_scale, w2_scale, b1, b2):
+        if g is not None:
+            _addresses(x, *((g,) if isinstance(g, Tensor) else g))
     p1, pp1, k1 = _grouped(w1, x.device, stream)
     p2, pp2, k2 = _grouped(w2, x.device, stream)
     s1, ss1, k3 = _grouped(w1_scale, x.device, stream)
     s2, ss2, k4 = _grouped(w2_scale, x.device, stream)
     q1, qq1, k5 = _grouped(b1, x.device, stream)
     q2, qq2, k6 = _grouped(b2, x.device, stream)
-    _check(load().gl_moe_few_tokens(E, K, F, N, T, k, _dtype(x), _DT[wd] if wd in _DT else -1, _ptr(x), _ptr(ids),
-                                    _ptr(weights), p1, pp1, s1, ss1, q1, qq1, p2, pp2, s2, ss2, q2, qq2,
-                                    _ptr(residual), _ptr(y), y.shape[0], _ptr(workspace), _stream(stream)))
+    _check(load().gl_moe_few_tokens(E, K, F, N, T, k, _dtype(x), _DT[wd] if wd in _DT else -1, px, pi, pw, p1, pp1,
+                                    s1, ss1, q1, qq1, p2, pp2, s2, ss2, q2, qq2, pr, py, y.shape[0], ws,
+                                    _stream(stream)))
     del k1, k2, k3, k4, k5, k6
     return y
 

@@ -31,6 +31,11 @@ def _masked(l):
     return np.minimum(np.where(np.isnan(l), -np.inf, l), float(np.finfo(np.float32).max))
 
 
+def _sigmoid(l):
+    with np.errstate(over="ignore"):
+        return 1 / (1 + np.exp(-l))
+
+
 def route(logits, top_k, sigmoid=False, renormalize=True):
     """(ids, weights) of every token: the largest logits, ties to the lowest expert, NaN
     as -inf, +inf as the largest finite value; a masked (-inf) expert weighs 0."""
@@ -43,7 +48,7 @@ def route(logits, top_k, sigmoid=False, renormalize=True):
         scores = np.zeros(E)
         live = l > -np.inf
         if sigmoid:
-            scores[live] = 1 / (1 + np.exp(-l[live]))
+            scores[live] = _sigmoid(l[live])
         elif live.any():
             scores[live] = np.exp(l[live] - l[live].max())
             scores /= scores.sum()
@@ -77,7 +82,7 @@ def route_backward(logits, ids, dweights, sigmoid=False, renormalize=True):
         c = np.asarray(ids[t], np.int64)
         s, d = np.zeros(c.size), np.asarray(dweights[t], np.float64)
         if sigmoid:
-            s[live[c]] = 1 / (1 + np.exp(-l[c][live[c]]))
+            s[live[c]] = _sigmoid(l[c][live[c]])
             if renormalize and s.sum() > 0:  # w = s / sum(s)
                 d = (d - d @ s / s.sum()) / s.sum()
             out[t, c] = d * s * (1 - s)

@@ -162,6 +162,34 @@ def test_only_the_rows_are_written_and_no_rows_is_fine():
     assert (dg == 0).all()
 
 
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows against the oracle, forward and backward."""
+    T, C = 70001, 65536
+    x = torch.zeros(T, C, dtype=BF16, device=DEV)  # 9.2 GB
+    g = torch.Generator().manual_seed(3)
+    last, gam, dy = torch.randn(2, C, generator=g).to(BF16), torch.randn(C, generator=g).to(BF16), torch.randn(2, C, generator=g).to(BF16)
+    x[-2:] = last.to(DEV)
+    y = torch.empty_like(x)
+    data = torch.empty(T, C, dtype=torch.uint8, device=DEV)
+    scale = torch.empty(T, C // 32, dtype=torch.uint8, device=DEV)
+    gl.gl_rmsnorm_forward(x, gam.to(DEV), EPS, y=y, data=data, scale=scale)
+    ref = eb.rmsnorm(to64(last), to64(gam), EPS)[1]
+    check_y(y[-2:], None, ref, BF16, C, "last rows")
+    assert (y[:-2] == 0).all() and not (data[:-2] & 0x7F).any()
+    deq = oracle.dequantize_mxfp8(data[-2:].cpu().numpy(), scale[-2:].cpu().numpy())
+    assert np.linalg.norm(deq - ref) < 2.0 ** -4 * np.linalg.norm(ref)
+    del data, scale
+    y.zero_()
+    y[-2:] = dy.to(DEV)
+    dg = torch.empty(C, device=DEV)
+    ws = torch.empty(gl.gl_rmsnorm_workspace_size(T, C), dtype=torch.uint8, device=DEV)
+    gl.gl_rmsnorm_backward(y, x, gam.to(DEV), EPS, y, dgamma=dg, workspace=ws)  # in place of dy
+    dx64, dg64 = eb.rmsnorm_backward(to64(dy), to64(last), to64(gam), EPS)
+    assert (y[:-2] == 0).all()
+    assert np.linalg.norm(to64(y[-2:]) - dx64) < 2.0 ** -8 * np.linalg.norm(dx64)
+    assert np.linalg.norm(to64(dg) - dg64) < 1e-5 * np.linalg.norm(dg64)
+
+
 def check_backward(T, C, dtype, gdtype, with_dh):
     _, h, gam, dy, dh = inputs(T * 17 + C, T, C, dtype, gdtype)
     ws = torch.empty(gl.gl_rmsnorm_workspace_size(T, C), dtype=torch.uint8, device=DEV)

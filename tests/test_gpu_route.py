@@ -112,6 +112,27 @@ def test_many_tokens_match_a_stable_sort():
         assert torch.equal(got["m_splits"], torch.bincount(flat, minlength=E))
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens' gates, the counts, and the gradient's last rows."""
+    T, E = 2200003, 1000
+    l = torch.zeros(T, E, dtype=BF16, device=DEV)  # 4.4 GB
+    tail = logits_of(6, 70, E, BF16, False)
+    l[-70:] = tail.to(DEV)
+    got = forward(l, 2, False, False)
+    ids, w = eb.route(to64(tail), 2, False, False)
+    assert np.array_equal(got["ids"][-70:].cpu().numpy(), ids)
+    assert np.allclose(to64(got["weights"][-70:]), w, rtol=1e-5)
+    counts = torch.bincount(got["ids"].reshape(-1).long(), minlength=E)
+    assert torch.equal(got["m_splits"], counts) and counts[0] >= T - 70
+    assert torch.equal(got["slot_index"][got["row_index"].reshape(-1).long()].long(), torch.arange(2 * T, device=DEV))
+    dl = torch.empty_like(l)
+    dw = torch.ones(T, 2, device=DEV)
+    dw[:, 1] = -2
+    gl.gl_route_backward(l, got["ids"], dw, dl, renormalize=False)
+    ref = eb.route_backward(to64(tail), ids, np.tile([1.0, -2.0], (70, 1)), False, False)
+    assert np.linalg.norm(to64(dl[-70:]) - ref) < 2.0 ** -8 * np.linalg.norm(ref)
+
+
 def test_plan_feeds_the_offsets():
     l = logits_of(4, 300, 12, F32, False).to(DEV)
     got = forward(l, 3, False, True)
