@@ -8,16 +8,16 @@
 // chosen scores divided by their sum (for softmax: a softmax over the chosen logits).
 // A token whose experts are all masked gets weights 0.
 //
-// 32768 tokens over 256 experts, bf16, top 8: gates 14.6 us, scan 4.6, rows 5.3 (21 MB in
-// all); 32 tokens over 64 experts with their plan, one launch, 4.2 us; the gradient of
-// 16384 x 64 fp32 4.9 us.
+// 32768 tokens over 256 experts, bf16, top 8: gates 14.0 us, scan 4.2, rows 5.6 (21 MB in
+// all); 32 tokens over 64 experts with their plan, one launch, 4.0 us; the gradient of
+// 16384 x 64 fp32 5.0 us.
 #include <type_traits>
 
 #include "gl_vec.hpp"
 
 namespace gl {
 
-constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTopK = 32;
 constexpr int kChunk = 64;  // tokens of a workgroup: one bit each of a 64-bit mask
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 
@@ -80,10 +80,10 @@ __device__ __forceinline__ uint32_t row_min(uint32_t v) {
 }
 
 // The lane's experts as keys in the order of choice, and a round of it: the row's best
-// expert still there, which its lane drops.  No key but a missing expert's is 0.
+// expert still there.  No key but a missing expert's is 0.
 template <int EL, int LPR, int PER>
 struct Choices {
-  uint32_t key[PER];
+  uint32_t key[PER], last = 0;
   int e0;
   __device__ Choices(const float *l, int e0_, int E) : e0(e0_) {
 #pragma unroll
@@ -103,20 +103,27 @@ struct Choices {
   // every lane of the row gets the choice's key and expert
   __device__ void next(uint32_t &m, int &e) {
     uint32_t best = 0;
+    if constexpr (EL == EL_F32) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) best = key[i] > best ? key[i] : best;
-    m = row_max<LPR>(best);
-    if constexpr (EL == EL_F32) {  // the lowest expert of that key
-      uint32_t at = 0xffffffffu;
+      for (int i = 0; i < PER; ++i) best = key[i] > best ? key[i] : best;
+      m = row_max<LPR>(best);
+      uint32_t at = 0xffffffffu;  // the lowest expert of that key
 #pragma unroll
       for (int i = PER - 1; i >= 0; --i) at = key[i] == m ? e0 + i : at;
       e = (int)row_min<LPR>(at);
 #pragma unroll
       for (int i = 0; i < PER; ++i) key[i] = e == e0 + i ? 0 : key[i];
     } else {
-      e = 0xffff - (int)(m & 0xffff);
+      // the keys differ, so the next is the largest below the last: modulo 2^32 the keys
+      // below it are the ones of the largest differences to it (at first, to 0, all are)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = key[i] == m ? 0 : key[i];
+      for (int i = 0; i < PER; ++i) {
+        const uint32_t d = key[i] - last;
+        best = d > best ? d : best;
+      }
+      m = last + row_max<LPR>(best);
+      last = m;
+      e = 0xffff - (int)(m & 0xffff);
     }
   }
   // the logit of a choice's key
@@ -203,18 +210,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, pos = lane % LPR;
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   const int e0 = pos * PER, k = p.k;
-  if (p.m_splits) {
+  constexpr int kRounds = kChunk / (kRouteWaves * R::rows);
+  int id[kRounds][H];  // the row's lane j keeps choices j and, of 16 lanes, 16 + j; -1: none
+  if (p.m_splits)
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = 0;
-    __syncthreads();
-  }
-  for (int r = wave * R::rows + sub; r < kChunk; r += kRouteWaves * R::rows) {
+#pragma unroll
+  for (int round = 0; round < kRounds; ++round) {
+    const int r = (round * kRouteWaves + wave) * R::rows + sub;
     const int64_t t = t0 + r;
-    if (t >= p.T) break;
+#pragma unroll
+    for (int h = 0; h < H; ++h) id[round][h] = -1;
+    if (t >= p.T) continue;
     float l[PER];
     load_row<EL, PER>(p.logits, t, p.E, e0, p.whole, l);
     Choices<EL, LPR, PER> choices(l, e0, p.E);
     uint32_t key[H] = {};
-    int id[H] = {};  // the row's lane j keeps choices j and, of 16 lanes, 16 + j
     for (int j = 0; j < k; ++j) {
       uint32_t m;
       int e;
@@ -223,7 +233,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
       for (int h = 0; h < H; ++h) {
         const bool mine = j == h * LPR + pos;
         key[h] = mine ? m : key[h];
-        id[h] = mine ? e : id[h];
+        id[round][h] = mine ? e : id[round][h];
       }
     }
     // scores of the choices, and of all where they are divided by their sum
@@ -249,13 +259,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
     for (int h = 0; h < H; ++h) {
       const int j = h * LPR + pos;
       if (j < k) {
-        p.ids[t * k + j] = id[h];
+        p.ids[t * k + j] = id[round][h];
         p.weights[t * k + j] = sum > 0.f ? w[h] / sum : 0.f;
-        if (p.m_splits) atomicOr(&mask[id[h]], 1ull << r);
       }
     }
   }
   if (!p.m_splits) return;
+  const auto each_slot = [&](auto f) {  // f(token of the chunk, slot, expert)
+#pragma unroll
+    for (int round = 0; round < kRounds; ++round)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (id[round][h] >= 0) f((round * kRouteWaves + wave) * R::rows + sub, h * LPR + pos, id[round][h]);
+  };
+  __syncthreads();
+  each_slot([&](int r, int, int e) { atomicOr(&mask[e], 1ull << r); });
   __syncthreads();
   if (p.T > kChunk) {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.masks[(int64_t)blockIdx.x * p.E + e] = mask[e];
@@ -267,12 +285,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
   start[e] = block_scan(n) - n;
   if (e < p.E) p.m_splits[e] = n;
   __syncthreads();
-  for (int s = threadIdx.x; s < (int)p.T * k; s += kRouteThreads) {
-    const int e = p.ids[s];
-    const int row = start[e] + __popcll(mask[e] & ((1ull << (s / k)) - 1));
+  each_slot([&](int r, int j, int e) {
+    const int row = start[e] + __popcll(mask[e] & ((1ull << r) - 1)), s = r * k + j;
     p.row_index[s] = row;
     p.slot_index[row] = s;
-  }
+  });
 }
 
 // Where a chunk's slots of an expert start among the expert's.  A workgroup takes 16
@@ -315,6 +332,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t
   __shared__ unsigned long long mask[kRouteMaxExperts];
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   const int n = (int)min64(kChunk, T - t0) * k;
+  constexpr int kSlots = kChunk * kRouteMaxTopK / kRouteThreads;  // slots of a thread
+  int id[kSlots];  // loaded with the tables, so that the scan does not wait twice
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int s = i * kRouteThreads + threadIdx.x;
+    id[i] = s < n ? ids[t0 * k + s] : -1;
+  }
   const int e = threadIdx.x;
   int total = 0, here = 0;
   if (e < E) {
@@ -324,9 +348,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t
   }
   start[e] = block_scan(total) - total + here;
   __syncthreads();
-  for (int s = threadIdx.x; s < n; s += kRouteThreads) {
-    const int e = ids[t0 * k + s];
-    const int row = start[e] + __popcll(mask[e] & ((1ull << (s / k)) - 1));
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int s = i * kRouteThreads + threadIdx.x;
+    if (id[i] < 0) continue;
+    const int row = start[id[i]] + __popcll(mask[id[i]] & ((1ull << (s / k)) - 1));
     row_index[t0 * k + s] = row;
     slot_index[row] = (int32_t)(t0 * k + s);
   }
