@@ -18,7 +18,8 @@
 //     of 8 rows, the lanes' sums added at the end (vec_sum).
 //
 //   up    workgroup (expert, 16 columns of a): its waves split the contraction over K and add
-//         up through LDS, or, by dot products, take 4 columns each.  Leaves
+//         up through LDS, or, by dot products, take 4 columns each (8 a workgroup where all
+//         go that way).  Leaves
 //         a = w SwiGLU(W1 x + b1), w the token's weight for the expert, in the workspace.
 //   down  workgroup (16 or 8 columns of y): its waves share the (expert, piece of F) items of
 //         the whole call; each wave adds its products to its own sum of every token in LDS,
@@ -31,7 +32,7 @@
 //
 // Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.83 ms (7.1
 // TB/s of weights), down 1.11 ms (5.9 TB/s: 448 workgroups over 256 CUs); one token, 8 of 64
-// experts of 2048/768: up 12.4 us, down 8.4 us, half of it latency.
+// experts of 2048/768: up 11.8 us, down 8.5 us, half of it latency.
 #include <type_traits>
 
 #include "gl_vec.hpp"
@@ -587,14 +588,19 @@ __device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok,
   }
 }
 
+// Without MFMA the waves share nothing but the search, and smaller workgroups spread more
+// evenly (one token, 8 experts of 2048/768, 768 workgroups of two waves: 11.8 us, 384 of four
+// 13.2).
+template <int NT>
+constexpr int up_threads() { return NT ? kUpThreads : kUpThreads / 2; }
 // NV: experts of up to that many tokens go by up_vector, the others by up_product in at
 // most NT tiles (NT 0: the call has no more than NV tokens).
 template <int EL, int WEL, int NV, int NT>
-__global__ __launch_bounds__(kUpThreads) void moe_up_kernel(const MoeParams p) {
+__global__ __launch_bounds__(up_threads<NT>()) void moe_up_kernel(const MoeParams p) {
   __shared__ UpTokens tok;
   __shared__ __align__(16) float sums[NT ? NT * kUpWaves * 2 * 64 * 4 : 4];
   const int lane = threadIdx.x & 63;
-  const int64_t f0 = (int64_t)blockIdx.x * kMoeRows;
+  const int64_t f0 = (int64_t)blockIdx.x * (up_threads<NT>() / 16);
   const bool by_expert = p.E <= p.T * p.k;
   const int e = by_expert ? (int)blockIdx.y : p.ids[blockIdx.y];
   const bool valid = e >= 0 && e < p.E;
@@ -884,9 +890,10 @@ size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t F) {
 
 template <int EL, int WEL>
 static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
-  const dim3 up((unsigned)((p.F + kMoeRows - 1) / kMoeRows), p.n_entries);
   const auto go_up = [&](auto nv, auto nt) {
-    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, nv(), nt()>), up, dim3(kUpThreads), 0, s, p);
+    constexpr int threads = up_threads<nt()>(), columns = threads / 16;
+    hipLaunchKernelGGL((moe_up_kernel<EL, WEL, nv(), nt()>), dim3((unsigned)((p.F + columns - 1) / columns), p.n_entries),
+                       dim3(threads), 0, s, p);
   };
   using std::integral_constant;
   using Zero = integral_constant<int, 0>;
