@@ -423,7 +423,7 @@ __device__ __forceinline__ void store_a(const MoeParams &p, int slot, int64_t f,
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
 
-// The 8 rows of W1 behind 4 columns of a, a wave's share of the workgroup's 16.
+// The 8 rows of W1 behind 4 columns of a, a wave's share of the workgroup's.
 template <int WEL>
 struct UpRows {
   __amdgpu_buffer_rsrc_t wg, wu, sg, su;
@@ -593,6 +593,7 @@ __device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok,
 // 13.2).
 template <int NT>
 constexpr int up_threads() { return NT ? kUpThreads : kUpThreads / 2; }
+
 // NV: experts of up to that many tokens go by up_vector, the others by up_product in at
 // most NT tiles (NT 0: the call has no more than NV tokens).
 template <int EL, int WEL, int NV, int NT>
