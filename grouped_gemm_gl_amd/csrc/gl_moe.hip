@@ -593,11 +593,15 @@ __device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok,
 // 13.2).
 template <int NT>
 constexpr int up_threads() { return NT ? kUpThreads : kUpThreads / 2; }
+// Waves a SIMD that the registers have to allow: three (17 tokens over 32 experts of 4096/2048
+// in MXFP8 codes: 74 us, 81 at the two that the compiler settles for); four tiles would spill.
+template <int NT>
+constexpr int up_waves() { return NT == 1 || NT == 2 ? 3 : 1; }
 
 // NV: experts of up to that many tokens go by up_vector, the others by up_product in at
 // most NT tiles (NT 0: the call has no more than NV tokens).
 template <int EL, int WEL, int NV, int NT>
-__global__ __launch_bounds__(up_threads<NT>()) void moe_up_kernel(const MoeParams p) {
+__global__ __launch_bounds__(up_threads<NT>(), up_waves<NT>()) void moe_up_kernel(const MoeParams p) {
   __shared__ UpTokens tok;
   __shared__ __align__(16) float sums[NT ? NT * kUpWaves * 2 * 64 * 4 : 4];
   const int lane = threadIdx.x & 63;
@@ -912,6 +916,7 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   else if (p.T == 2) go_up(Two(), Zero());
   else if (p.T <= 4 && !is_mx(WEL)) go_up(integral_constant<int, is_mx(WEL) ? 2 : 4>(), Zero());
   else if (p.T <= 16) go_up(Few(), One());
+  else if (p.T <= 32) go_up(Few(), Two());
   else go_up(Few(), Four());
 
   // LDS: at most 4 KiB of sums a wave, 24 KiB of entries and 4 KiB of slots
