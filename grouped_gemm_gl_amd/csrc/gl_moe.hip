@@ -40,8 +40,9 @@
 namespace gl {
 
 // Weights as E4M3 codes with an E8M0 scale per 32 of a row; EL_MX: K and F are multiples of
-// 128, so that four scales of a row are an aligned word, EL_MX_RAGGED: of 32.
+// 128 above 128, so that a row has eight scales from an aligned word on, EL_MX_RAGGED: of 32.
 enum { EL_MX = 3, EL_MX_RAGGED = 4 };
+typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 constexpr bool is_mx(int wel) { return wel >= EL_MX; }
 constexpr int kMoeMaxTokens = 64;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
@@ -129,10 +130,10 @@ struct RowPair {
 // Where the lane's weight rows are: offsets from the first of the workgroup's R rows.
 struct WeightLane {
   uint32_t row, end_low, end_high, step, chunk;  // step: from row r to r + 8
-  uint32_t srow, send;                           // scales of row l % 16
+  uint32_t srow, send, wb;                       // scales of row l % 16
   int q;
   // rows: how many of the 16 there are; wb: bytes of one
-  __device__ WeightLane(int64_t rows, uint32_t wb, int64_t cols) {
+  __device__ WeightLane(int64_t rows, uint32_t wb, int64_t cols) : wb(wb) {
     const int lane = threadIdx.x & 63, r = lane & 15;
     q = lane >> 4;
     row = (r & 7) * wb;
@@ -152,6 +153,7 @@ template <int WEL, int R>
 struct Unit {  // bf16, fp16 and fp32 weights
   static constexpr int kElems = 128 / elem_bytes(WEL);
   static constexpr int steps = 2;
+  static constexpr bool pairs = false;
   static constexpr int b_bytes = 128;  // of a token's row
   RowPair r;
   __device__ static uint32_t b_byte(int i, int q) { return i * 64 + q * 16; }
@@ -161,6 +163,8 @@ struct Unit {  // bf16, fp16 and fp32 weights
     r.high = (i32x4_t){0, 0, 0, 0};
     if constexpr (R == 16) r.high = load_weight(w, b < o.end_high ? o.row + o.step + b : kNowhere);
   }
+  __device__ void load_scales(__amdgpu_buffer_rsrc_t, const WeightLane &, uint32_t) {}
+  __device__ void take_scales(const WeightLane &, uint32_t, Unit &) {}
   __device__ i32x4_t operand(int i) const { return r.chunk(i); }
 };
 
@@ -169,8 +173,11 @@ struct CodeUnit {  // MXFP8 weights
   static constexpr int kElems = 128;
   static constexpr int steps = 4;
   static constexpr int b_bytes = 256;
+  // A load of scales touches 16 lines, one of codes 8: two units' scales are one load.
+  static constexpr bool pairs = WEL == EL_MX;
   RowPair r;
   uint32_t s;  // the 4 scales of the unit's codes in row l % 16
+  i32x2_t s2;  // with `pairs`: of this and the next unit, as loaded
   int q;
   __device__ static uint32_t b_byte(int i, int q) { return (i >> 1) * 128 + q * 32 + (i & 1) * 16; }
   __device__ void load(__amdgpu_buffer_rsrc_t w, __amdgpu_buffer_rsrc_t sc, const WeightLane &o, uint32_t at) {
@@ -179,10 +186,7 @@ struct CodeUnit {  // MXFP8 weights
     r.low = load_weight(w, b < o.end_low ? o.row + b : kNowhere);
     r.high = (i32x4_t){0, 0, 0, 0};
     if constexpr (R == 16) r.high = load_weight(w, b < o.end_high ? o.row + o.step + b : kNowhere);
-    if constexpr (WEL == EL_MX) {
-      s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sc, (int)(at < o.send ? o.srow + at / 32 : kNowhere), 0, 0);
-      return;
-    }
+    if constexpr (pairs) return;
     s = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -190,6 +194,19 @@ struct CodeUnit {  // MXFP8 weights
       const uint32_t v = __builtin_amdgcn_raw_buffer_load_b8(sc, (int)(c < o.send ? o.srow + c / 32 : kNowhere), 0, 0);
       s |= (v & 0xff) << (16 * i + 8 * (q >> 1));
     }
+  }
+  // Scales of the units at `at` and behind it; where the former is the row's last, of it and
+  // the one before (a row has two units or more).
+  __device__ void load_scales(__amdgpu_buffer_rsrc_t sc, const WeightLane &o, uint32_t at) {
+    const uint32_t from = at / 32 - (at + 128 >= o.wb ? 4 : 0);
+    s2 = __builtin_bit_cast(
+        i32x2_t, __builtin_amdgcn_raw_buffer_load_b64(sc, (int)(at < o.send ? o.srow + from : kNowhere), 0, 0));
+  }
+  // Takes its scales, and gives the next unit its own, when the load is waited for.
+  __device__ void take_scales(const WeightLane &o, uint32_t at, CodeUnit &next) {
+    const bool last = at + 128 >= o.wb;
+    s = (uint32_t)(last ? s2[1] : s2[0]);
+    next.s = last ? 0u : (uint32_t)s2[1];
   }
   // 8 codes as bf16: their values are exact there.  The conversion takes the exponent
   // field of an fp32 scale, which is the E8M0 byte (255, NaN, included).
@@ -491,8 +508,9 @@ __device__ __forceinline__ void up_vector(const MoeParams &p, const UpTokens &to
 }
 
 // ----------------------------------------------------------------- many columns --
-// Contraction over K for up to NT tiles of 16 columns (HIGH false: one of 8): wave w takes units w, w + kUpWaves,
-// ... of the gate's and the up's 16 rows, U of each at a time.
+// Contraction over K for up to NT tiles of 16 columns (HIGH false: one of 8): wave w takes
+// units (MXFP8: pairs of units) w, w + kUpWaves, ... of the gate's and the up's 16 rows, U of
+// each at a time.
 template <int EL, int WEL, int NT, bool HIGH>
 __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &tok, int64_t f0, float *sums) {
   using W = Unit<WEL, kMoeRows>;
@@ -502,17 +520,22 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
   const auto wg = moe_rsrc(weight_row<WEL>(p.w1, e, f0)), wu = moe_rsrc(weight_row<WEL>(p.w1, e, p.F + f0));
   const auto sg = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, f0) : nullptr);
   const auto su = moe_rsrc(is_mx(WEL) ? scale_row(p.w1, e, p.F + f0) : nullptr);
-  // units past the end load zeros
-  const auto load = [&](W *g, W *u, int c0) {
+  // units past the end load zeros; scales: the unit is the first of a pair
+  const auto load = [&](W *g, W *u, int c0, auto scales) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t at = (uint32_t)(c0 + i * kUpWaves) * 128;
       g[i].load(wg, sg, rows, at);
       u[i].load(wu, su, rows, at);
     }
+    if constexpr (W::pairs && scales()) {
+      g->load_scales(sg, rows, (uint32_t)c0 * 128);
+      u->load_scales(su, rows, (uint32_t)c0 * 128);
+    }
   };
+  static_assert(!W::pairs || U == 1, "a pair is two steps");
   W g[U], u[U], ng[U], nu[U];
-  load(g, u, wave);
+  load(g, u, W::pairs ? 2 * wave : wave, std::true_type());
   const uint32_t xb = (uint32_t)(p.K * elem_bytes(EL));
   const auto xr = moe_rsrc(p.x);
   uint32_t xrow[NT][2], xend[NT][2];
@@ -528,7 +551,7 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
 #pragma unroll
   for (int t = 0; t < NT; ++t) ag[t] = au[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   const int units = (int)((p.K + W::kElems - 1) / W::kElems);
-  const auto step = [&](int c0, const W *g, const W *u, W *ng, W *nu) {
+  const auto step = [&](int c0, int next, W *g, W *u, W *ng, W *nu, auto first) {
     uint32_t at[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) at[i] = (uint32_t)(c0 + i * kUpWaves) * W::b_bytes;
@@ -539,8 +562,13 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
       // order, the products wait for the former alone
       Columns<W, U, HIGH> b;
       b.load(xr, xrow[t][0], xend[t][0], xrow[t][1], xend[t][1], at);
-      if (t == 0) load(ng, nu, c0 + kUpWaves * U);
+      if (t == 0) load(ng, nu, next, std::bool_constant<!first()>());
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (W::pairs && first())
+        if (t == 0) {
+          g->take_scales(rows, (uint32_t)c0 * 128, *ng);
+          u->take_scales(rows, (uint32_t)c0 * 128, *nu);
+        }
 #pragma unroll
       for (int i = 0; i < U * W::steps; ++i) {
         const i32x4_t x = b.operand(i);
@@ -551,10 +579,11 @@ __device__ __forceinline__ void up_product(const MoeParams &p, const UpTokens &t
     }
   };
   // two register sets in turn: copying one to the other would wait for its loads
-  for (int c0 = wave; c0 < units; c0 += 2 * kUpWaves * U) {
-    step(c0, g, u, ng, nu);
-    if (c0 + kUpWaves * U >= units) break;
-    step(c0 + kUpWaves * U, ng, nu, g, u);
+  constexpr int kNext = W::pairs ? 1 : kUpWaves * U;
+  for (int c0 = W::pairs ? 2 * wave : wave; c0 < units; c0 += 2 * kUpWaves * U) {
+    step(c0, c0 + kNext, g, u, ng, nu, std::true_type());
+    if (c0 + kNext >= units) break;
+    step(c0 + kNext, c0 + 2 * kUpWaves * U, ng, nu, g, u, std::false_type());
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -769,11 +798,15 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
     const auto r = moe_rsrc(weight_row<WEL>(p.w2, e, o.n0));
     const auto s = moe_rsrc(is_mx(WEL) ? scale_row(p.w2, e, o.n0) : nullptr);
 #pragma unroll
-    for (int j = 0; j < U; ++j) w[j].load(r, s, rows, (c * U + j) * 128);
+    for (int j = 0; j < U; ++j) {
+      w[j].load(r, s, rows, (c * U + j) * 128);
+      if constexpr (W::pairs)
+        if (j % 2 == 0) w[j].load_scales(s, rows, (c * U + j) * 128);
+    }
   };
   int i = wave / pieces, c = wave - i * pieces;
   // one item with its weights in `cur`; moves on to the next, whose weights go to `nxt`
-  const auto step = [&](const W *cur, W *nxt) {
+  const auto step = [&](W *cur, W *nxt) {
     int ni = i, nc = c + kDownWaves;
     while (nc >= pieces) {
       nc -= pieces;
@@ -792,6 +825,10 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
       b.load(ar, row_lo, lo < m ? ab : 0, row_hi, hi < m ? ab : 0, at);
       if (t == 0 && ni < o.n_many) load(nxt, ni, nc);
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (W::pairs)
+        if (t == 0)
+#pragma unroll
+          for (int j = 0; j < U; j += 2) cur[j].take_scales(rows, (c * U + j) * 128, cur[j + 1]);
       f32x4_t sum = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < U * W::steps; ++s) sum = mma<EL>(cur[s / W::steps].operand(s % W::steps), b.operand(s), sum);
@@ -962,7 +999,7 @@ hipError_t launch_moe(int el, bool mx, int E, int64_t K, int64_t F, int64_t N, i
   p.entries = (MoeEntry *)ws;
   p.slot_of = (int16_t *)(p.entries + p.n_entries);
   p.a = (char *)ws + moe_table_bytes(p.n_entries);
-  if (mx && K % 128 == 0 && F % 128 == 0) launch_moe_typed<EL_BF16, EL_MX>(p, s);
+  if (mx && K % 128 == 0 && F % 128 == 0 && K > 128 && F > 128) launch_moe_typed<EL_BF16, EL_MX>(p, s);
   else if (mx) launch_moe_typed<EL_BF16, EL_MX_RAGGED>(p, s);
   else if (el == EL_F32) launch_moe_typed<EL_F32, EL_F32>(p, s);
   else if (el == EL_F16) launch_moe_typed<EL_F16, EL_F16>(p, s);

@@ -136,6 +136,18 @@ def test_mxfp8_weights(T, E, k, K, F, N):
     check(c, run(c))
 
 
+# rows of an odd number of 128 codes, whose last scales lie at the end of the tensor
+@pytest.mark.parametrize("T,E,k,K,F,N", [(6, 2, 2, 384, 384, 40), (12, 3, 2, 640, 1152, 4104), (25, 3, 2, 1152, 640, 72),
+                                         (40, 4, 3, 896, 384, 4096), (64, 3, 2, 384, 896, 24), (9, 1, 1, 256, 256, 16)])
+def test_mxfp8_rows_of_odd_length(T, E, k, K, F, N):
+    c = case(T * 11 + E, T, E, k, K, F, N, BF16, mx=True, bias=T % 2 == 1, residual=T % 2 == 0)
+    check(c, run(c))
+    c["w2_scale"][0, 1, -1] = 0xFF  # reaches column 1 of the tokens that name expert 0
+    ids, w = c["ids"].cpu().numpy(), c["weights"].cpu().numpy()
+    hit = torch.from_numpy(((ids == 0) & (w != 0)).any(1))
+    assert torch.equal(torch.isnan(run(c)).cpu().any(1), hit) and hit.any()
+
+
 def test_mxfp8_scales_at_the_ends_of_their_range():
     """Scales 2^-127 .. 2^127 and the NaN scale: codes expand exactly or to NaN."""
     c = case(5, 2, 2, 1, 64, 32, 16, BF16, mx=True)
