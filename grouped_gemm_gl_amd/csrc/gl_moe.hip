@@ -32,7 +32,7 @@
 //
 // Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.83 ms (7.1
 // TB/s of weights), down 1.11 ms (5.9 TB/s: 448 workgroups over 256 CUs); one token, 8 of 64
-// experts of 2048/768: up 11.8 us, down 8.5 us, half of it latency.
+// experts of 2048/768: up 12.4 us, down 8.6 us, half of it latency.
 #include <type_traits>
 
 #include "gl_vec.hpp"
@@ -46,11 +46,11 @@ typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 constexpr bool is_mx(int wel) { return wel >= EL_MX; }
 constexpr int kMoeMaxTokens = 64;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
-// Units that a wave takes at a time (an MXFP8 unit holds twice the k values).
+// Units that a wave takes at a time, in the up kernel (an MXFP8 unit holds twice the k values)
+// and in the down kernel (MXFP8, 17 tokens over 32 experts of 4096/2048: 44.3 us, 2 units 46.2).
 template <int WEL>
 constexpr int up_units() { return is_mx(WEL) ? 1 : 2; }
-template <int WEL>
-constexpr int down_units() { return is_mx(WEL) ? 2 : 4; }
+constexpr int kDownUnits = 4;
 constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64;
 constexpr int kMoeRows = 16;  // weight rows of a workgroup (per half of W1)
 
@@ -784,7 +784,7 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
 template <int EL, int WEL, int R>
 __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o) {
   using W = Unit<WEL, R>;
-  constexpr int U = down_units<WEL>();
+  constexpr int U = kDownUnits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const auto entry = [&](int i) { return o.ent[p.n_entries - 1 - i]; };
   const uint32_t ab = (uint32_t)(p.F * elem_bytes(EL));
@@ -946,8 +946,9 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   // in the up kernel (4 tokens over 8 experts of 4096/8192: 127 us, by MFMA 136), two
   // otherwise (down kernel, 2 tokens there: 63 us, by MFMA 85).  In larger calls only beside
   // MXFP8 codes, for the experts of one or two tokens, where the MFMA's columns would load
-  // 256 bytes of activations for every 128 of codes (8 tokens over 32 experts of 4096/2048:
-  // up 72 us, all by MFMA 81, down 40 and 50; bf16 does as well by MFMA, 116 and 117 us).
+  // 256 bytes of activations for every 128 of codes (8 tokens over 32 experts of 4096/1920:
+  // up 53.5 us, all by MFMA 55.7; 17 over 32 of 4096/2048: down 44.3 and 46.1; bf16 does as
+  // well by MFMA).
   using Few = integral_constant<int, is_mx(WEL) ? 2 : 0>;
   if (p.T == 1) go_up(One(), Zero());
   else if (p.T == 2) go_up(Two(), Zero());
