@@ -25,10 +25,15 @@
 //         the whole call; each wave adds its products to its own sum of every token in LDS,
 //         and the waves' sums are added at the end: no atomics, a fixed order.
 //
-// For 16-bit weights a is kept as two values of the weights' type, the rounded value and
-// the rest, which share a step as two columns: the products see 16 significant bits of a
-// (22 for fp16) where one value would add its own rounding, of the output's size, to the
-// result.
+// Between the kernels a is fp32 beside fp32 and fp16 weights, and for bf16 products two bf16
+// values, the rounded value and the rest (2^-18 of a or less is lost).  An MFMA step of 16-bit
+// weights takes a as two such parts, which share the step as two columns: the products see at
+// least 16 significant bits of a where one value would add its own rounding, of the output's
+// size, to the result.  fp16's exponents are too few for that (a = 70000 is no fp16 value, and
+// of 1e-5 the two parts would keep 8 bits), so the fp16 parts are made in the down kernel under
+// a power-of-two scale for a token's 256 columns of an item (ScaledColumns): 2^-20 of a value
+// or 2^-49 of the largest of the 256 is lost, over fp32's whole range.  Its dot products take
+// the fp32 values as they are.
 //
 // Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.83 ms (7.1
 // TB/s of weights), down 1.11 ms (5.9 TB/s: 448 workgroups over 256 CUs); one token, 8 of 64
@@ -81,7 +86,7 @@ struct MoeParams {
   char *y;
   MoeEntry *entries;  // [min(T k, E)]
   int16_t *slot_of;   // [entries][64] slot whose row of a holds a token's values
-  char *a;            // [T k][F] fp32, or two planes [T k][F] of the 16-bit type
+  char *a;            // [T k][F] fp32, or two planes [T k][F] of bf16
   int T, k, E, n_entries;
   int64_t K, F, N;
 };
@@ -252,6 +257,78 @@ struct Columns {
   __device__ i32x4_t operand(int piece) const { return b[piece / 2].chunk(piece & 1); }
 };
 
+// The same of fp32 values for fp16 products, two columns a token: the value's leading bits in
+// columns 0-7 and the rest in 8-15, both in the scale 2^shift that brings the largest of the U
+// units' values to 2^14 ... 2^15, the rest 2^11 above that.  (The weights' sums are divided by
+// both afterwards.)  Both parts are cut off rather than rounded, which keeps them below 2^15.
+// The lanes of a token's two columns each load and split half of the 8 values that both need,
+// so a load takes whole lines (8 rows by 128 bytes: 64 tokens over 8 experts of 4096/14336 take
+// 704 us, 711 where each lane loads 32 bytes of its own), and change halves by rotations.  The
+// splitting is some 150 instructions an item that its wave waits for: fp16 values stored in
+// two unscaled parts, as bf16's are, would take 360 us and not 385 for 5 tokens over those
+// experts, and 695 for the 64, but hold neither 70000 nor 16 bits of 10^-3.
+constexpr float kRestScale = 2048.f;
+template <class W, int U>
+struct ScaledColumns {
+  static constexpr int n = U * W::steps;
+  i32x4_t b[n];  // 4 fp32 values of a piece; split: two words of leading bits, two of the rest
+  int shift;
+  // row / end: the lane's token (l % 8) in bytes of fp32
+  __device__ void load(__amdgpu_buffer_rsrc_t a, uint32_t row, uint32_t end, const uint32_t *unit_at) {
+    const int lane = threadIdx.x & 63, h = (lane >> 3) & 1, q = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const uint32_t at = 2 * (unit_at[j / W::steps] + W::b_byte(j % W::steps, q)) + 16 * h;
+      b[j] = load16(a, at < end ? row + at : kNowhere);
+    }
+  }
+  __device__ void split() {
+    float top = 0.f;  // (NaN leaves it as it is)
+#pragma unroll
+    for (int j = 0; j < n; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(__int_as_float(b[j][i])));
+    // over the token's eight lanes: l ^ 8 by a rotation, l ^ 16 and l ^ 32 by swaps
+    top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x128, 0xf, 0xf, true)));
+    const auto s16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
+    const auto s32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(s32[0]), __uint_as_float(s32[1]));
+    shift = min(141 - (int)(__float_as_uint(top) >> 23), 127);
+    const float scale = __uint_as_float((uint32_t)(shift + 127) << 23);
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      i32x4_t o;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float v = __int_as_float(b[j][2 * i]) * scale, w = __int_as_float(b[j][2 * i + 1]) * scale;
+        const auto h = __builtin_amdgcn_cvt_pkrtz(v, w);
+        o[i] = __builtin_bit_cast(int, h);
+        o[2 + i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_pkrtz((v - (float)h[0]) * kRestScale,
+                                                                      (w - (float)h[1]) * kRestScale));
+      }
+      b[j] = o;
+    }
+  }
+  // lanes 0-7 of 16: their own leading bits, then those of l + 8; lanes 8-15: the rest of
+  // l - 8, then their own
+  __device__ i32x4_t operand(int piece) const {
+    const i32x4_t v = b[piece];
+    i32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o[i] = __builtin_amdgcn_update_dpp(v[i], v[2 + i], 0x128, 0xf, 0xc, false);
+      o[2 + i] = __builtin_amdgcn_update_dpp(v[2 + i], v[i], 0x128, 0xf, 0x3, false);
+    }
+    return o;
+  }
+  // a token's sum from those of its two columns; where a part was not finite the leading one
+  // tells all (the rest of an infinity is NaN)
+  __device__ float sum(float leading, float rest) const {
+    return ldexpf(fabsf(leading) < INFINITY ? fmaf(rest, 1.f / kRestScale, leading) : leading, -shift);
+  }
+};
+
 // acc[weight row][column] += A B over the k values of one 16-byte piece of each lane
 template <int EL>
 __device__ __forceinline__ f32x4_t mma(i32x4_t a, i32x4_t b, f32x4_t acc) {
@@ -329,10 +406,10 @@ struct VecRows {
 };
 
 // A lane's values of one token at the places of its 16 weight bytes: 16 bytes of the
-// activations' type, or 32 beside MXFP8 codes.
-template <int WEL>
+// activations' type, or 32 beside MXFP8 codes and where fp32 values meet fp16 weights.
+template <int WEL, bool WIDE = is_mx(WEL)>
 struct VecToken {
-  static constexpr int parts = is_mx(WEL) ? 2 : 1;
+  static constexpr int parts = WIDE ? 2 : 1;
   i32x4_t v[parts];
   __device__ void load(__amdgpu_buffer_rsrc_t x, uint32_t row, uint32_t at, uint32_t xb) {
 #pragma unroll
@@ -353,11 +430,21 @@ __device__ __forceinline__ float dot2(int a, int b, float c) {
 
 // acc[r][c] += row r . token c over the lane's places, for n tokens whose values are the
 // sum of P parts
-template <int EL, int WEL, int NV, int P>
-__device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<WEL> (*x)[P], int n, float (*acc)[NV]) {
+template <int EL, int WEL, int NV, int P, bool WIDE>
+__device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<WEL, WIDE> (*x)[P], int n,
+                                         float (*acc)[NV]) {
 #pragma unroll
   for (int r = 0; r < kVecRows; ++r) {
-    if constexpr (is_mx(WEL)) {
+    if constexpr (WIDE && WEL == EL_F16) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        if (c < n)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const f16x8_t h = __builtin_bit_cast(f16x8_t, w.r[r]);
+            acc[r][c] = fmaf((float)h[i], __int_as_float(x[c][0].v[i >> 2][i & 3]), acc[r][c]);
+          }
+    } else if constexpr (is_mx(WEL)) {
       const float f = __uint_as_float((uint32_t)w.s[r] << 23);
       int q[8];  // 16 codes as bf16 pairs, exact there
 #pragma unroll
@@ -418,25 +505,28 @@ __device__ __forceinline__ float vec_sum(const float *v, int stride) {
   return s;
 }
 
-// Rounds v to the weights' 16-bit type in two parts: v ~ hi + lo.
-template <bool F16>
+// Rounds v to bf16 in two parts: v ~ hi + lo.
 __device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
-  hi = f32_to_h16<F16>(v);
-  const float rest = v - h16_to_f32<F16>(hi);
-  lo = fabsf(rest) < INFINITY ? f32_to_h16<F16>(rest) : (uint16_t)0;  // hi is not finite
+  hi = f32_to_h16<false>(v);
+  const float rest = v - h16_to_f32<false>(hi);
+  lo = fabsf(rest) < INFINITY ? f32_to_h16<false>(rest) : (uint16_t)0;  // hi is not finite
 }
 
 // Token's value a for slot's row of the workspace, column f.
 template <int EL>
 __device__ __forceinline__ void store_a(const MoeParams &p, int slot, int64_t f, float a) {
   const int64_t at = slot * p.F + f;
-  if constexpr (EL == EL_F32) {
+  if constexpr (EL != EL_BF16) {
     ((float *)p.a)[at] = a;
   } else {
     uint16_t *hi = (uint16_t *)p.a, *lo = hi + (int64_t)p.T * p.k * p.F;
-    split<EL == EL_F16>(a, hi[at], lo[at]);
+    split(a, hi[at], lo[at]);
   }
 }
+
+// Bytes of a row of a (bf16: of one of its planes).
+template <int EL>
+__device__ __forceinline__ uint32_t a_row_bytes(int64_t F) { return (uint32_t)(F * (EL == EL_BF16 ? 2 : 4)); }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
 
@@ -487,13 +577,13 @@ __device__ __forceinline__ void up_vector(const MoeParams &p, const UpTokens &to
     load_x(x1, b + 1);
     rows.load(w1, b + 1);
     __builtin_amdgcn_sched_barrier(0);
-    vec_dots<EL, WEL, NV, 1>(w0, x0, tok.n, acc);
+    vec_dots<EL, WEL, NV>(w0, x0, tok.n, acc);
     if (b + 1 >= blocks) break;
     __builtin_amdgcn_sched_barrier(0);
     load_x(x0, b + 2);
     rows.load(w0, b + 2);
     __builtin_amdgcn_sched_barrier(0);
-    vec_dots<EL, WEL, NV, 1>(w1, x1, tok.n, acc);
+    vec_dots<EL, WEL, NV>(w1, x1, tok.n, acc);
     __builtin_amdgcn_sched_barrier(0);
   }
   const int64_t f = rows.f0 + (vec_row(lane) & 3);
@@ -719,15 +809,16 @@ struct DownPlace {
 // in turn.
 template <int EL, int WEL, int R, int NV>
 __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace &o) {
-  constexpr int parts = EL == EL_F32 ? 1 : 2;  // of a
-  constexpr uint32_t kX = 16 * VecToken<WEL>::parts;
+  constexpr int parts = EL == EL_BF16 ? 2 : 1;  // of a
+  using Token = VecToken<WEL, is_mx(WEL) || EL == EL_F16>;
+  constexpr uint32_t kX = 16 * Token::parts;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = (uint32_t)(p.F * elem_bytes(EL));
+  const uint32_t wb = (uint32_t)row_bytes<WEL>(p.F), ab = a_row_bytes<EL>(p.F);
   const uint32_t plane = (uint32_t)(p.T * p.k) * ab;
   const auto ar = moe_rsrc(p.a);
   const int blocks = (int)((p.F + block_elems<WEL>() - 1) / block_elems<WEL>()), per = blocks * (R / 8);
   int i = wave / per, c = wave - i * per;
-  const auto load = [&](VecRows<WEL> &w, VecToken<WEL> (*x)[parts], int i, int c) {
+  const auto load = [&](VecRows<WEL> &w, Token (*x)[parts], int i, int c) {
     const int h = c / blocks, b = c - h * blocks;
     const DownEntry t = o.ent[i];
     const int e = __builtin_amdgcn_readfirstlane(t.expert), n = __builtin_amdgcn_readfirstlane(t.n);
@@ -743,8 +834,7 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
     w.load(moe_rsrc(weight_row<WEL>(p.w2, e, r0)), moe_rsrc(is_mx(WEL) ? scale_row(p.w2, e, r0) : nullptr), 0, 8,
            (uint32_t)(b * 64 + lane) * 16, wb, (int)min64(p.N - r0, 8));
   };
-  const auto step = [&](const VecRows<WEL> &w, const VecToken<WEL> (*x)[parts], VecRows<WEL> &nw,
-                        VecToken<WEL> (*nx)[parts]) {
+  const auto step = [&](const VecRows<WEL> &w, const Token (*x)[parts], VecRows<WEL> &nw, Token (*nx)[parts]) {
     int ni = i, nc = c + kDownWaves;
     while (nc >= per) {
       nc -= per;
@@ -754,7 +844,7 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
     __builtin_amdgcn_sched_barrier(0);
     const int n = __builtin_amdgcn_readfirstlane(o.ent[i].n), base = __builtin_amdgcn_readfirstlane(o.ent[i].base);
     float acc[kVecRows][NV] = {};
-    vec_dots<EL, WEL, NV, parts>(w, x, n, acc);
+    vec_dots<EL, WEL, NV>(w, x, n, acc);
     // lanes 0 ... 7 of a row's 8 hold the same sum: the k-th adds token k's
     const int k = lane & 7;
     float sum = 0.f;
@@ -770,7 +860,7 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
     c = nc;
   };
   VecRows<WEL> w0, w1;
-  VecToken<WEL> x0[NV][parts], x1[NV][parts];
+  Token x0[NV][parts], x1[NV][parts];
   if (i < o.n_vec) load(w0, x0, i, c);
   while (i < o.n_vec) {  // two register sets in turn
     step(w0, x0, w1, x1);
@@ -787,7 +877,7 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
   constexpr int U = kDownUnits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const auto entry = [&](int i) { return o.ent[p.n_entries - 1 - i]; };
-  const uint32_t ab = (uint32_t)(p.F * elem_bytes(EL));
+  const uint32_t ab = a_row_bytes<EL>(p.F);
   const WeightLane rows(min64(p.N - o.n0, R), (uint32_t)row_bytes<WEL>(p.F), p.F);
   const auto ar = moe_rsrc(p.a);
   constexpr int kCols = EL == EL_F32 ? 16 : 8;  // tokens of a step
@@ -816,25 +906,31 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
     uint32_t at[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) at[j] = (c * U + j) * W::b_bytes;
-    // the entry's tokens as columns; a 16-bit a's two parts are columns of the same step
+    // the entry's tokens as columns; for 16-bit products a's two parts are columns of a step
     for (int t = 0; t < m; t += kCols) {
       const int lo = t + (lane & 7), hi = kCols == 16 ? lo + 8 : lo;
       const uint32_t row_lo = lo < m ? (uint32_t)o.slots[base + lo] * ab : 0;
       const uint32_t row_hi = kCols == 8 ? row_lo + plane : hi < m ? (uint32_t)o.slots[base + hi] * ab : 0;
-      Columns<W, U, true> b;
-      b.load(ar, row_lo, lo < m ? ab : 0, row_hi, hi < m ? ab : 0, at);
+      std::conditional_t<EL == EL_F16, ScaledColumns<W, U>, Columns<W, U, true>> b;
+      if constexpr (EL == EL_F16) b.load(ar, row_lo, lo < m ? ab : 0, at);
+      else b.load(ar, row_lo, lo < m ? ab : 0, row_hi, hi < m ? ab : 0, at);
       if (t == 0 && ni < o.n_many) load(nxt, ni, nc);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (W::pairs)
         if (t == 0)
 #pragma unroll
           for (int j = 0; j < U; j += 2) cur[j].take_scales(rows, (c * U + j) * 128, cur[j + 1]);
+      if constexpr (EL == EL_F16) b.split();
       f32x4_t sum = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < U * W::steps; ++s) sum = mma<EL>(cur[s / W::steps].operand(s % W::steps), b.operand(s), sum);
       if constexpr (kCols == 8)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] += __shfl_xor(sum[r], 8);
+        for (int r = 0; r < 4; ++r) {
+          const float rest = __shfl_xor(sum[r], 8);
+          if constexpr (EL == EL_F16) sum[r] = b.sum(sum[r], rest);
+          else sum[r] += rest;
+        }
       if (col < kCols && t + col < m) {  // each column another token: no lane shares a sum
         f32x4_t *to = (f32x4_t *)(o.acc + (wave * p.T + o.slots[base + t + col] / p.k) * 16 + q * 4);
         *to += sum;

@@ -578,9 +578,11 @@ int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype d
  *   y        [y_rows, N], y_rows >= T; rows >= T are never written.  A token without a
  *            slot gets its residual, or zeros
  *   workspace  gl_moe_few_tokens_workspace_size bytes, 16-byte aligned
- * Sums are fp32 in a fixed order (deterministic), the SwiGLU output between the two
- * products keeps at least 16 significant bits, y is rounded once.  K, F and N multiples of
- * 8 (16-bit) or 4 (fp32), for MXFP8 K and F multiples of 32; at most 2^22, and
+ * Sums are fp32 in a fixed order (deterministic) and y is rounded once.  The SwiGLU output
+ * between the two products, times w_j, is computed in fp32, and the products with W2 take
+ * at least 16 significant bits of it (bf16: of values from 2^-117 on; fp16: from 2^-32 of
+ * the largest of 256 neighbours on, however large or small that is).  K, F and N multiples
+ * of 8 (16-bit) or 4 (fp32), for MXFP8 K and F multiples of 32; at most 2^22, and
  * T * top_k * F < 2^29.
  */
 #define GL_MOE_MAX_TOKENS 64
