@@ -257,7 +257,20 @@ struct Columns {
   __device__ i32x4_t operand(int piece) const { return b[piece / 2].chunk(piece & 1); }
 };
 
-// The same of fp32 values for fp16 products, two columns a token: the value's leading bits in
+// Rounds v to bf16 in two parts: v ~ hi + lo.
+__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
+  hi = f32_to_h16<false>(v);
+  const float rest = v - h16_to_f32<false>(hi);
+  lo = fabsf(rest) < INFINITY ? f32_to_h16<false>(rest) : (uint16_t)0;  // hi is not finite
+}
+
+// A sum of weights times a from those of a's two parts.  Where the leading one is not finite it
+// tells all: an infinite weight meets the rest as NaN or in the other sign.
+__device__ __forceinline__ float join(float leading, float rest) {
+  return fabsf(leading) < INFINITY ? leading + rest : leading;
+}
+
+// The tokens' side of U units from fp32 values for fp16 products, two columns a token: the value's leading bits in
 // columns 0-7 and the rest in 8-15, both in the scale 2^shift that brings the largest of the U
 // units' values to 2^14 ... 2^15, the rest 2^11 above that.  (The weights' sums are divided by
 // both afterwards.)  Both parts are cut off rather than rounded, which keeps them below 2^15.
@@ -322,11 +335,9 @@ struct ScaledColumns {
     }
     return o;
   }
-  // a token's sum from those of its two columns; where a part was not finite the leading one
-  // tells all (the rest of an infinity is NaN)
-  __device__ float sum(float leading, float rest) const {
-    return ldexpf(fabsf(leading) < INFINITY ? fmaf(rest, 1.f / kRestScale, leading) : leading, -shift);
-  }
+  // a token's sum from those of its two columns (an infinite weight gives NaN where a is below
+  // 2^-39 of the largest: its leading part is 0)
+  __device__ float sum(float leading, float rest) const { return ldexpf(join(leading, rest * (1.f / kRestScale)), -shift); }
 };
 
 // acc[weight row][column] += A B over the k values of one 16-byte piece of each lane
@@ -428,11 +439,10 @@ __device__ __forceinline__ float dot2(int a, int b, float c) {
   }
 }
 
-// acc[r][c] += row r . token c over the lane's places, for n tokens whose values are the
-// sum of P parts
+// acc[r][c P + d] += row r . part d of token c over the lane's places, for n tokens
 template <int EL, int WEL, int NV, int P, bool WIDE>
 __device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<WEL, WIDE> (*x)[P], int n,
-                                         float (*acc)[NV]) {
+                                         float (*acc)[NV * P]) {
 #pragma unroll
   for (int r = 0; r < kVecRows; ++r) {
     if constexpr (WIDE && WEL == EL_F16) {
@@ -459,7 +469,8 @@ __device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<W
 #pragma unroll
           for (int d = 0; d < P; ++d)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[r][c] = dot2<EL>(q[i], x[c][d].v[i >> 2][i & 3], acc[r][c]);
+            for (int i = 0; i < 8; ++i)
+              acc[r][c * P + d] = dot2<EL>(q[i], x[c][d].v[i >> 2][i & 3], acc[r][c * P + d]);
       __builtin_amdgcn_sched_barrier(0);  // one row's expanded codes in registers at a time
     } else {
 #pragma unroll
@@ -470,8 +481,9 @@ __device__ __forceinline__ void vec_dots(const VecRows<WEL> &w, const VecToken<W
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int a = w.r[r][i], b = x[c][d].v[0][i];
-              if constexpr (EL == EL_F32) acc[r][c] = fmaf(__int_as_float(a), __int_as_float(b), acc[r][c]);
-              else acc[r][c] = dot2<EL>(a, b, acc[r][c]);
+              float &s = acc[r][c * P + d];
+              if constexpr (EL == EL_F32) s = fmaf(__int_as_float(a), __int_as_float(b), s);
+              else s = dot2<EL>(a, b, s);
             }
     }
   }
@@ -503,13 +515,6 @@ __device__ __forceinline__ float vec_sum(const float *v, int stride) {
   s += dpp_move<0x4e>(s);   // quad_perm [2, 3, 0, 1]
   s += dpp_move<0x141>(s);  // mirrored within 8: the other quad
   return s;
-}
-
-// Rounds v to bf16 in two parts: v ~ hi + lo.
-__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
-  hi = f32_to_h16<false>(v);
-  const float rest = v - h16_to_f32<false>(hi);
-  lo = fabsf(rest) < INFINITY ? f32_to_h16<false>(rest) : (uint16_t)0;  // hi is not finite
 }
 
 // Token's value a for slot's row of the workspace, column f.
@@ -843,15 +848,20 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
     if (ni < o.n_vec) load(nw, nx, ni, nc);
     __builtin_amdgcn_sched_barrier(0);
     const int n = __builtin_amdgcn_readfirstlane(o.ent[i].n), base = __builtin_amdgcn_readfirstlane(o.ent[i].base);
-    float acc[kVecRows][NV] = {};
+    float acc[kVecRows][NV * parts] = {};
     vec_dots<EL, WEL, NV>(w, x, n, acc);
+    if constexpr (parts == 2)
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) acc[r][j * parts] = join(acc[r][j * parts], acc[r][j * parts + 1]);
     // lanes 0 ... 7 of a row's 8 hold the same sum: the k-th adds token k's
     const int k = lane & 7;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (j < n) {
-        const float v = vec_sum(&acc[0][j], NV);
+        const float v = vec_sum(&acc[0][j * parts], NV * parts);
         sum = k == j ? v : sum;
       }
     if (k < n) o.acc[(wave * p.T + o.slots[base + k] / p.k) * 16 + (c / blocks) * 8 + vec_row(lane)] += sum;
@@ -929,7 +939,7 @@ __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o
         for (int r = 0; r < 4; ++r) {
           const float rest = __shfl_xor(sum[r], 8);
           if constexpr (EL == EL_F16) sum[r] = b.sum(sum[r], rest);
-          else sum[r] += rest;
+          else sum[r] = join(sum[r], rest);
         }
       if (col < kCols && t + col < m) {  // each column another token: no lane shares a sum
         f32x4_t *to = (f32x4_t *)(o.acc + (wave * p.T + o.slots[base + t + col] / p.k) * 16 + q * 4);

@@ -96,3 +96,34 @@ def test_one_column_far_above_the_others(T):
     c["w2"][:, :, 100] = 0
     ref = check(c)
     assert 2.0 ** -12 < np.abs(ref).max() < 60000
+
+
+@pytest.mark.parametrize("T,E,k,K,F,N", SHAPES)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_infinite_weights_give_what_the_formula_gives(T, E, k, K, F, N, dtype):
+    """Single infinite weights of W2, of both signs and in one row also two of them: infinities
+    of the right sign, NaN where they meet with opposite signs, and all else as without them."""
+    c = case(T + N + 3, T, E, k, K, F, N, dtype)
+    clean, lim = limits(c)
+    for n, f, v in ((0, 3, np.inf), (1, F - 1, -np.inf), (5, 9, np.inf), (5, F // 2, np.inf), (N - 1, F - 8, -np.inf)):
+        c["w2"][1, n, f] = v
+    y = to64(run(c))
+    with np.errstate(invalid="ignore"):
+        ref = eb.moe(to64(c["x"]), c["ids"].numpy(), to64(c["weights"]), to64(c["w1"]), to64(c["w2"]))
+    finite = np.isfinite(ref)
+    assert (~finite).any() or not (c["ids"] == 1).any()
+    assert np.array_equal(y[~finite], ref[~finite], equal_nan=True)
+    assert (np.abs(y - clean) <= lim)[finite].all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 20])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_infinite_values_between_the_products(T, dtype):
+    """An infinite weight of W1's second half: a is infinite in one column."""
+    c = case(3, T, 2, 1, 64, 72, 40, dtype)
+    c["w1"][1, 72 + 7, 5] = np.inf
+    y = to64(run(c))
+    with np.errstate(invalid="ignore"):
+        ref = eb.moe(to64(c["x"]), c["ids"].numpy(), to64(c["weights"]), to64(c["w1"]), to64(c["w2"]))
+    hit = c["ids"][:, 0].numpy() == 1
+    assert np.isinf(ref[hit]).all() and np.array_equal(y[hit], ref[hit]) and np.isfinite(y[~hit]).all()
