@@ -408,7 +408,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteBackward p) {
         const float v = load_logit<EL>(p.logits, t * p.E + e);
         if (p.sigm) {
           s[h] = 1.f / (1.f + expf(-v));
-          slope[h] = 1.f - s[h];
+          slope[h] = 1.f / (1.f + expf(v));  // 1 - s would cancel: nothing is left of it from 17 on
         } else {
           s[h] = top == -INFINITY ? 0.f : expf(v - top);
         }
