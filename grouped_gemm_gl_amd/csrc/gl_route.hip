@@ -32,6 +32,16 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
   else return as_logit(h16_to_f32<EL == EL_F16>(((const uint16_t *)p)[i]));
 }
 
+// sigmoid(v) e^-base, base at most 0 (and 0 where any v of the row is above): without overflow
+// of e^-v, and with the base of score_base no sum of a row's scores underflows.
+__device__ __forceinline__ float sigmoid_score(float v, float base) {
+  return (v > 0.f ? 1.f : expf(v - base)) / (1.f + expf(-fabsf(v)));
+}
+// The base for scores that are divided by their sum, from the largest logit among them.  Below
+// -745, where 64 bits hold its sigmoid as 0, a logit is a mask (a type's lowest value, say):
+// scores stay 0.
+__device__ __forceinline__ float score_base(float largest) { return largest > -745.f ? fminf(largest, 0.f) : 0.f; }
+
 // Unsigned order of floats without NaN, -0 equal to +0; every value maps above 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
@@ -70,6 +80,12 @@ __device__ __forceinline__ float row_sum(float v) {
   }));
 }
 
+template <int LPR>
+__device__ __forceinline__ float row_max_float(float v) {
+  return __uint_as_float(row_reduce<LPR>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
@@ -238,11 +254,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
     }
     // scores of the choices, and of all where they are divided by their sum
     const float top = choices.logit((uint32_t)__shfl((int)key[0], sub * LPR));
+    const float base = p.renorm ? score_base(top) : 0.f;
     float w[H], sum = 0.f;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const float v = choices.logit(key[h]);
-      w[h] = h * LPR + pos >= k ? 0.f : p.sigm ? 1.f / (1.f + expf(-v)) : top == -INFINITY ? 0.f : expf(v - top);
+      w[h] = h * LPR + pos >= k ? 0.f : p.sigm ? sigmoid_score(v, base) : top == -INFINITY ? 0.f : expf(v - top);
       sum += w[h];
     }
     if (p.renorm) {
@@ -388,32 +405,36 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteBackward p) {
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
-  top = __uint_as_float(row_reduce<LPR>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
+  top = row_max_float<LPR>(top);
   // the row's lane j holds slots j and LPR + j; an id outside the experts takes no part
   int id[H];
-  float dw[H], s[H], slope[H];
+  float dw[H], s[H], slope[H], v[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int j = h * LPR + pos;
     id[h] = -1;
-    dw[h] = s[h] = 0.f;
-    slope[h] = 1.f;
+    dw[h] = 0.f;
+    v[h] = -INFINITY;
     if (in && j < k) {
       const int e = p.ids[t * k + j];
       if (e >= 0 && e < p.E) {
         id[h] = e;
         dw[h] = p.dweights[t * k + j];
-        const float v = load_logit<EL>(p.logits, t * p.E + e);
-        if (p.sigm) {
-          s[h] = 1.f / (1.f + expf(-v));
-          slope[h] = 1.f / (1.f + expf(v));  // 1 - s would cancel: nothing is left of it from 17 on
-        } else {
-          s[h] = top == -INFINITY ? 0.f : expf(v - top);
-        }
+        v[h] = load_logit<EL>(p.logits, t * p.E + e);
       }
     }
+  }
+  float base = 0.f;
+  if (p.sigm && p.renorm) {
+    base = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < H; ++h) base = fmaxf(base, v[h]);
+    base = score_base(row_max_float<LPR>(base));
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    s[h] = p.sigm ? sigmoid_score(v[h], base) : top == -INFINITY ? 0.f : expf(v[h] - top);
+    slope[h] = p.sigm ? 1.f / (1.f + expf(v[h])) : 1.f;  // 1 - s would cancel: nothing is left of it from 17 on
   }
   const bool dense = !p.sigm && !p.renorm;  // every expert has a share
   float x[PER], total = 1.f;

@@ -52,3 +52,35 @@ def test_sigmoid_gradient_keeps_its_relative_precision(dtype, renorm, lo, hi):
     lim = U[dtype] * np.abs(exact) + (4 * hi + k + 40) * E24 * mag + FLOOR[dtype]
     bad = ~(np.abs(got - exact) <= lim)
     assert not bad.any(), f"{int(bad.sum())} of {bad.size}, worst {np.max(np.abs(got - exact) / (lim + 1e-300)):.3g} times"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("E,k", [(24, 5), (300, 8), (3, 3)])
+def test_renormalised_sigmoids_below_the_range_of_fp32(dtype, E, k):
+    """Every logit so low that fp32 holds its sigmoid as 0 or subnormally: the weights are
+    still the scores divided by their sum, and the gradient theirs."""
+    T = 40
+    l = (-torch.linspace(80, 700, T)[:, None] - 6 * torch.rand(T, E, generator=torch.Generator().manual_seed(E))).to(dtype)
+    L, dw = to64(l), torch.randn(T, k, generator=torch.Generator().manual_seed(k))
+    got = forward(l.to(DEV), k, True, True)
+    ids, w = eb.route(L, k, True, True)
+    assert np.array_equal(got["ids"].cpu().numpy(), ids)
+    n = (4 * 20 + k + 40) * E24  # the exponentials' arguments are differences of at most 6 and a step of the type
+    assert (np.abs(to64(got["weights"]) - w) <= n * w).all()
+    D = dw.numpy().astype(np.float64)
+    exact, mag = np.zeros((T, E)), np.zeros((T, E))  # slopes are 1
+    np.put_along_axis(exact, ids, w * (D - (D * w).sum(1, keepdims=True)), 1)
+    np.put_along_axis(mag, ids, w * (np.abs(D) + (np.abs(D) * w).sum(1, keepdims=True)), 1)
+    assert (np.abs(backward(l, ids, dw, True, True) - exact) <= U[dtype] * np.abs(exact) + n * mag + FLOOR[dtype]).all()
+    alone = forward(l.to(DEV), k, True, False)["weights"]  # not renormalised: the small numbers themselves
+    s = np.exp(np.take_along_axis(L, ids, 1))
+    assert (np.abs(to64(alone) - s) <= (4 * 90 + 40) * E24 * s + 2.0 ** -148).all()
+
+
+def test_a_types_lowest_value_masks_sigmoids():
+    for dtype in (F32, BF16):
+        l = torch.full((3, 9), float(torch.finfo(dtype).min), dtype=dtype)
+        l[1, 4] = -1.0
+        l[2, 2] = l[2, 7] = -800.0
+        got = forward(l.to(DEV), 2, True, True)
+        assert got["ids"].tolist() == [[0, 1], [4, 0], [2, 7]] and got["weights"].tolist() == [[0, 0], [1, 0], [0, 0]]
