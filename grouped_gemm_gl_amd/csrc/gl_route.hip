@@ -419,8 +419,9 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteBackward p) {
       const int e = p.ids[t * k + j];
       if (e >= 0 && e < p.E) {
         id[h] = e;
-        dw[h] = p.dweights[t * k + j];
+        const float d = p.dweights[t * k + j];
         v[h] = load_logit<EL>(p.logits, t * p.E + e);
+        dw[h] = v[h] > -INFINITY ? d : 0.f;  // a masked slot's may be anything, NaN too
       }
     }
   }

@@ -551,7 +551,8 @@ int gl_route_forward(int64_t total_rows, int num_experts, int top_k, gl_dtype dt
 /*
  * Gradient of the routing weights: dlogits [T, E] of dtype from dweights float
  * [T, top_k], at the logits and ids of gl_route_forward (the choice itself has no
- * gradient).  Masked experts and tokens get 0.  An id outside [0, E) takes no part.
+ * gradient).  Masked experts and tokens get 0, whatever dweights holds for them.  An id
+ * outside [0, E) takes no part.
  */
 int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype dtype, int score, int renormalize,
                       const void *logits, const int32_t *ids, const float *dweights, void *dlogits,

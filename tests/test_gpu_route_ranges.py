@@ -84,3 +84,21 @@ def test_a_types_lowest_value_masks_sigmoids():
         l[2, 2] = l[2, 7] = -800.0
         got = forward(l.to(DEV), 2, True, True)
         assert got["ids"].tolist() == [[0, 1], [4, 0], [2, 7]] and got["weights"].tolist() == [[0, 0], [1, 0], [0, 0]]
+
+
+@pytest.mark.parametrize("E,k", [(12, 4), (300, 6)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_masked_slots_take_no_part_in_the_gradient(E, k, bad):
+    """dweights of slots that a mask left (weight 0) may be NaN or infinite."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(9, E, generator=g)
+    l[1:, 2:] = -float("inf")  # two experts left
+    l[8] = float("nan")  # none
+    dw = torch.randn(9, k, generator=g)
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            ids, w = eb.route(to64(l), k, sigmoid, renorm)
+            broken = torch.where(torch.from_numpy(w) == 0, torch.tensor(bad), dw)
+            got = backward(l, ids, broken, sigmoid, renorm)
+            assert np.array_equal(got, backward(l, ids, dw, sigmoid, renorm))
+            assert np.abs(got[1:, 2:]).max() == 0 and np.abs(got[8]).max() == 0
