@@ -422,18 +422,30 @@ static void each_split(int64_t vectors, F f, L too_long) {
 hipError_t launch_rmsnorm_fwd(int el, bool g32, int64_t T, int64_t C, const void *x, const void *residual,
                               const void *gamma, float eps, void *h, void *y, uint8_t *data, uint8_t *scale,
                               hipStream_t s) {
-  const NormForward p{(const char *)x, (const char *)residual, (const char *)gamma, (char *)h, (char *)y,
-                      data, scale, T, C, eps};
+  // f(a slice of the rows, its workgroups)
+  const auto slices = [&](int threads, int rows, auto f) {
+    const int64_t step = kSliceThreads / threads * rows, row = C * elem_bytes(el);
+    const auto at = [](auto *q, int64_t bytes) { return q ? q + bytes : nullptr; };
+    for (int64_t t = 0; t < T; t += step) {
+      const int64_t n = min64(T - t, step);
+      f(NormForward{(const char *)x + t * row, at((const char *)residual, t * row), (const char *)gamma,
+                    at((char *)h, t * row), at((char *)y, t * row), at(data, t * C), at(scale, t * (C / 32)), n, C, eps},
+        dim3((unsigned)((n + rows - 1) / rows)));
+    }
+  };
   each_type(el, g32, [&](auto e, auto g) {
     each_split<true>(
         C / Vec<e()>::n,
         [&](auto nt, auto vpt) {
-          constexpr int rows = RowSplit<nt()>::rows;
-          hipLaunchKernelGGL((rmsnorm_fwd_kernel<e(), g(), nt(), vpt()>), dim3((unsigned)((T + rows - 1) / rows)),
-                             dim3(RowSplit<nt()>::threads), 0, s, p);
+          using S = RowSplit<nt()>;
+          slices(S::threads, S::rows, [&](const NormForward &p, dim3 grid) {
+            hipLaunchKernelGGL((rmsnorm_fwd_kernel<e(), g(), nt(), vpt()>), grid, dim3(S::threads), 0, s, p);
+          });
         },
         [&] {
-          hipLaunchKernelGGL((rmsnorm_fwd_long_kernel<e(), g()>), dim3((unsigned)T), dim3(kNormThreads), 0, s, p);
+          slices(kNormThreads, 1, [&](const NormForward &p, dim3 grid) {
+            hipLaunchKernelGGL((rmsnorm_fwd_long_kernel<e(), g()>), grid, dim3(kNormThreads), 0, s, p);
+          });
         });
   });
   return hipGetLastError();

@@ -48,6 +48,10 @@ struct Vec<EL_BF16> : Vec16<EL_BF16> {};
 template <>
 struct Vec<EL_F16> : Vec16<EL_F16> {};
 
+// A launch may have fewer than 2^32 threads: grids that grow with the rows go out in slices of
+// at most this many.
+constexpr int64_t kSliceThreads = (int64_t)1 << 31;
+
 constexpr int elem_bytes(int el) { return el == EL_F32 ? 4 : 2; }
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
