@@ -207,7 +207,7 @@ struct RouteForward {
   unsigned long long *masks;  // [chunks][E] tokens of the chunk that chose the expert, or null
   int64_t *m_splits;
   int32_t *row_index, *slot_index;
-  int64_t T;
+  int64_t T, chunk0;  // chunk0: of the launch's first workgroup
   int E, k, sigm, renorm, whole;
 };
 
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
   constexpr int LPR = R::LPR, PER = R::PER, H = LPR == 64 ? 1 : 2;
   __shared__ unsigned long long mask[kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPR, pos = lane % LPR;
-  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  const int64_t chunk = p.chunk0 + blockIdx.x, t0 = chunk * kChunk;
   const int e0 = pos * PER, k = p.k;
   constexpr int kRounds = kChunk / (kRouteWaves * R::rows);
   int id[kRounds][H];  // the row's lane j keeps choices j and, of 16 lanes, 16 + j; -1: none
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteF
   each_slot([&](int r, int, int e) { atomicOr(&mask[e], 1ull << r); });
   __syncthreads();
   if (p.T > kChunk) {
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.masks[(int64_t)blockIdx.x * p.E + e] = mask[e];
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.masks[chunk * p.E + e] = mask[e];
     return;
   }
   // the only chunk: an expert's rows start at the sum of the counts before it
@@ -339,15 +339,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(const unsigne
 
 // The rows of a chunk's slots: the experts' starts (a scan of the totals, made by every
 // workgroup), the chunk's within the expert, and the rank within the chunk.
-__global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t *__restrict__ ids, int64_t T, int E,
-                                                                   int k, const unsigned long long *__restrict__ masks,
+__global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t *__restrict__ ids, int64_t T,
+                                                                   int64_t chunk0, int E, int k,
+                                                                   const unsigned long long *__restrict__ masks,
                                                                    const int32_t *__restrict__ base,
                                                                    const int64_t *__restrict__ m_splits,
                                                                    int32_t *__restrict__ row_index,
                                                                    int32_t *__restrict__ slot_index) {
   __shared__ int start[kRouteMaxExperts];
   __shared__ unsigned long long mask[kRouteMaxExperts];
-  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  const int64_t chunk = chunk0 + blockIdx.x, t0 = chunk * kChunk;
   const int n = (int)min64(kChunk, T - t0) * k;
   constexpr int kSlots = kChunk * kRouteMaxTopK / kRouteThreads;  // slots of a thread
   int id[kSlots];  // loaded with the tables, so that the scan does not wait twice
@@ -360,8 +361,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(const int32_t
   int total = 0, here = 0;
   if (e < E) {
     total = (int)m_splits[e];
-    here = base[(int64_t)blockIdx.x * E + e];
-    mask[e] = masks[(int64_t)blockIdx.x * E + e];
+    here = base[chunk * E + e];
+    mask[e] = masks[chunk * E + e];
   }
   start[e] = block_scan(total) - total + here;
   __syncthreads();
@@ -527,30 +528,45 @@ hipError_t launch_route_fwd(int el, int64_t T, int E, int k, int sigm, int renor
                             float *weights, int64_t *m_splits, int32_t *row_index, int32_t *slot_index, void *ws,
                             hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const RouteForward p{logits, ids, weights, (unsigned long long *)ws, m_splits, row_index, slot_index,
-                       T, E, k, sigm, renorm, whole_rows(el, E)};
-  // (no tokens: one workgroup writes the counts)
-  const dim3 grid((unsigned)(chunks ? chunks : 1)), block(kRouteThreads);
+  RouteForward p{logits, ids, weights, (unsigned long long *)ws, m_splits, row_index, slot_index,
+                 T, 0, E, k, sigm, renorm, whole_rows(el, E)};
+  const dim3 block(kRouteThreads);
+  // f(first chunk, workgroups) of every slice of the chunks (no tokens: one workgroup writes
+  // the counts)
+  const auto slices = [&](auto f) {
+    constexpr int64_t step = kSliceThreads / kRouteThreads;
+    for (int64_t c = 0; c == 0 || c < chunks; c += step) f(c, dim3((unsigned)(chunks ? min64(chunks - c, step) : 1)));
+  };
   each_route(el, E, [&](auto e, auto r) {
-    hipLaunchKernelGGL((route_gates_kernel<e(), decltype(r)>), grid, block, 0, s, p);
+    slices([&](int64_t c, dim3 grid) {
+      p.chunk0 = c;
+      hipLaunchKernelGGL((route_gates_kernel<e(), decltype(r)>), grid, block, 0, s, p);
+    });
   });
   if (m_splits && chunks > 1) {
     int32_t *base = (int32_t *)(p.masks + chunks * E);
     hipLaunchKernelGGL(route_scan_kernel, dim3((unsigned)((E + 15) / 16)), block, 0, s, p.masks,
                        chunks, E, base, m_splits);
-    hipLaunchKernelGGL(route_rows_kernel, grid, block, 0, s, ids, T, E, k, p.masks, base, m_splits, row_index,
-                       slot_index);
+    slices([&](int64_t c, dim3 grid) {
+      hipLaunchKernelGGL(route_rows_kernel, grid, block, 0, s, ids, T, c, E, k, p.masks, base, m_splits, row_index,
+                         slot_index);
+    });
   }
   return hipGetLastError();
 }
 
 hipError_t launch_route_bwd(int el, int64_t T, int E, int k, int sigm, int renorm, const void *logits,
                             const int32_t *ids, const float *dweights, void *dlogits, hipStream_t s) {
-  const RouteBackward p{logits, ids, dweights, dlogits, T, E, k, sigm, renorm, whole_rows(el, E)};
   each_route(el, E, [&](auto e, auto r) {
-    const int64_t rows = 4 * decltype(r)::rows;
-    hipLaunchKernelGGL((route_bwd_kernel<e(), decltype(r)>), dim3((unsigned)((T + rows - 1) / rows)), dim3(256), 0, s,
-                       p);
+    constexpr int64_t rows = 4 * decltype(r)::rows, step = kSliceThreads / 256 * rows;
+    const int64_t row = (int64_t)E * elem_bytes(e());
+    for (int64_t t = 0; t < T; t += step) {
+      const int64_t n = min64(T - t, step);
+      const RouteBackward p{(const char *)logits + t * row, ids + t * k, dweights + t * k, (char *)dlogits + t * row,
+                            n, E, k, sigm, renorm, whole_rows(el, E)};
+      hipLaunchKernelGGL((route_bwd_kernel<e(), decltype(r)>), dim3((unsigned)((n + rows - 1) / rows)), dim3(256), 0,
+                         s, p);
+    }
   });
   return hipGetLastError();
 }
