@@ -744,6 +744,7 @@ int gl_rmsnorm_forward(int64_t total_rows, int64_t features, gl_dtype dtype, gl_
   if (T == 0) return ok();
   if ((data == nullptr) != (scale == nullptr)) return fail(GL_ERR_ARG, "%s: give both data and scale, or neither", who);
   if (!y && !data) return fail(GL_ERR_ARG, "%s: neither y nor data is given", who);
+  if (h && h == y) return fail(GL_ERR_ARG, "%s: h and y are the same buffer", who);
   GL_TRY(check_buf(x, T, "x"));
   if (!aligned16(residual) || !aligned16(h) || !aligned16(y) || !aligned16(data))
     return fail(GL_ERR_ARG, "%s: buffers must be 16-byte aligned", who);

@@ -134,3 +134,8 @@ def test_binding_refuses_on_the_host():
             gl.gl_moe_few_tokens(**a)
     with pytest.raises(ValueError):
         gl.gl_moe_few_tokens(x, ids, w, w1, w2, y, ws, b1=z(4, 63))
+
+
+def test_rmsnorm_forward_refuses_one_buffer_for_h_and_y():
+    assert norm(h=C_, y=C_) == -1 and "same buffer" in gl.load().gl_last_error().decode()
+    assert norm(T=0, x=None, h=C_, y=C_) == 0  # no rows: nothing to write
