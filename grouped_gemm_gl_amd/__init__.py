@@ -713,9 +713,12 @@ def gl_moe_few_tokens(x: Tensor, ids: Tensor, weights: Tensor, w1: Grouped, w2: 
     _each_shape(b2, E, (N,), x.dtype, "b2")
     _enough(workspace, gl_moe_few_tokens_workspace_size(T, k, E, F))
     px, pi, pw, pr, py, ws = _addresses(x, ids, weights, residual, y, workspace)
-    for g in (w1, w2, w1_scale, w2_scale, b1, b2):
+    for g, what, align in ((w1, "w1", 16), (w2, "w2", 16), (w1_scale, "w1_scale", 4), (w2_scale, "w2_scale", 4),
+                           (b1, "b1", 1), (b2, "b2", 1)):
         if g is not None:
-            _addresses(x, *((g,) if isinstance(g, Tensor) else g))
+            at = _addresses(x, *((g,) if isinstance(g, Tensor) else g))[1:]
+            if not isinstance(g, Tensor) and any(a % align for a in at):  # the library sees only their array
+                raise ValueError(f"every expert's {what} must be {align}-byte aligned")
     p1, pp1, k1 = _grouped(w1, x.device, stream)
     p2, pp2, k2 = _grouped(w2, x.device, stream)
     s1, ss1, k3 = _grouped(w1_scale, x.device, stream)

@@ -573,8 +573,9 @@ int gl_route_backward(int64_t total_rows, int num_experts, int top_k, gl_dtype d
  *   ids      int32 [T, top_k]; a slot whose id is outside [0, E) takes no part (an expert
  *            held by another device), nor does a slot of weight 0
  *   weights  float [T, top_k]
- *   w1, w2   [E, 2F, K] and [E, N, F], stacked or as device pointer arrays, scales in
- *            the same form [E, rows, cols / 32]; b1 [E, 2F], b2 [E, N] or none.  SwiGLU
+ *   w1, w2   [E, 2F, K] and [E, N, F], stacked or as device pointer arrays, 16-byte
+ *            aligned (each expert's), scales in the same form [E, rows, cols / 32], 4-byte
+ *            aligned; b1 [E, 2F], b2 [E, N] or none.  SwiGLU
  *            as in gl_swiglu_forward: the first F rows of W1 are the gate's
  *   residual [T, N], or NULL; may be y itself
  *   y        [y_rows, N], y_rows >= T; rows >= T are never written.  A token without a

@@ -127,3 +127,16 @@ def test_infinite_values_between_the_products(T, dtype):
         ref = eb.moe(to64(c["x"]), c["ids"].numpy(), to64(c["weights"]), to64(c["w1"]), to64(c["w2"]))
     hit = c["ids"][:, 0].numpy() == 1
     assert np.isinf(ref[hit]).all() and np.array_equal(y[hit], ref[hit]) and np.isfinite(y[~hit]).all()
+
+
+def test_misaligned_matrices_of_an_expert_are_refused():
+    """Per-expert weights off a 16-byte boundary, scales off a 4-byte one: refused on the host."""
+    for mx, name, off in ((False, "w1", 1), (False, "w2", 4), (True, "w1", 8), (True, "w1_scale", 2), (True, "w2_scale", 1)):
+        c = case(1, 3, 2, 1, 64, 64, 32, BF16, mx=mx)
+        names = ["w1", "w2"] + (["w1_scale", "w2_scale"] if mx else [])
+        lists = {n: [t.cuda().clone() for t in c[n]] for n in names}
+        run(c, **lists)
+        t = lists[name][1]
+        lists[name][1] = torch.cat([t.reshape(-1), t.reshape(-1)])[off:off + t.numel()].view(t.shape)
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            run(c, **lists)
