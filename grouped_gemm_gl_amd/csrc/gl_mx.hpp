@@ -8,10 +8,11 @@ namespace gl {
 // E4M3 codes of four finite floats (already scaled into the block's range), packed
 // one per byte: round to nearest even, magnitudes above 448 saturate to 448, the sign
 // bit is kept (also for zero).  gfx950's pack conversion to OCP E4M3 rounds to
-// nearest even and keeps the sign; the clamp first makes overflow saturate.  Over
-// every value the quantizers can pass (8 significant bits, exponents -149 .. 9, both
-// signs) it gives the same bytes as the rule spelled out (checked exhaustively on
-// the device).
+// nearest even and keeps the sign; the clamp first makes overflow saturate.  It gives
+// the same bytes as the rule spelled out: over every bf16 value (8 significant bits,
+// exponents -149 .. 9, both signs) checked exhaustively on the device, and for the
+// 24-bit values of quantize_lanes at every code, every middle of two codes, the
+// saturated range and one fp32 step to either side of each (tests of the RMS norm).
 __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
   const auto sat = [](float v) { return __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f); };
   uint32_t o = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
