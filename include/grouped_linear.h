@@ -479,7 +479,8 @@ int gl_forward_noalloc(int num_groups, int64_t in_features, int64_t out_features
 
 /*
  * RMS norm with the residual's addition (the norm in front of the layer's experts and
- * router; its MXFP8 output is the E4M3 operand of gl_forward):
+ * router; its MXFP8 output, rows of codes and scales gathered into the experts' order by
+ * gl_route_forward's slot_index, is the E4M3 operand of gl_forward):
  *   s = x + residual,  h = s,  y = s * rstd * gamma,
  *   rstd = (mean over the row of s^2 + eps)^-1/2
  * computed in fp32; h, y and the codes are each rounded once from the fp32 values (the
