@@ -49,7 +49,7 @@ namespace gl {
 enum { EL_MX = 3, EL_MX_RAGGED = 4 };
 typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 constexpr bool is_mx(int wel) { return wel >= EL_MX; }
-constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxTokens = 64, kCUs = 256;
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
 // Units that a wave takes at a time, in the up kernel (an MXFP8 unit holds twice the k values)
 // and in the down kernel (MXFP8, 17 tokens over 32 experts of 4096/2048: 44.3 us, 2 units 46.2).
@@ -1069,14 +1069,18 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
     hipLaunchKernelGGL((moe_down_kernel<EL, WEL, r(), nv(), many()>), dim3((unsigned)((p.N + r() - 1) / r())),
                        dim3(kDownThreads), lds, s, p);
   };
-  // Rows of a workgroup: 16, or 8 where 16 would leave CUs without one (one token, 8 experts
-  // of 768 into 2048: 9.3 us, with 16 rows 10.6)
+  // Rows of a workgroup: 8 as long as no CU gets a second one (call over 64 experts of 2048/768,
+  // top 8: 16 tokens into N = 2048 117 us, by 16 rows 125; into 1024 109 and 121), else 16, whose
+  // loads share the tokens' between more rows (64 tokens over 32 experts of 2880/2880 into 2880:
+  // 367 us, by 8 rows 456; 17 tokens in MXFP8 codes, 32 experts of 4096/2048, into 2176: 150 and
+  // 167).  The short workgroups of one token go without MXFP8 codes as well by two on a CU (one
+  // token, 64 experts of 2048/768, into 4032: 8 rows 25.0 us, 16 26.3; into 7168 33.7 and 31.6).
   const auto by_tokens = [&](auto r) {
     if (p.T == 1) go_down(r, One(), std::false_type());
     else if (p.T == 2) go_down(r, Two(), std::false_type());
     else go_down(r, Few(), std::true_type());
   };
-  if (p.N / 16 < 256) by_tokens(integral_constant<int, 8>());
+  if (p.N <= 8 * kCUs || (p.T == 1 && !is_mx(WEL) && p.N < 16 * kCUs)) by_tokens(integral_constant<int, 8>());
   else by_tokens(integral_constant<int, 16>());
 }
 

@@ -140,3 +140,10 @@ def test_misaligned_matrices_of_an_expert_are_refused():
         lists[name][1] = torch.cat([t.reshape(-1), t.reshape(-1)])[off:off + t.numel()].view(t.shape)
         with pytest.raises(ValueError, match=f"{name} must be"):
             run(c, **lists)
+
+
+@pytest.mark.parametrize("T,N", [(1, 2048), (1, 2056), (1, 4088), (1, 4096), (2, 2048), (2, 2056), (9, 2040), (9, 2056), (20, 2064)])
+@pytest.mark.parametrize("dtype,mx", [(F16, False), (BF16, False), (F32, False), (BF16, True)])
+def test_output_widths_where_the_workgroups_change(T, N, dtype, mx):
+    c = case(T + N + 4, T, 3, 2, 64, 96, N, dtype, mx=mx)
+    check(c)
