@@ -277,9 +277,8 @@ __device__ __forceinline__ float join(float leading, float rest) {
 // The lanes of a token's two columns each load and split half of the 8 values that both need,
 // so a load takes whole lines (8 rows by 128 bytes: 64 tokens over 8 experts of 4096/14336 take
 // 704 us, 711 where each lane loads 32 bytes of its own), and change halves by rotations.  The
-// splitting is some 150 instructions an item that its wave waits for: fp16 values stored in
-// two unscaled parts, as bf16's are, would take 360 us and not 385 for 5 tokens over those
-// experts, and 695 for the 64, but hold neither 70000 nor 16 bits of 10^-3.
+// splitting is some 150 instructions an item that its wave waits for (stored unscaled parts, as
+// bf16's are, took 695 us there, but hold neither 70000 nor 16 bits of 10^-3).
 constexpr float kRestScale = 2048.f;
 template <class W, int U>
 struct ScaledColumns {
@@ -1054,8 +1053,11 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   // MXFP8 codes, for the experts of one or two tokens, where the MFMA's columns would load
   // 256 bytes of activations for every 128 of codes (8 tokens over 32 experts of 4096/1920:
   // up 53.5 us, all by MFMA 55.7; 17 over 32 of 4096/2048: down 44.3 and 46.1; bf16 does as
-  // well by MFMA).
+  // well by MFMA), and in the down kernel beside fp16 weights, whose MFMA steps have to split a
+  // (calls of 5 tokens over 8 experts of 4096/14336: 374 us, all by MFMA 384; 32 tokens, top 6
+  // of 64 experts of 2048/1408: 227 and 249; 64 over the 8: 703 both).
   using Few = integral_constant<int, is_mx(WEL) ? 2 : 0>;
+  using FewDown = integral_constant<int, is_mx(WEL) || EL == EL_F16 ? 2 : 0>;
   if (p.T == 1) go_up(One(), Zero());
   else if (p.T == 2) go_up(Two(), Zero());
   else if (p.T <= 4 && !is_mx(WEL)) go_up(integral_constant<int, is_mx(WEL) ? 2 : 4>(), Zero());
@@ -1078,7 +1080,7 @@ static void launch_moe_typed(const MoeParams &p, hipStream_t s) {
   const auto by_tokens = [&](auto r) {
     if (p.T == 1) go_down(r, One(), std::false_type());
     else if (p.T == 2) go_down(r, Two(), std::false_type());
-    else go_down(r, Few(), std::true_type());
+    else go_down(r, FewDown(), std::true_type());
   };
   if (p.N <= 8 * kCUs || (p.T == 1 && !is_mx(WEL) && p.N < 16 * kCUs)) by_tokens(integral_constant<int, 8>());
   else by_tokens(integral_constant<int, 16>());
