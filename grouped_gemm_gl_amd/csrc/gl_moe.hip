@@ -9,7 +9,8 @@
 // layout of the MFMA's operand, streams 4.2 TB/s where one that takes 1 KiB of a row streams
 // 5.9 (67 MB over 512 workgroups; 16 rows of 8 would cost the same again).  So every weight
 // goes straight from memory to the registers of the one wave that uses it, no load takes less
-// than whole 128-byte lines, and the next loads are in flight during the products:
+// than whole 128-byte lines, and the next loads are in flight during the products (but for the
+// W2 kernel's MFMA steps, see down_many):
 //
 //   - experts of many tokens by MFMA steps of 16 weight rows by 16 columns, the columns being
 //     the expert's tokens, compacted; loads of 8 rows by 128 bytes and a rotation of 8 lanes
@@ -35,9 +36,9 @@
 // or 2^-49 of the largest of the 256 is lost, over fp32's whole range.  Its dot products take
 // the fp32 values as they are.
 //
-// Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.83 ms (7.1
+// Measured (kernel times): 64 tokens over 256 experts of 7168/2048, bf16: up 1.85 ms (7.0
 // TB/s of weights), down 1.11 ms (5.9 TB/s: 448 workgroups over 256 CUs); one token, 8 of 64
-// experts of 2048/768: up 12.4 us, down 8.6 us, half of it latency.
+// experts of 2048/768: up 12.7 us, down 9.0 us, half of it latency.
 #include <type_traits>
 
 #include "gl_vec.hpp"
@@ -717,7 +718,8 @@ __device__ __forceinline__ void up_many(const MoeParams &p, const UpTokens &tok,
 template <int NT>
 constexpr int up_threads() { return NT ? kUpThreads : kUpThreads / 2; }
 // Waves a SIMD that the registers have to allow: three (17 tokens over 32 experts of 4096/2048
-// in MXFP8 codes: 74 us, 81 at the two that the compiler settles for); four tiles would spill.
+// in MXFP8 codes: 74 us, 81 at the two that the compiler settles for), for which two tiles of
+// MXFP8 codes spill 8 registers; four tiles would spill more.
 template <int NT>
 constexpr int up_waves() { return NT == 1 || NT == 2 ? 3 : 1; }
 
@@ -879,7 +881,12 @@ __device__ __forceinline__ void down_vector(const MoeParams &p, const DownPlace 
 }
 
 // The other entries: items (entry, U units of F), dealt to the waves in turn, 16 rows by
-// the entry's tokens in MFMA steps.
+// the entry's tokens in MFMA steps.  The branches around the next item's loads (the last item,
+// an array of addresses, the loop over tokens) make the compiler wait for them before the
+// products, so a CU's other waves cover a step's time.  Without them (loads that go nowhere
+// after the last item, addresses by scalar loads, the first tokens apart) small layers gained
+// and large ones lost: 20 tokens over 32 experts of 2048/1024 in fp32 184 -> 172 us, 64 over
+// 256 of 7168/2048 in bf16 3.02 -> 3.12 ms, 64 over 8 of 4096/14336 in fp16 703 -> 716 us.
 template <int EL, int WEL, int R>
 __device__ __forceinline__ void down_many(const MoeParams &p, const DownPlace &o) {
   using W = Unit<WEL, R>;

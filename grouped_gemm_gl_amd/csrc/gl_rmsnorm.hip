@@ -12,8 +12,8 @@
 //
 // Bound by HBM: a row is held in registers between its sum and its output, so every value
 // is read once and written once.  16384 rows of 4096 bf16: forward with residual, h, y and
-// codes (606 MB) 106 us, 5.7 TB/s; backward with dh and dgamma (537 MB) 108 us for dx and the
-// partial sums of dgamma and 5 us for their addition, 4.8 TB/s.  (A copy of 2 GiB reaches
+// codes (606 MB) 102 us, 5.9 TB/s; backward with dh and dgamma (537 MB) 109 us for dx and the
+// partial sums of dgamma and 5 us for their addition, 4.7 TB/s.  (A copy of 2 GiB reaches
 // 4.9 TB/s, reads and writes counted.)
 #include <type_traits>
 

@@ -8,9 +8,9 @@
 // chosen scores divided by their sum (for softmax: a softmax over the chosen logits).
 // A token whose experts are all masked gets weights 0.
 //
-// 32768 tokens over 256 experts, bf16, top 8: gates 14.0 us, scan 4.2, rows 5.6 (21 MB in
-// all); 32 tokens over 64 experts with their plan, one launch, 4.0 us; the gradient of
-// 16384 x 64 fp32 5.0 us.
+// 32768 tokens over 256 experts, bf16, top 8: gates 14.3 us, scan 4.7, rows 5.2 (21 MB in
+// all); 32 tokens over 64 experts with their plan, one launch, 4.1 us; the gradient of
+// 16384 x 64 fp32 6.3 us (5.0 out of the last-level cache).
 #include <type_traits>
 
 #include "gl_vec.hpp"
@@ -218,7 +218,8 @@ struct RouteForward {
 //
 // Bound by instructions and, for few tokens, latency: k rounds over the keys that the
 // row's lanes hold.  (Sorting each lane's keys first, so that a round looks at one, took
-// four times as long: the keys that sort need 64 bits.)
+// four times as long with keys of 64 bits, value and expert; with the 32-bit keys that
+// 16-bit logits have now it has not been tried.)
 template <int EL, class R>
 __global__ __launch_bounds__(kRouteThreads) void route_gates_kernel(const RouteForward p) {
   constexpr int LPR = R::LPR, PER = R::PER, H = LPR == 64 ? 1 : 2;

@@ -528,6 +528,8 @@ int gl_rmsnorm_backward(int64_t total_rows, int64_t features, gl_dtype dtype, gl
  *            the chosen experts; GL_SCORE_SIGMOID: the sigmoid of the chosen logits.
  *            renormalize = 1: divided by their sum over the token's slots (sigmoids of
  *            logits that are all below -745 count as 0, as masks do).
+ *            The choice is always by the logits that weigh: routers that choose by a
+ *            corrected score (a bias per expert) but weigh by the plain one are not covered
  * A logit of -inf masks its expert: it is chosen only when fewer than top_k others are
  * left, and weighs 0 then, so a token that is masked everywhere has top_k ids of weight
  * 0.  NaN counts as -inf, +inf as the largest finite value.
