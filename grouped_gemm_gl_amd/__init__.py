@@ -32,12 +32,15 @@ __all__ = [
     "NOALLOC_MAX_GROUPS", "gl_rmsnorm_forward", "gl_rmsnorm_workspace_size", "gl_rmsnorm_backward",
     "GL_SCORE_SOFTMAX", "GL_SCORE_SIGMOID", "gl_route_workspace_size", "gl_route_forward", "gl_route_backward",
     "gl_moe_few_tokens_workspace_size", "gl_moe_few_tokens", "MOE_MAX_TOKENS",
+    "GL_GLU_SILU", "GL_GLU_GELU", "GL_GLU_GELU_TANH", "gl_glu_forward", "gl_glu_backward",
+    "gl_quantize_int8", "gl_forward_int8", "gl_glu_forward_int8",
 ]
 
 GL_F32, GL_BF16, GL_F16, GL_E4M3 = 0, 1, 2, 3
 NOALLOC_MAX_GROUPS = 16384  # GL_NOALLOC_MAX_GROUPS
 GL_SCORE_SOFTMAX, GL_SCORE_SIGMOID = 0, 1
 MOE_MAX_TOKENS = 64  # GL_MOE_MAX_TOKENS
+GL_GLU_SILU, GL_GLU_GELU, GL_GLU_GELU_TANH = 0, 1, 2
 GL_STATUS_NEGATIVE_SPLIT, GL_STATUS_SUM_MISMATCH, GL_STATUS_WORKSPACE = 1, 2, 4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -107,6 +110,11 @@ def load():
         "gl_route_backward": (I, [I64, I, I, I, I, I] + [P] * 5),
         "gl_moe_few_tokens_workspace_size": (ctypes.c_size_t, [I64, I, I, I64]),
         "gl_moe_few_tokens": (I, [I, I64, I64, I64, I64, I, I, I] + [P] * 17 + [I64, P, P]),
+        "gl_glu_forward": (I, [I, I64, I64, I64, I, I] + [P] * 7 + [I64, P, P]),
+        "gl_glu_backward": (I, [I, I64, I64, I64, I, I, I] + [P] * 10 + [I64] + [P] * 4 + [I, P, P]),
+        "gl_quantize_int8": (I, [I64, I64, I, P, P, P, P]),
+        "gl_forward_int8": (I, [I, I64, I64, I64, I] + [P] * 9 + [I64, P, P]),
+        "gl_glu_forward_int8": (I, [I, I64, I64, I64, I, I] + [P] * 9 + [I64, P, P]),
         "gl_last_error": (ctypes.c_char_p, []),
         "gl_version": (ctypes.c_char_p, []),
     }
@@ -730,6 +738,152 @@ def gl_moe_few_tokens(x: Tensor, ids: Tensor, weights: Tensor, w1: Grouped, w2: 
                                     _stream(stream)))
     del k1, k2, k3, k4, k5, k6
     return y
+
+
+# ------------------------------------------------- gated layer, 8-bit integers
+
+
+def _on_current_device(x: Tensor) -> None:
+    """The launch goes to the current device, so its tensors have to be there."""
+    if x.is_cuda and x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {x.device}, which is not the current device")
+
+
+def _grouped_on(x: Tensor, stream, **groups):
+    """Stacked address and pointer array of each stacked tensor or list, all on x's device,
+    contiguous, each 16-byte aligned (scales: 4), and what to keep alive until the call is made."""
+    at, keep = [], []
+    for what, g in groups.items():
+        if g is None:
+            at += [None, None]
+            continue
+        align = 4 if what.endswith("scale") else 16
+        each = _addresses(x, *((g,) if isinstance(g, Tensor) else g))[1:]
+        if any(a % align for a in each):
+            raise ValueError(f"{what} must be {align}-byte aligned (each group's)")
+        if isinstance(g, Tensor):
+            at += [each[0], None]
+        else:
+            ptrs = torch.tensor(each, dtype=torch.int64, device=x.device)
+            _record([ptrs], stream)
+            at += [None, ptrs.data_ptr()]
+            keep.append((ptrs, list(g)))
+    return at, keep
+
+
+def _glu_sizes(x: Tensor, w: Grouped, gated: bool):
+    """(G, K, N, F) of x [T, K] and the weights, which all have one shape and x's type."""
+    _on_current_device(x)
+    w0 = _first(w)
+    if x.dim() != 2 or w0.dim() != 2 or (isinstance(w, Tensor) and w.dim() != 3):
+        raise ValueError("x must be [T, K] and w [G, N, K] or G tensors [N, K]")
+    G = w.shape[0] if isinstance(w, Tensor) else len(w)
+    N, K = w0.shape[-2:]
+    if x.shape[1] != K or (gated and N % 2):
+        raise ValueError(f"x must be [T, {K}], and w have an even number of rows where they are gated")
+    _each_shape(w, G, (N, K), x.dtype, "w")
+    return G, K, N, N // 2 if gated else N
+
+
+def gl_glu_forward(x: Tensor, w: Grouped, a: Tensor, workspace: Tensor, *, bias: Optional[Grouped] = None,
+                   h: Optional[Tensor] = None, act: int = GL_GLU_SILU, stream=None) -> Tensor:
+    """a[:T] = act(h[:, :F]) * h[:, F:] with h = grouped x W_g^T (+ b_g), in one launch.
+
+    x: [T, K]; w: [G, 2F, K] or G tensors [2F, K], the gate's rows first; bias [G, 2F] or G
+    tensors [2F]; a: [>= T, F], rows past T are left untouched; h: [T, 2F] to keep for
+    ``gl_glu_backward``, or None.  One dtype (float32, bfloat16, float16)."""
+    G, K, N, F = _glu_sizes(x, w, True)
+    T = x.shape[0]
+    if a.dim() != 2 or a.shape[1] != F or a.dtype != x.dtype:
+        raise ValueError(f"a must be [rows >= {T}, {F}] of x's dtype")
+    if h is not None and (h.shape != (T, N) or h.dtype != x.dtype):
+        raise ValueError(f"h must be [{T}, {N}] of x's dtype")
+    _each_shape(bias, G, (N,), x.dtype, "bias")
+    px, ph, pa, ws = _addresses(x, h, a, workspace)
+    _enough(workspace, gl_workspace_size(G))
+    (pw, pww, pb, pbb), keep = _grouped_on(x, stream, w=w, bias=bias)
+    _check(load().gl_glu_forward(G, K, F, T, _dtype(x), int(act), px, pw, pww, pb, pbb, ph, pa, a.shape[0], ws,
+                                 _stream(stream)))
+    del keep
+    return a
+
+
+def gl_glu_backward(x: Tensor, w: Grouped, da: Tensor, dh: Tensor, dx: Optional[Tensor], dw: Grouped,
+                    workspace: Tensor, *, h: Optional[Tensor] = None, bias: Optional[Grouped] = None,
+                    a: Optional[Tensor] = None, db: Optional[Grouped] = None, act: int = GL_GLU_SILU,
+                    accumulate: bool = False, stream=None) -> Optional[Tensor]:
+    """Backward of gl_glu_forward for the gradient da [T, F] of a: dh [T, 2F] (the gradient of
+    h, a caller's buffer; may be h), dx[:T] (or None), dw (of x's dtype or float32, added into
+    with ``accumulate``) and db (of x's dtype).  ``h`` as the forward kept it, or None: computed
+    again from x, w and ``bias``.  ``a`` [T, F] receives the forward's output again."""
+    G, K, N, F = _glu_sizes(x, w, True)
+    T = x.shape[0]
+    for t, shape, what in ((da, (T, F), "da"), (dh, (T, N), "dh"), (h, (T, N), "h"), (a, (T, F), "a")):
+        if t is not None and (t.shape != shape or t.dtype != x.dtype):
+            raise ValueError(f"{what} must be [{shape[0]}, {shape[1]}] of x's dtype")
+    if dx is not None and (dx.dim() != 2 or dx.shape[1] != K or dx.dtype != x.dtype):
+        raise ValueError(f"dx must be [rows >= {T}, {K}] of x's dtype")
+    wd = _first(dw).dtype
+    _each_shape(dw, G, (N, K), wd, "dw")
+    _each_shape(bias, G, (N,), x.dtype, "bias")
+    _each_shape(db, G, (N,), x.dtype, "db")
+    px, ph, pda, pdh, pa, pdx, ws = _addresses(x, h, da, dh, a, dx, workspace)
+    _enough(workspace, gl_workspace_size(G))
+    (pw, pww, pb, pbb, pdw, pdww, pdb, pdbb), keep = _grouped_on(x, stream, w=w, bias=bias, dw=dw, db=db)
+    _check(load().gl_glu_backward(G, K, F, T, _dtype(x), _dtype(_first(dw)), int(act), px, pw, pww, pb, pbb, ph, pda,
+                                  pdh, pa, pdx, 0 if dx is None else dx.shape[0], pdw, pdww, pdb, pdbb,
+                                  int(bool(accumulate)), ws, _stream(stream)))
+    del keep
+    return dx
+
+
+def gl_quantize_int8(src: Tensor, data: Tensor, scale: Tensor, stream=None):
+    """Rows of src [..., cols] as int8 codes data (src's shape) and float32 scale [...]: a
+    token's activations, or with weights [G, N, K] a channel's."""
+    _on_current_device(src)
+    if src.dim() < 1 or data.shape != src.shape or data.dtype != torch.int8:
+        raise ValueError("data must be int8 of src's shape")
+    if scale.shape != src.shape[:-1] or scale.dtype != torch.float32:
+        raise ValueError("scale must be float32 with one value for each row of src")
+    cols = src.shape[-1]
+    at = _addresses(src, data, scale)
+    _check(load().gl_quantize_int8(src.numel() // cols if cols else 0, cols, _dtype(src), *at, _stream(stream)))
+    return data, scale
+
+
+def _int8(name: str, gated: bool, x, x_scale, w, w_scale, y, workspace, bias, act, stream) -> Tensor:
+    G, K, N, F = _glu_sizes(x, w, gated)
+    T = x.shape[0]
+    if x.dtype != torch.int8 or x_scale.shape != (T,) or x_scale.dtype != torch.float32:
+        raise ValueError("x must be int8 [T, K] and x_scale float32 [T]")
+    if y.dim() != 2 or y.shape[1] != F:
+        raise ValueError(f"the output must be [rows >= {T}, {F}]")
+    if isinstance(w, Tensor) != isinstance(w_scale, Tensor):
+        raise ValueError("w and w_scale must both be stacked or both be lists")
+    _each_shape(w_scale, G, (N,), torch.float32, "w_scale")
+    _each_shape(bias, G, (N,), y.dtype, "bias")
+    px, ps, py, ws = _addresses(x, x_scale, y, workspace)
+    _enough(workspace, gl_workspace_size(G))
+    (pw, pww, pc, pcc, pb, pbb), keep = _grouped_on(x, stream, w=w, w_scale=w_scale, bias=bias)
+    _check(getattr(load(), name)(G, K, F, T, _dtype(y), *((int(act),) if gated else ()), px, ps, pw, pww, pc, pcc, pb,
+                                 pbb, py, y.shape[0], ws, _stream(stream)))
+    del keep
+    return y
+
+
+def gl_forward_int8(x: Tensor, x_scale: Tensor, w: Grouped, w_scale: Grouped, y: Tensor, workspace: Tensor, *,
+                    bias: Optional[Grouped] = None, stream=None) -> Tensor:
+    """y[:T] = grouped (x W_g^T) x_scale[t] w_scale_g[n] (+ b_g) from int8 x [T, K] and w
+    [G, N, K] (or G tensors [N, K]) with float32 scales x_scale [T] and w_scale [G, N] (or G
+    tensors [N]); y [>= T, N] is float32, bfloat16 or float16, the bias of its dtype."""
+    return _int8("gl_forward_int8", False, x, x_scale, w, w_scale, y, workspace, bias, 0, stream)
+
+
+def gl_glu_forward_int8(x: Tensor, x_scale: Tensor, w: Grouped, w_scale: Grouped, a: Tensor, workspace: Tensor, *,
+                        bias: Optional[Grouped] = None, act: int = GL_GLU_SILU, stream=None) -> Tensor:
+    """gl_glu_forward from int8 x and w (w [G, 2F, K], the gate's rows first) with the scales
+    of gl_forward_int8; a [>= T, F] is float32, bfloat16 or float16."""
+    return _int8("gl_glu_forward_int8", True, x, x_scale, w, w_scale, a, workspace, bias, act, stream)
 
 
 def _tensors(obj):

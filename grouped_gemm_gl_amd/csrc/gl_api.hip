@@ -16,6 +16,7 @@
 
 #include "../../include/grouped_linear.h"
 #include "gl_common.hpp"
+#include "gl_glu.hpp"
 
 namespace gl {
 hipError_t launch_offsets(const int64_t *m_splits, int G, int64_t total_rows, void *ws, int split_slots,
@@ -63,6 +64,14 @@ hipError_t launch_quantize_mxfp8_weights(const uint16_t *w, int G, int64_t N, in
                                          hipStream_t s);
 hipError_t launch_swiglu_fwd(int el, int64_t T, int64_t F, const void *h, void *a, hipStream_t s);
 hipError_t launch_swiglu_bwd(int el, int64_t T, int64_t F, const void *h, const void *da, void *dh, hipStream_t s);
+hipError_t launch_glu_bf16(const GluParams &p, bool grad, hipStream_t s);
+hipError_t launch_glu_f16(const GluParams &p, bool grad, hipStream_t s);
+hipError_t launch_glu_f32(const GluParams &p, bool grad, hipStream_t s);
+hipError_t launch_glu_int8(int el_out, const GluParams &p, bool gated, hipStream_t s);
+hipError_t launch_glu_grad(int el, int64_t T, int64_t F, int act, const void *h, const void *da, void *dh, void *a,
+                           hipStream_t s);
+hipError_t launch_quantize_int8(int el, int64_t rows, int64_t cols, const void *src, int8_t *data, float *scale,
+                                hipStream_t s);
 hipError_t launch_rmsnorm_fwd(int el, bool g32, int64_t T, int64_t C, const void *x, const void *residual,
                               const void *gamma, float eps, void *h, void *y, uint8_t *data, uint8_t *scale,
                               hipStream_t s);
@@ -682,6 +691,176 @@ int gl_grouped_mlp_backward(int num_groups, int64_t in_features, int64_t ffn_fea
   if (T > 0) GL_TRY(hip_result(gl::launch_swiglu_bwd(el_code(dtype), T, F, h, da, dh, stream), "gl_grouped_mlp_backward"));
   GL_TRY(fc1_wgrad(true));
   return fc1_dgrad(true);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- gated layer, 8-bit integers --
+// The gated grouped layer (both projections, the activation and their product in one
+// launch) with its gradient, and the grouped product of 8-bit integers.
+
+namespace {
+int check_act(const char *who, int act) {
+  if (act != GL_GLU_SILU && act != GL_GLU_GELU && act != GL_GLU_GELU_TANH)
+    return fail(GL_ERR_ARG, "%s: unknown activation (%d)", who, act);
+  return GL_OK;
+}
+
+// Sizes of the grouped products with a gated or scaled epilogue: `wide` outputs a group, K
+// whole 16-byte pieces of `per16` elements, rows of four (fp32 outputs) or eight.
+int check_glu_sizes(const char *who, int G, int64_t K, int64_t F, int64_t T, int64_t wide, int per16, int per_row) {
+  GL_TRY(check_sizes(G, K, F, T));
+  if (K % per16) return fail(GL_ERR_SHAPE, "%s: in_features must be a multiple of %d (got %lld)", who, per16, (long long)K);
+  if (F % per_row) return fail(GL_ERR_SHAPE, "%s: the output features must be a multiple of %d (got %lld)", who, per_row, (long long)F);
+  if (K > kMaxBf16Dim || wide > kMaxBf16Dim)
+    return fail(GL_ERR_SHAPE, "%s: in_features and the weights' rows must be at most %lld (got %lld, %lld)", who,
+                (long long)kMaxBf16Dim, (long long)K, (long long)wide);
+  return GL_OK;
+}
+
+int check_rows(const char *who, int64_t have, int64_t T) {
+  if (have < T) return fail(GL_ERR_SHAPE, "%s: output buffer has %lld rows, needs at least %lld", who, (long long)have, (long long)T);
+  return GL_OK;
+}
+
+int launch_glu(gl_dtype dtype, const gl::GluParams &p, bool grad, hipStream_t s, const char *who) {
+  return hip_result(dtype == GL_F32 ? gl::launch_glu_f32(p, grad, s) : dtype == GL_F16 ? gl::launch_glu_f16(p, grad, s)
+                                                                                       : gl::launch_glu_bf16(p, grad, s),
+                    who);
+}
+
+int int8_impl(const char *who, bool gated, int G, int64_t K, int64_t F, int64_t T, gl_dtype out_dtype, int act,
+              const int8_t *x, const float *x_scale, const int8_t *w, const int8_t *const *w_ptrs,
+              const float *w_scale, const float *const *w_scale_ptrs, const void *bias, const void *const *bias_ptrs,
+              void *y, int64_t y_rows, const void *workspace, hipStream_t stream) {
+  GL_TRY(check_float_dtype(out_dtype, who));
+  if (gated) GL_TRY(check_act(who, act));
+  GL_TRY(check_glu_sizes(who, G, K, F, T, gated ? 2 * F : F, 16, 8));
+  // 2^17 products of magnitude 2^14 would pass the int32 sums
+  if (K >= (1 << 17)) return fail(GL_ERR_SHAPE, "%s: in_features must be below %d (got %lld)", who, 1 << 17, (long long)K);
+  if (!workspace || !aligned16(workspace)) return fail(GL_ERR_ARG, "%s: workspace NULL or not 16-byte aligned", who);
+  GL_TRY(check_rows(who, y_rows, T));
+  GL_TRY(check_one_form(w, w_ptrs, "weight", false));
+  GL_TRY(check_one_form(bias, bias_ptrs, "bias", true));
+  if ((w != nullptr) != (w_scale != nullptr) || (w_ptrs != nullptr) != (w_scale_ptrs != nullptr))
+    return fail(GL_ERR_ARG, "%s: weight scales must come in the same form as the weights", who);
+  if (((uintptr_t)w_scale & 3u) || ((uintptr_t)w_scale_ptrs & 7u))
+    return fail(GL_ERR_ARG, "%s: weight scales not aligned to their elements", who);
+  GL_TRY(check_buf(x, T, "x"));
+  GL_TRY(check_buf(y, T, gated ? "a" : "y"));
+  if (T == 0) return ok();
+  if (!x_scale || ((uintptr_t)x_scale & 3u)) return fail(GL_ERR_ARG, "%s: x_scale NULL or not 4-byte aligned", who);
+  gl::GluParams p{};
+  p.x = (const char *)x; p.w = (const char *)w; p.w_ptrs = (const char *const *)w_ptrs;
+  p.bias = bias; p.bias_ptrs = bias_ptrs;
+  p.x_scale = x_scale; p.w_scale = w_scale; p.w_scale_ptrs = w_scale_ptrs;
+  p.out = y; p.ws = workspace; p.G = G; p.act = act; p.T = T; p.K = K; p.F = F;
+  return hip_result(gl::launch_glu_int8(el_code(out_dtype), p, gated, stream), who);
+}
+}  // namespace
+
+extern "C" {
+
+int gl_glu_forward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows, gl_dtype dtype,
+                   int act, const void *x, const void *w, const void *const *w_ptrs, const void *bias,
+                   const void *const *bias_ptrs, void *h, void *a, int64_t a_rows, const void *workspace,
+                   hipStream_t stream) {
+  const char *who = "gl_glu_forward";
+  const int64_t K = in_features, F = ffn_features, T = total_rows;
+  GL_TRY(check_float_dtype(dtype, who));
+  GL_TRY(check_act(who, act));
+  GL_TRY(check_glu_sizes(who, num_groups, K, F, T, 2 * F, is16(dtype) ? 8 : 4, is16(dtype) ? 8 : 4));
+  if (!workspace || !aligned16(workspace)) return fail(GL_ERR_ARG, "%s: workspace NULL or not 16-byte aligned", who);
+  GL_TRY(check_rows(who, a_rows, T));
+  GL_TRY(check_one_form(w, w_ptrs, "weight", false));
+  GL_TRY(check_one_form(bias, bias_ptrs, "bias", true));
+  GL_TRY(check_buf(x, T, "x"));
+  GL_TRY(check_buf(a, T, "a"));
+  if (h) GL_TRY(check_buf(h, T, "h"));
+  if (T == 0) return ok();
+  if (h == a) return fail(GL_ERR_ARG, "%s: h and a must be different buffers", who);
+  gl::GluParams p{};
+  p.x = (const char *)x; p.w = (const char *)w; p.w_ptrs = (const char *const *)w_ptrs;
+  p.bias = bias; p.bias_ptrs = bias_ptrs; p.out = a; p.h = h;
+  p.ws = workspace; p.G = num_groups; p.act = act; p.T = T; p.K = K; p.F = F;
+  return launch_glu(dtype, p, false, stream, who);
+}
+
+int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows, gl_dtype dtype,
+                    gl_dtype wgrad_dtype, int act, const void *x, const void *w, const void *const *w_ptrs,
+                    const void *bias, const void *const *bias_ptrs, const void *h, const void *da, void *dh, void *a,
+                    void *dx, int64_t dx_rows, void *dw, void *const *dw_ptrs, void *db, void *const *db_ptrs,
+                    int accumulate, const void *workspace, hipStream_t stream) {
+  const char *who = "gl_glu_backward";
+  const int G = num_groups;
+  const int64_t K = in_features, F = ffn_features, T = total_rows;
+  const bool with_db = db || db_ptrs;
+  GL_TRY(check_float_dtype(dtype, who));
+  GL_TRY(check_act(who, act));
+  GL_TRY(check_glu_sizes(who, G, K, F, T, 2 * F, is16(dtype) ? 8 : 4, is16(dtype) ? 8 : 4));
+  if (!workspace || !aligned16(workspace)) return fail(GL_ERR_ARG, "%s: workspace NULL or not 16-byte aligned", who);
+  GL_TRY(check_one_form(w, w_ptrs, "weight", false));
+  GL_TRY(check_one_form(bias, bias_ptrs, "bias", true));
+  if (h) GL_TRY(check_buf(h, T, "h"));
+  GL_TRY(check_buf(da, T, "da"));
+  GL_TRY(check_buf(dh, T, "dh"));
+  if (a) GL_TRY(check_buf(a, T, "a"));
+  if (T > 0 && (a == dh || (a && a == da))) return fail(GL_ERR_ARG, "%s: a must be a buffer of its own", who);
+  if (T > 0 && dh == da) return fail(GL_ERR_ARG, "%s: dh must not be da", who);
+  auto wgrad = [&](bool launch) {
+    return wgrad_impl(who, G, K, 2 * F, T, dtype, wgrad_dtype, x, dh, dw, dw_ptrs, accumulate, with_db, dtype, db,
+                      db_ptrs, workspace, stream, launch);
+  };
+  auto dgrad = [&](bool launch) {
+    return dgrad_impl(G, K, 2 * F, T, dtype, dh, w, w_ptrs, dx, dx_rows, workspace, stream, launch);
+  };
+  // every step is checked before any is launched
+  GL_TRY(wgrad(false));
+  if (dx) GL_TRY(dgrad(false));
+  if (T > 0 && h) {
+    GL_TRY(hip_result(gl::launch_glu_grad(el_code(dtype), T, F, act, h, da, dh, a, stream), who));
+  } else if (T > 0) {
+    gl::GluParams p{};
+    p.x = (const char *)x; p.w = (const char *)w; p.w_ptrs = (const char *const *)w_ptrs;
+    p.bias = bias; p.bias_ptrs = bias_ptrs; p.out = dh; p.da = da; p.a = a;
+    p.ws = workspace; p.G = G; p.act = act; p.T = T; p.K = K; p.F = F;
+    GL_TRY(launch_glu(dtype, p, true, stream, who));
+  }
+  GL_TRY(wgrad(true));  // also runs for T == 0: empty groups' gradients
+  return dx ? dgrad(true) : ok();
+}
+
+int gl_quantize_int8(int64_t rows, int64_t cols, gl_dtype dtype, const void *src, int8_t *data, float *scale,
+                     hipStream_t stream) {
+  const char *who = "gl_quantize_int8";
+  if (rows < 0 || cols <= 0) return fail(GL_ERR_ARG, "%s: invalid sizes (%lld, %lld)", who, (long long)rows, (long long)cols);
+  GL_TRY(check_float_dtype(dtype, who));
+  if (cols % 16) return fail(GL_ERR_SHAPE, "%s: cols must be a multiple of 16 (got %lld)", who, (long long)cols);
+  if (cols > kMaxBf16Dim || rows > INT32_MAX)
+    return fail(GL_ERR_SHAPE, "%s: at most %lld columns and 2^31 - 1 rows", who, (long long)kMaxBf16Dim);
+  GL_TRY(check_buf(src, rows, "src"));
+  GL_TRY(check_buf(data, rows, "data"));
+  if (rows == 0) return ok();
+  if (!scale || ((uintptr_t)scale & 3u)) return fail(GL_ERR_ARG, "%s: scale NULL or not 4-byte aligned", who);
+  if (src == (const void *)data) return fail(GL_ERR_ARG, "%s: data must not be src", who);
+  return hip_result(gl::launch_quantize_int8(el_code(dtype), rows, cols, src, data, scale, stream), who);
+}
+
+int gl_forward_int8(int num_groups, int64_t in_features, int64_t out_features, int64_t total_rows, gl_dtype out_dtype,
+                    const int8_t *x, const float *x_scale, const int8_t *w, const int8_t *const *w_ptrs,
+                    const float *w_scale, const float *const *w_scale_ptrs, const void *bias,
+                    const void *const *bias_ptrs, void *y, int64_t y_rows, const void *workspace, hipStream_t stream) {
+  return int8_impl("gl_forward_int8", false, num_groups, in_features, out_features, total_rows, out_dtype, 0, x,
+                   x_scale, w, w_ptrs, w_scale, w_scale_ptrs, bias, bias_ptrs, y, y_rows, workspace, stream);
+}
+
+int gl_glu_forward_int8(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows,
+                        gl_dtype out_dtype, int act, const int8_t *x, const float *x_scale, const int8_t *w,
+                        const int8_t *const *w_ptrs, const float *w_scale, const float *const *w_scale_ptrs,
+                        const void *bias, const void *const *bias_ptrs, void *a, int64_t a_rows,
+                        const void *workspace, hipStream_t stream) {
+  return int8_impl("gl_glu_forward_int8", true, num_groups, in_features, ffn_features, total_rows, out_dtype, act, x,
+                   x_scale, w, w_ptrs, w_scale, w_scale_ptrs, bias, bias_ptrs, a, a_rows, workspace, stream);
 }
 
 }  // extern "C"

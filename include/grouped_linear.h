@@ -406,6 +406,86 @@ int gl_grouped_mlp_backward(int num_groups, int64_t in_features, int64_t ffn_fea
                             const void *workspace, hipStream_t stream);
 
 /*
+ * The gated grouped layer in one launch: both projections, the activation and their product
+ * (the first half of gl_grouped_mlp_forward without h's way through memory).  For the rows of
+ * group g
+ *   h = x W_g^T + b_g,  a = act(h[:, :F]) * h[:, F:]
+ *   act          GL_GLU_SILU v / (1 + exp(-v)); GL_GLU_GELU v Phi(v), Phi the normal
+ *                distribution; GL_GLU_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2
+ *   dtype        GL_F32, GL_BF16 or GL_F16 for every tensor
+ *   x [T, K]; w / w_ptrs [G, 2F, K] or G x [2F, K], the gate's rows first; bias / bias_ptrs
+ *                [G, 2F] or G x [2F], or none
+ *   h            [T, 2F], kept for gl_glu_backward, or NULL
+ *   a            [a_rows, F], a_rows >= T: rows >= T are never written
+ * Sums, activation and product are fp32 (a is not computed from the rounded h, as
+ * gl_swiglu_forward would); h and a are each rounded once.  K and F multiples of 8 (16-bit) or 4
+ * (fp32), K and 2F at most 2^22; every tensor, each group's too, 16-byte aligned.  fp32 products
+ * run on the matrix cores and differ from gl_forward's in the last bits.  The workspace is the
+ * one of gl_offsets; h and a do not overlap any other buffer.
+ */
+enum { GL_GLU_SILU = 0, GL_GLU_GELU = 1, GL_GLU_GELU_TANH = 2 };
+int gl_glu_forward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows, gl_dtype dtype,
+                   int act, const void *x, const void *w, const void *const *w_ptrs, const void *bias,
+                   const void *const *bias_ptrs, void *h, void *a, int64_t a_rows, const void *workspace,
+                   hipStream_t stream);
+
+/*
+ * Its backward, for the gradient da [T, F] of a:
+ *   dh = [da h_u act'(h_g), da act(h_g)],  dx = dh W_g,  dW_g (+)= dh^T x,  db_g = sum of dh's rows
+ *   h            [T, 2F] as gl_glu_forward kept it, or NULL: computed again from x, w and bias
+ *                (nothing of the forward is kept then; the activation takes the fp32 sums)
+ *   bias         the forward's; read only where h is NULL
+ *   dh           [T, 2F] of dtype, rounded once: what dx, dW and db are the products of.  May be h
+ *   a            [T, F], the forward's output again (the next layer's wgrad needs it), or NULL
+ *   dx           [dx_rows, K], dx_rows >= T, rows >= T never written; NULL: not computed
+ *   dw / dw_ptrs, wgrad_dtype and accumulate as in gl_wgrad; db / db_ptrs of dtype as in
+ *                gl_wgrad_bgrad, or none
+ * Every step is checked before any is launched.  T = 0 writes the empty groups' gradients.
+ */
+int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows, gl_dtype dtype,
+                    gl_dtype wgrad_dtype, int act, const void *x, const void *w, const void *const *w_ptrs,
+                    const void *bias, const void *const *bias_ptrs, const void *h, const void *da, void *dh, void *a,
+                    void *dx, int64_t dx_rows, void *dw, void *const *dw_ptrs, void *db, void *const *db_ptrs,
+                    int accumulate, const void *workspace, hipStream_t stream);
+
+/*
+ * Rows as 8-bit integers with a scale each (a token's activations, or a channel's weights:
+ * weights [G, N, K] are G * N rows):
+ *   m = max(largest magnitude of the row, 2^-100),  scale = m / 127,  q = rint(v * (127 * (1 / m)))
+ * in fp32, each operation rounded, ties to even; codes are within +-127.  A row that holds an infinity or NaN gets codes
+ * 0 and scale NaN, so that every product with it is NaN.
+ *   src [rows, cols] of dtype (GL_F32, GL_BF16 or GL_F16); data int8 [rows, cols];
+ *   scale float [rows].  cols a multiple of 16, at most 2^22; src and data 16-byte aligned and
+ *   not overlapping
+ */
+int gl_quantize_int8(int64_t rows, int64_t cols, gl_dtype dtype, const void *src, int8_t *data, float *scale,
+                     hipStream_t stream);
+
+/*
+ * The grouped product of 8-bit integers with scales for each token and channel: for the rows t
+ * of group g
+ *   y[t, n] = (sum_k x[t, k] w_g[n, k]) x_scale[t] w_scale_g[n] + b_g[n]
+ * and gl_glu_forward_int8: the same h [T, 2F] through the gate, a = act(h[:, :F]) * h[:, F:].
+ *   x int8 [T, K], x_scale float [T]; w / w_ptrs int8 [G, N, K] or G x [N, K] (N = 2F, the
+ *                gate's rows first), w_scale / w_scale_ptrs float [G, N] or G x [N], in the
+ *                weights' form; codes may take the whole of [-128, 127], scales any value
+ *   out_dtype    GL_F32, GL_BF16 or GL_F16 for y / a and the bias / bias_ptrs (or none)
+ *   y [y_rows, N] / a [a_rows, F], at least T rows: rows >= T are never written
+ * The sums are exact in int32; from there on fp32, one rounding at the end.  K a multiple of 16
+ * below 2^17; N (F) a multiple of 8; the weights' rows at most 2^22; tensors 16-byte aligned,
+ * each group's weights and biases too, scales 4-byte.  The workspace is the one of gl_offsets.
+ */
+int gl_forward_int8(int num_groups, int64_t in_features, int64_t out_features, int64_t total_rows, gl_dtype out_dtype,
+                    const int8_t *x, const float *x_scale, const int8_t *w, const int8_t *const *w_ptrs,
+                    const float *w_scale, const float *const *w_scale_ptrs, const void *bias,
+                    const void *const *bias_ptrs, void *y, int64_t y_rows, const void *workspace, hipStream_t stream);
+int gl_glu_forward_int8(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows,
+                        gl_dtype out_dtype, int act, const int8_t *x, const float *x_scale, const int8_t *w,
+                        const int8_t *const *w_ptrs, const float *w_scale, const float *const *w_scale_ptrs,
+                        const void *bias, const void *const *bias_ptrs, void *a, int64_t a_rows,
+                        const void *workspace, hipStream_t stream);
+
+/*
  * Deferred weight gradients (page "transformer_engine/pytorch/ops/basic/
  * grouped_linear.py", delay_wgrad_compute and backward_dw): the backward pass puts
  * its wgrad call in a queue instead of running it, and a later call runs the
