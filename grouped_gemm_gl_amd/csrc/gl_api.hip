@@ -712,9 +712,11 @@ int check_glu_sizes(const char *who, int G, int64_t K, int64_t F, int64_t T, int
   GL_TRY(check_sizes(G, K, F, T));
   if (K % per16) return fail(GL_ERR_SHAPE, "%s: in_features must be a multiple of %d (got %lld)", who, per16, (long long)K);
   if (F % per_row) return fail(GL_ERR_SHAPE, "%s: the output features must be a multiple of %d (got %lld)", who, per_row, (long long)F);
-  if (K > kMaxBf16Dim || wide > kMaxBf16Dim)
+  // 256 rows are addressed with 32 bits, 2^30 bytes of them at most
+  constexpr int64_t most = (int64_t)1 << 20;
+  if (K > most || wide > most)
     return fail(GL_ERR_SHAPE, "%s: in_features and the weights' rows must be at most %lld (got %lld, %lld)", who,
-                (long long)kMaxBf16Dim, (long long)K, (long long)wide);
+                (long long)most, (long long)K, (long long)wide);
   return GL_OK;
 }
 

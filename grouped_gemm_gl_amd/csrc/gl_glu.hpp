@@ -11,6 +11,8 @@
 // rounded once to fp32); every output is rounded once, from the fp32 values.
 #pragma once
 
+#include <type_traits>
+
 #include "gl_vec.hpp"
 
 namespace gl {
@@ -23,28 +25,34 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
 }
 
-// act(v), and with SLOPE also act'(v), for a v that the whole wave takes through the same
-// activation.  Infinities get the limits (0 and slope 0, or v and slope 1) and NaN stays NaN:
+// act(v), and with SLOPE also act'(v).  Infinities get the limits (0 and slope 0, or v and slope 1) and NaN stays NaN:
 // beyond +-100 each activation and slope is its limit in fp32, so v is held to that range
 // wherever an infinity would meet a zero.
-template <bool SLOPE>
-__device__ __forceinline__ float activate(int act, float v, float &slope) {
+template <bool SLOPE, int ACT>
+__device__ __forceinline__ float activate(float v, float &slope) {
   const float lo = v < -100.f ? -100.f : v;  // NaN stays
   const float c = lo > 100.f ? 100.f : lo;
-  if (act == ACT_GELU) {
+  if constexpr (ACT == ACT_GELU) {
     const float p = 0.5f + 0.5f * erff(c * 0.70710678118654752f);
     if (SLOPE) slope = p + c * 0.3989422804014327f * __builtin_amdgcn_exp2f(c * c * -0.72134752044448170f);
     return lo * p;
-  }
-  if (act == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)
+  } else if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)
     const float c2 = c * c;
     const float p = sigmoid_fast(c * (1.5957691216057308f + 0.07135481282651713f * c2));
     if (SLOPE) slope = p + c * p * (1.f - p) * (1.5957691216057308f + 0.21406443847955140f * c2);
     return lo * p;
+  } else {
+    const float p = sigmoid_fast(c);
+    if (SLOPE) slope = p + c * p * (1.f - p);
+    return lo * p;
   }
-  const float p = sigmoid_fast(c);
-  if (SLOPE) slope = p + c * p * (1.f - p);
-  return lo * p;
+}
+// Runs f with the activation as a compile-time tag: one test for many values.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+  if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+  else if (act == ACT_GELU_TANH) f(std::integral_constant<int, ACT_GELU_TANH>{});
+  else f(std::integral_constant<int, ACT_SILU>{});
 }
 
 // ------------------------------------------------------------ operands --
@@ -161,13 +169,13 @@ __device__ __forceinline__ float4 finish(typename Operand<IN>::acc_t s, float ro
     return make_float4(s[0] + c.bias.x, s[1] + c.bias.y, s[2] + c.bias.z, s[3] + c.bias.w);
 }
 
-template <bool SLOPE>
-__device__ __forceinline__ float4 activate4(int act, float4 v, float4 &slope) {
+template <bool SLOPE, int ACT>
+__device__ __forceinline__ float4 activate4(float4 v, float4 &slope) {
   float4 o;
-  o.x = activate<SLOPE>(act, v.x, slope.x);
-  o.y = activate<SLOPE>(act, v.y, slope.y);
-  o.z = activate<SLOPE>(act, v.z, slope.z);
-  o.w = activate<SLOPE>(act, v.w, slope.w);
+  o.x = activate<SLOPE, ACT>(v.x, slope.x);
+  o.y = activate<SLOPE, ACT>(v.y, slope.y);
+  o.z = activate<SLOPE, ACT>(v.z, slope.z);
+  o.w = activate<SLOPE, ACT>(v.w, slope.w);
   return o;
 }
 __device__ __forceinline__ float4 mul4(float4 a, float4 b) {
@@ -176,10 +184,10 @@ __device__ __forceinline__ float4 mul4(float4 a, float4 b) {
 
 // The gated epilogues for columns col .. col + 3 of row `row`: g and u are the finished
 // values of h's two halves there.
-template <int EL, int EPI>
+template <int EL, int EPI, int ACT>
 __device__ __forceinline__ void gated4(const GluParams &p, int64_t row, int64_t col, float4 g, float4 u) {
   float4 slope = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 y = activate4<EPI == EPI_GLU_GRAD>(p.act, g, slope);
+  const float4 y = activate4<EPI == EPI_GLU_GRAD, ACT>(g, slope);
   if constexpr (EPI == EPI_GLU) {
     put4<EL>(p.out, row * p.F + col, mul4(y, u));
     if (p.h) {

@@ -152,8 +152,9 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p, int t
           if (c < cols1)
             put4<EL>(p.out, row * p.F + second + c, finish<IN>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
         } else if (c < cols0) {
-          gated4<EL, EPI>(p, row, col0 + c, finish<IN>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)),
-                          finish<IN>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
+          const float4 v0 = finish<IN>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
+          const float4 v1 = finish<IN>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
+          with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
         }
       }
       __syncthreads();

@@ -23,14 +23,16 @@ __global__ __launch_bounds__(kGradThreads) void glu_grad_kernel(const char *h, c
     V::load(h + (r * 2 * F + c) * B, g);
     V::load(h + (r * 2 * F + F + c) * B, u);
     V::load(da + (r * F + c) * B, d);
+    with_activation(act, [&](auto tag) {
 #pragma unroll
-    for (int i = 0; i < V::n; ++i) {
-      float slope;
-      const float y = activate<true>(act, g[i], slope);
-      o[i] = y * u[i];
-      g[i] = d[i] * u[i] * slope;
-      u[i] = d[i] * y;
-    }
+      for (int i = 0; i < V::n; ++i) {
+        float slope;
+        const float y = activate<true, decltype(tag)::value>(g[i], slope);
+        o[i] = y * u[i];
+        g[i] = d[i] * u[i] * slope;
+        u[i] = d[i] * y;
+      }
+    });
     V::store(dh + (r * 2 * F + c) * B, g);
     V::store(dh + (r * 2 * F + F + c) * B, u);
     if (a) V::store(a + (r * F + c) * B, o);

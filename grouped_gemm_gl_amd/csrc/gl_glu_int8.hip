@@ -6,15 +6,15 @@
 // rounded once in fp32.  A row with an infinity or NaN gets codes 0 and scale NaN, so that
 // whatever is multiplied with it is NaN.  HBM-bound: a row is held in registers between the
 // two uses of its values, by a wave or a workgroup.
-#include "gl_glu_few.hpp"
+#include "gl_glu_tile.hpp"
 
 namespace gl {
 
 template <int EPI>
 static hipError_t launch_int8(int el_out, const GluParams &p, hipStream_t s) {
-  if (el_out == EL_F32) return launch_glu_few<IN_I8, EL_F32, EPI>(p, s);
-  if (el_out == EL_F16) return launch_glu_few<IN_I8, EL_F16, EPI>(p, s);
-  return launch_glu_few<IN_I8, EL_BF16, EPI>(p, s);
+  if (el_out == EL_F32) return launch_glu<IN_I8, EL_F32, EPI>(p, s);
+  if (el_out == EL_F16) return launch_glu<IN_I8, EL_F16, EPI>(p, s);
+  return launch_glu<IN_I8, EL_BF16, EPI>(p, s);
 }
 
 hipError_t launch_glu_int8(int el_out, const GluParams &p, bool gated, hipStream_t s) {

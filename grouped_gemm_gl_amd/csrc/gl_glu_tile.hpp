@@ -1,0 +1,335 @@
+// Grouped products with a gated or scaled epilogue on 256-row tiles, for groups of many rows.
+//
+// A workgroup of eight waves takes 256 rows of a group by two sets of 128 weight rows, B0 and
+// B1: the gate's and the other half's rows of the same 128 columns (plain: 256 neighbouring
+// columns).  So h_g and h_u of an output are in the same lane, and the epilogue is in registers.
+// The contraction goes by stages of 128 bytes of every row (64 values of 16 bits, 128 of 8, 32
+// of 32: the same kernel for each, but for the matrix instruction).  Waves are 4 x 2; a wave has
+// 32 + 32 rows (of A0 and A1, the tile's halves) by 64 + 64 columns (of B0 and B1).
+//
+// A stage is four phases, one quadrant of the wave's outputs each, and each phase reads half
+// an operand from LDS, asks for half an operand of the stage after next, and multiplies:
+//   phase   reads          loads          multiplies
+//     0     A0(s)          B0(s+2)        A0 B0
+//     1     B1(s)          A0(s+2)        A0 B1
+//     2     A1(s)          B1(s+2)        A1 B1
+//     3     B0(s+1)        A1(s+2)        A1 B0
+// A half's place in LDS is asked for again one phase after it was read, and what is loaded is
+// read seven phases later, so a wave has 12 to 14 loads of 1 KiB in flight all the time and
+// waits (vmcnt) for none that is younger than six phases: 96-112 KiB a CU, nearly the whole
+// ring of two stages, with no wait for a stage as a whole.
+//
+// The waves 4-7 run one barrier behind the waves 0-3, which share their SIMDs: while one of a
+// SIMD's two waves multiplies, the other reads.  A wave's reads are complete (lgkmcnt) before the
+// barrier that ends its reading, so the loads that the other group sends after it may write there.
+//
+// The pipeline runs on over tiles: the last two stages of a tile ask for the first two of the
+// next, whose loads are under way during the epilogue.  So the tiles' addresses are found in
+// registers: lane i holds the place of the workgroup's i-th tile of 64 (filled by all lanes at
+// once), and nothing in the loop loads to registers or waits for it.
+//
+// Addresses: every stream is a buffer resource on a half's first row whose length ends with the
+// last valid row, so rows past the group's or the matrix's end load zeros without a test; a lane's
+// offset from there is the same for every stream, because the rows of both operands have the same
+// length; past the row's end (the last stage) lanes take an offset out of range, and get zeros.
+#pragma once
+
+#include "gl_gemm_tile.hpp"
+#include "gl_glu_few.hpp"
+
+namespace gl {
+
+constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+constexpr int kTileRowsM = 256, kHalf = 128;
+constexpr int kStageB = 128;                 // bytes of a row in a stage
+constexpr int kHalfBytes = kHalf * kStageB;  // a half operand of a stage in LDS
+constexpr int kRingBytes = 4 * kHalfBytes;   // A0, A1, B0, B1
+constexpr uint32_t kOutside = 0x80000000u;   // past every resource's end
+
+struct TilePlace {
+  int g, jt;
+  int rows;      // of the tile, 1 .. 256
+  int64_t row0;  // the first in the packed rows
+};
+
+template <int IN, int EL, int EPI>
+__global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
+  using Op = Operand<IN>;
+  using acc_t = typename Op::acc_t;
+  constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;  // output columns of a tile
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes];
+
+  const WsView ws = ws_view(p.ws, p.G);
+  if (!ws_usable(ws.hdr, p.G, p.T)) return;
+  const int64_t *__restrict__ off = ws.off;
+  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(kTileRowsM)];
+  const int tiles_j = (int)((p.F + kColsB - 1) / kColsB);
+  const int total = pre[p.G] * tiles_j;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int grid = gridDim.x, b = blockIdx.x;
+  // each XCD (blockIdx % 8) walks a run of neighbouring tiles
+  const int first = (grid & 7) == 0 ? (b & 7) * (grid >> 3) + (b >> 3) : b;
+  if (first >= total) return;
+  const int count = (total - first + grid - 1) / grid;  // tiles of this workgroup
+  const int kb = (int)(p.K * in_bytes(IN));
+  const int nk = max(2, (kb + kStageB - 1) / kStageB);  // (two at least: loads are two stages ahead)
+
+  // ---- places of 64 tiles, one a lane
+  int base = 0;
+  int t_g = 0, t_row0 = 0, t_jr = 0;
+  auto fill = [&]() {
+    const int w = first + min(base + lane, count - 1) * grid;
+    const int q = w / tiles_j;
+    int lo = 0, hi = p.G;  // the last g with pre[g] <= q
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= q) lo = mid;
+      else hi = mid;
+    }
+    const int local = w - pre[lo] * tiles_j, mt = pre[lo + 1] - pre[lo];
+    // bands of kOrdN column tiles, in a band blocks of kOrdM row tiles, row tiles fastest
+    const int cb = local / (mt * gemm::kOrdN), bw = min(gemm::kOrdN, tiles_j - cb * gemm::kOrdN);
+    const int l2 = local - cb * mt * gemm::kOrdN;
+    const int rb = l2 / (gemm::kOrdM * bw), bh = min(gemm::kOrdM, mt - rb * gemm::kOrdM);
+    const int l3 = l2 - rb * gemm::kOrdM * bw;
+    const int it = rb * gemm::kOrdM + l3 % bh, jt = cb * gemm::kOrdN + l3 / bh;
+    const int64_t r0 = off[lo] + (int64_t)it * kTileRowsM;
+    t_g = lo;
+    t_row0 = (int)r0;
+    t_jr = (jt << 9) | (int)min64(kTileRowsM, off[lo + 1] - r0);
+    if (GL_DEVICE_CHECKS) {
+      const int rows = t_jr & 511;
+      const bool good = mt > 0 && local >= 0 && it < mt && jt < tiles_j && rows > 0 && rows <= kTileRowsM && r0 >= 0 &&
+                        r0 + rows <= p.T;
+      if (!device_check(good, p.ws)) t_g = t_row0 = t_jr = 0;  // the first row is loaded, nothing stored
+    }
+  };
+  fill();
+  auto place = [&](int n) {  // of the workgroup's n-th tile
+    TilePlace t;
+    const int i = n - base;
+    t.g = __builtin_amdgcn_readlane(t_g, i);
+    t.row0 = __builtin_amdgcn_readlane(t_row0, i);
+    const int jr = __builtin_amdgcn_readlane(t_jr, i);
+    t.jt = jr >> 9;
+    t.rows = jr & 511;
+    return t;
+  };
+
+  // ---- loads: pieces of 8 rows, wave w has the pieces w and w + 8 of each half
+  const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;  // place in the stage's 128 bytes
+  const uint32_t voff = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)kb + (uint32_t)c16;
+  __amdgpu_buffer_rsrc_t ra, rb0, rb1;
+  int load_tile = 0, load_stage = 0;  // what the next four phases ask for
+  auto rsrc = [&](const char *at, int64_t rows) {
+    const uint64_t v = (uint64_t)(uintptr_t)at;  // the same in every lane; made visibly so
+    const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t h = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)(((uint64_t)h << 32) | l), (short)0,
+                                             (int)rows * kb, 0x00020000);
+  };
+  auto aim = [&]() {  // the streams of tile load_tile
+    if (load_tile >= count) return;
+    const TilePlace t = place(load_tile);
+    const char *wg = group_weights<IN, EPI>(p, t.g);
+    const int64_t col0 = (int64_t)t.jt * kColsB, left = p.F - col0;
+    ra = rsrc(p.x + t.row0 * kb, GL_DEVICE_CHECKS ? max(t.rows, 1) : t.rows);
+    rb0 = rsrc(wg + col0 * kb, min64(kHalf, left));
+    if (EPI == EPI_PLAIN)
+      rb1 = left > kHalf ? rsrc(wg + (col0 + kHalf) * kb, min64(kHalf, left - kHalf)) : rsrc(wg + col0 * kb, 1);
+    else
+      rb1 = rsrc(wg + (p.F + col0) * kb, min64(kHalf, left));
+  };
+  // half 0 A0, 1 A1, 2 B0, 3 B1 of stage load_stage into ring slot `ring`
+  auto issue = [&](int half, int ring) {
+    const int at = load_stage * kStageB;
+    const int lim = load_tile < count ? kb - at : 0;  // bytes of the row left
+    const __amdgpu_buffer_rsrc_t r = half < 2 ? ra : half == 2 ? rb0 : rb1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t o = voff + (uint32_t)(((half == 1) * kHalf + q * 64) * kb);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (GL_LDS void *)(lds + ring * kRingBytes + half * kHalfBytes + (wave + 8 * q) * 1024), 16,
+          c16 < lim ? o : kOutside, lim > 0 ? at : 0, 0, 0);
+    }
+  };
+  auto next_stage = [&]() {
+    if (++load_stage == nk) {
+      load_stage = 0;
+      ++load_tile;
+      aim();
+    }
+  };
+
+  // ---- fragments: 16 bytes of row l % 16 of a block, of the stage's half s
+  const int fr = lane & 15, fq = lane >> 4;
+  auto frag = [&](int half, int row, int ring, int s) {
+    const int r = row + fr;
+    return *(const i32x4_t *)(lds + ring * kRingBytes + half * kHalfBytes + r * kStageB +
+                              (((4 * s + fq) ^ ((r >> 1) & 7)) << 4));
+  };
+  i32x4_t fa[2][2], fb[2][4][2];  // [block][half of the stage]; two sets of B
+  auto read_a = [&](int half, int ring) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fa[i][s] = frag(half, wm * 32 + i * 16, ring, s);
+  };
+  auto read_b = [&](int set, int half, int ring) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fb[set][j][s] = frag(half, wn * 64 + j * 16, ring, s);
+  };
+  acc_t acc[2][2][2][4];  // [A half][B half][row block][column block]
+  auto zero = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int l = 0; l < 4; ++l) acc[i][j][k][l] = acc_t{0, 0, 0, 0};
+  };
+  auto multiply = [&](int set, acc_t(&c)[2][4]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = Op::mma(fb[set][j][s], fa[i][s], c[i][j]);
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  auto barrier = [&] {
+    fence();
+    __builtin_amdgcn_s_barrier();
+    fence();
+  };
+  auto read_done = [&]() {  // ends a phase's reading: own reads back, loads of six phases ago there
+    fence();
+    __builtin_amdgcn_s_waitcnt(0x007c);  // vmcnt(12) lgkmcnt(0)
+    barrier();
+  };
+  // One stage in ring slot `ring`, B0 in register set S on entry, the next stage's B0 in the
+  // other set after it.
+  auto stage = [&](auto set_tag, int ring) __attribute__((always_inline)) {
+    constexpr int S = decltype(set_tag)::value;
+    read_a(0, ring);
+    issue(2, ring);
+    read_done();
+    multiply(S, acc[0][0]);
+    barrier();
+    read_b(1 - S, 3, ring);
+    issue(0, ring);
+    read_done();
+    multiply(1 - S, acc[0][1]);
+    barrier();
+    read_a(1, ring);
+    issue(3, ring);
+    read_done();
+    multiply(1 - S, acc[1][1]);
+    barrier();
+    read_b(1 - S, 2, ring ^ 1);
+    issue(1, ring);
+    next_stage();
+    read_done();
+    multiply(S, acc[1][0]);
+    barrier();
+  };
+
+  // ---- the first two stages, then B0 of the first
+  aim();
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    issue(2, s);
+    issue(0, s);
+    issue(3, s);
+    issue(1, s);
+    next_stage();
+  }
+  fence();
+  gemm::wait_vm<12>();
+  barrier();
+  read_b(0, 2, 0);
+  gemm::wait_lgkm0();
+  barrier();
+
+  int ring = 0;
+  for (int n = 0; n < count; ++n) {
+    zero();
+    if (wave >= 4) barrier();  // one barrier behind
+    int k = 0;
+    for (; k + 1 < nk; k += 2) {
+      stage(std::integral_constant<int, 0>{}, ring);
+      stage(std::integral_constant<int, 1>{}, ring ^ 1);
+    }
+    if (k < nk) {
+      stage(std::integral_constant<int, 0>{}, ring);
+      ring ^= 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) fb[0][j][s] = fb[1][j][s];
+    }
+    if (wave < 4) barrier();  // in step again: both groups' epilogues at the same time
+
+    const TilePlace t = place(n);
+    auto epilogue = [&](auto act_tag) __attribute__((always_inline)) {
+      constexpr int ACT = decltype(act_tag)::value;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int cl = wn * 64 + j * 16 + fq * 4;
+        const int64_t col = (int64_t)t.jt * kColsB + cl;
+        const int64_t col1 = EPI == EPI_PLAIN ? col + kHalf : p.F + col;
+        const bool in0 = col < p.F, in1 = EPI == EPI_PLAIN ? col1 < p.F : in0;
+        if (!in0) continue;
+        const ColumnTerms c0 = column_terms<IN, EL, EPI>(p, t.g, col);
+        const ColumnTerms c1 = column_terms<IN, EL, EPI>(p, t.g, in1 ? col1 : col);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rl = a * kHalf + wm * 32 + i * 16 + fr;
+            if (rl >= t.rows) continue;
+            const int64_t row = t.row0 + rl;
+            const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
+            const float4 v0 = finish<IN>(acc[a][0][i][j], rs, c0), v1 = finish<IN>(acc[a][1][i][j], rs, c1);
+            if constexpr (EPI == EPI_PLAIN) {
+              put4<EL>(p.out, row * p.F + col, v0);
+              if (in1) put4<EL>(p.out, row * p.F + col1, v1);
+            } else {
+              gated4<EL, EPI, ACT>(p, row, col, v0, v1);
+            }
+          }
+      }
+    };
+    if constexpr (EPI == EPI_PLAIN) epilogue(std::integral_constant<int, ACT_SILU>{});
+    else with_activation(p.act, epilogue);
+    if (n + 3 - base >= 64) {  // the loads are at most two tiles ahead
+      base = n + 1;
+      fill();
+    }
+  }
+  gemm::wait_vm0();  // no load may be under way to the LDS of a workgroup that has ended
+}
+
+template <int IN, int EL, int EPI>
+inline hipError_t launch_glu_tile(const GluParams &p, hipStream_t s) {
+  constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;
+  const int64_t groups = p.T < p.G ? p.T : p.G;
+  const int64_t items = ((p.T + kTileRowsM - 1) / kTileRowsM + groups) * ((p.F + kColsB - 1) / kColsB);
+  hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI>), dim3(gemm::persistent_grid(items)), dim3(kTileThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+// Few rows a group (up to 32 on average, or 64 in all): the kernel that only streams weights.
+template <int IN, int EL, int EPI>
+inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
+  if (p.T <= 64 || p.T <= (int64_t)32 * p.G) return launch_glu_few<IN, EL, EPI>(p, s);
+  return launch_glu_tile<IN, EL, EPI>(p, s);
+}
+
+}  // namespace gl

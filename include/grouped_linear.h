@@ -419,7 +419,7 @@ int gl_grouped_mlp_backward(int num_groups, int64_t in_features, int64_t ffn_fea
  *   a            [a_rows, F], a_rows >= T: rows >= T are never written
  * Sums, activation and product are fp32 (a is not computed from the rounded h, as
  * gl_swiglu_forward would); h and a are each rounded once.  K and F multiples of 8 (16-bit) or 4
- * (fp32), K and 2F at most 2^22; every tensor, each group's too, 16-byte aligned.  fp32 products
+ * (fp32), K and 2F at most 2^20; every tensor, each group's too, 16-byte aligned.  fp32 products
  * run on the matrix cores and differ from gl_forward's in the last bits.  The workspace is the
  * one of gl_offsets; h and a do not overlap any other buffer.
  */
@@ -472,7 +472,7 @@ int gl_quantize_int8(int64_t rows, int64_t cols, gl_dtype dtype, const void *src
  *   out_dtype    GL_F32, GL_BF16 or GL_F16 for y / a and the bias / bias_ptrs (or none)
  *   y [y_rows, N] / a [a_rows, F], at least T rows: rows >= T are never written
  * The sums are exact in int32; from there on fp32, one rounding at the end.  K a multiple of 16
- * below 2^17; N (F) a multiple of 8; the weights' rows at most 2^22; tensors 16-byte aligned,
+ * below 2^17; N (F) a multiple of 8; the weights' rows at most 2^20; tensors 16-byte aligned,
  * each group's weights and biases too, scales 4-byte.  The workspace is the one of gl_offsets.
  */
 int gl_forward_int8(int num_groups, int64_t in_features, int64_t out_features, int64_t total_rows, gl_dtype out_dtype,

@@ -15,7 +15,7 @@ F32, BF16, F16, MX = gl.GL_F32, gl.GL_BF16, gl.GL_F16, gl.GL_E4M3
 GLU = dict(G=4, K=64, F=32, T=3, dt=BF16, act=0, x=A, w=B, wp=None, b=None, bp=None, h=None, a=C_, rows=3, ws=D)
 SIZES = [(dict(G=0), -1), (dict(K=0), -1), (dict(F=0), -1), (dict(F=-8), -1), (dict(T=-1), -1), (dict(dt=MX), -2),
          (dict(dt=7), -2), (dict(act=3), -1), (dict(act=-1), -1), (dict(K=60), -3), (dict(F=36), -3),
-         (dict(dt=F32, K=62), -3), (dict(dt=F32, F=30), -3), (dict(K=(1 << 22) + 8), -3), (dict(F=(1 << 21) + 8), -3),
+         (dict(dt=F32, K=62), -3), (dict(dt=F32, F=30), -3), (dict(K=(1 << 20) + 8), -3), (dict(F=(1 << 19) + 8), -3),
          (dict(T=1 << 31, rows=1 << 31), -3), (dict(ws=None), -1), (dict(ws=D + 8), -1), (dict(w=None), -1),
          (dict(wp=B), -1), (dict(w=B + 8), -1), (dict(w=None, wp=B + 4), -1), (dict(b=E_, bp=E_), -1),
          (dict(b=E_ + 2), -1), (dict(x=None), -1), (dict(x=A + 2), -1)]
@@ -58,7 +58,7 @@ INT8 = dict(G=4, K=64, F=32, T=3, dt=BF16, x=A, xs=B, w=C_, wp=None, s=D, sp=Non
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("kw,code", [
     (dict(G=0), -1), (dict(K=0), -1), (dict(F=0), -1), (dict(T=-1), -1), (dict(dt=MX), -2), (dict(K=72), -3),
-    (dict(F=28), -3), (dict(K=1 << 17), -3), (dict(F=(1 << 22) + 8), -3), (dict(rows=2), -3), (dict(ws=None), -1),
+    (dict(F=28), -3), (dict(K=1 << 17), -3), (dict(F=(1 << 20) + 8), -3), (dict(rows=2), -3), (dict(ws=None), -1),
     (dict(ws=F_ + 4), -1), (dict(w=None, s=None), -1), (dict(wp=C_), -1), (dict(w=C_ + 8), -1), (dict(s=None), -1),
     (dict(s=None, sp=D), -1), (dict(s=D + 2), -1), (dict(w=None, wp=C_, s=None, sp=D + 4), -1), (dict(b=A, bp=A), -1),
     (dict(b=A + 8), -1), (dict(x=None), -1), (dict(x=A + 4), -1), (dict(xs=None), -1), (dict(xs=B + 1), -1),
