@@ -25,26 +25,28 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
 }
 
-// act(v), and with SLOPE also act'(v).  Infinities get the limits (0 and slope 0, or v and slope 1) and NaN stays NaN:
-// beyond +-100 each activation and slope is its limit in fp32, so v is held to that range
-// wherever an infinity would meet a zero.
+// act(v) = v p, and with SLOPE act'(v) = p + v p'.  Infinities get the limits (0 and slope 0, or
+// v and slope 1) and NaN stays NaN: where p or p' is 0 in fp32, so is its product with v, an
+// infinite v's too.
 template <bool SLOPE, int ACT>
 __device__ __forceinline__ float activate(float v, float &slope) {
-  const float lo = v < -100.f ? -100.f : v;  // NaN stays
-  const float c = lo > 100.f ? 100.f : lo;
+  auto times = [](float v, float p) { return p == 0.f ? 0.f : v * p; };
   if constexpr (ACT == ACT_GELU) {
-    const float p = 0.5f + 0.5f * erff(c * 0.70710678118654752f);
-    if (SLOPE) slope = p + c * 0.3989422804014327f * __builtin_amdgcn_exp2f(c * c * -0.72134752044448170f);
-    return lo * p;
+    const float p = 0.5f + 0.5f * erff(v * 0.70710678118654752f);
+    if (SLOPE) slope = p + times(v, 0.3989422804014327f * __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f));
+    return times(v, p);
   } else if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)
-    const float c2 = c * c;
-    const float p = sigmoid_fast(c * (1.5957691216057308f + 0.07135481282651713f * c2));
-    if (SLOPE) slope = p + c * p * (1.f - p) * (1.5957691216057308f + 0.21406443847955140f * c2);
-    return lo * p;
+    const float v2 = v * v;
+    const float p = sigmoid_fast(v * (1.5957691216057308f + 0.07135481282651713f * v2));
+    if (SLOPE) {
+      const float q = p * (1.f - p);
+      slope = p + (q == 0.f ? 0.f : v * q * (1.5957691216057308f + 0.21406443847955140f * v2));
+    }
+    return times(v, p);
   } else {
-    const float p = sigmoid_fast(c);
-    if (SLOPE) slope = p + c * p * (1.f - p);
-    return lo * p;
+    const float p = sigmoid_fast(v);
+    if (SLOPE) slope = p + times(v, p * (1.f - p));
+    return times(v, p);
   }
 }
 // Runs f with the activation as a compile-time tag: one test for many values.
@@ -116,57 +118,75 @@ __device__ __forceinline__ const char *group_weights(const GluParams &p, int g) 
   return p.w ? p.w + (int64_t)g * n * p.K * in_bytes(IN) : p.w_ptrs[g];
 }
 
-// Four consecutive elements of a tensor as fp32 values, and back (16-bit types: 8 bytes).
+// Four consecutive elements of a tensor, as they are and as fp32 values (16-bit types: 8 bytes).
 template <int EL>
-__device__ __forceinline__ float4 load4(const void *base, int64_t at) {
-  if constexpr (EL == EL_F32) {
-    return *(const float4 *)((const float *)base + at);
-  } else {
-    const uint2 u = *(const uint2 *)((const uint16_t *)base + at);
+struct Quad {
+  typedef uint2 raw;
+  __device__ static __forceinline__ float4 value(uint2 u) {
     constexpr bool H = EL == EL_F16;
     return make_float4(h16_to_f32<H>(u.x & 0xffff), h16_to_f32<H>(u.x >> 16), h16_to_f32<H>(u.y & 0xffff),
                        h16_to_f32<H>(u.y >> 16));
   }
+  __device__ static __forceinline__ uint2 pack(float4 v) {
+    return make_uint2(pack_h16x2<EL == EL_F16>(v.x, v.y), pack_h16x2<EL == EL_F16>(v.z, v.w));
+  }
+};
+template <>
+struct Quad<EL_F32> {
+  typedef float4 raw;
+  __device__ static __forceinline__ float4 value(float4 v) { return v; }
+  __device__ static __forceinline__ float4 pack(float4 v) { return v; }
+};
+template <int EL>
+__device__ __forceinline__ typename Quad<EL>::raw load_raw4(const void *base, int64_t at) {
+  return *(const typename Quad<EL>::raw *)((const char *)base + at * elem_bytes(EL));
+}
+template <int EL>
+__device__ __forceinline__ float4 load4(const void *base, int64_t at) {
+  return Quad<EL>::value(load_raw4<EL>(base, at));
 }
 template <int EL>
 __device__ __forceinline__ void put4(void *base, int64_t at, float4 v) {
-  if constexpr (EL == EL_F32)
-    *(float4 *)((float *)base + at) = v;
-  else
-    *(uint2 *)((uint16_t *)base + at) =
-        make_uint2(pack_h16x2<EL == EL_F16>(v.x, v.y), pack_h16x2<EL == EL_F16>(v.z, v.w));
+  *(typename Quad<EL>::raw *)((char *)base + at * elem_bytes(EL)) = Quad<EL>::pack(v);
 }
 
-// What four columns of a group add to a row's sums: the bias, and for 8-bit integers the
-// channels' scales.
+// What four columns of a group add to a row's sums: the bias (as stored: it waits in registers),
+// and for 8-bit integers the channels' scales.
+template <int IN, int EL>
 struct ColumnTerms {
-  float4 scale, bias;
+  typename Quad<EL>::raw bias;
+};
+template <int EL>
+struct ColumnTerms<IN_I8, EL> {
+  typename Quad<EL>::raw bias;
+  float scale[4];
 };
 template <int IN, int EL, int EPI>
-__device__ __forceinline__ ColumnTerms column_terms(const GluParams &p, int g, int64_t col) {
+__device__ __forceinline__ ColumnTerms<IN, EL> column_terms(const GluParams &p, int g, int64_t col) {
   const int64_t n = EPI == EPI_PLAIN ? p.F : 2 * p.F;
-  ColumnTerms c;
-  c.scale = c.bias = make_float4(0.f, 0.f, 0.f, 0.f);
+  ColumnTerms<IN, EL> c;
   if constexpr (IN == IN_I8) {
     const float *s = p.w_scale ? p.w_scale + (int64_t)g * n : p.w_scale_ptrs[g];
-    c.scale = make_float4(s[col], s[col + 1], s[col + 2], s[col + 3]);  // a group's scales may sit at any word
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.scale[i] = s[col + i];  // a group's scales may sit at any word
   }
   if (p.bias)
-    c.bias = load4<EL>(p.bias, (int64_t)g * n + col);
+    c.bias = load_raw4<EL>(p.bias, (int64_t)g * n + col);
   else if (p.bias_ptrs)
-    c.bias = load4<EL>(p.bias_ptrs[g], col);
+    c.bias = load_raw4<EL>(p.bias_ptrs[g], col);
+  else
+    c.bias = typename Quad<EL>::raw{};
   return c;
 }
 
-template <int IN>
-__device__ __forceinline__ float4 finish(typename Operand<IN>::acc_t s, float row_scale, const ColumnTerms &c) {
+template <int IN, int EL>
+__device__ __forceinline__ float4 finish(typename Operand<IN>::acc_t s, float row_scale, const ColumnTerms<IN, EL> &c) {
+  const float4 b = Quad<EL>::value(c.bias);
   if constexpr (IN == IN_I8)
-    return make_float4((float)s[0] * (row_scale * c.scale.x) + c.bias.x,
-                       (float)s[1] * (row_scale * c.scale.y) + c.bias.y,
-                       (float)s[2] * (row_scale * c.scale.z) + c.bias.z,
-                       (float)s[3] * (row_scale * c.scale.w) + c.bias.w);
+    return make_float4((float)s[0] * (row_scale * c.scale[0]) + b.x, (float)s[1] * (row_scale * c.scale[1]) + b.y,
+                       (float)s[2] * (row_scale * c.scale[2]) + b.z, (float)s[3] * (row_scale * c.scale[3]) + b.w);
   else
-    return make_float4(s[0] + c.bias.x, s[1] + c.bias.y, s[2] + c.bias.z, s[3] + c.bias.w);
+    return make_float4(s[0] + b.x, s[1] + b.y, s[2] + b.z, s[3] + b.w);
 }
 
 template <bool SLOPE, int ACT>

@@ -148,12 +148,12 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p, int t
         const int c = 4 * q;
         if constexpr (EPI == EPI_PLAIN) {
           if (c < cols0)
-            put4<EL>(p.out, row * p.F + col0 + c, finish<IN>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)));
+            put4<EL>(p.out, row * p.F + col0 + c, finish<IN, EL>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)));
           if (c < cols1)
-            put4<EL>(p.out, row * p.F + second + c, finish<IN>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
+            put4<EL>(p.out, row * p.F + second + c, finish<IN, EL>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
         } else if (c < cols0) {
-          const float4 v0 = finish<IN>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
-          const float4 v1 = finish<IN>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
+          const float4 v0 = finish<IN, EL>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
+          const float4 v1 = finish<IN, EL>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
           with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
         }
       }

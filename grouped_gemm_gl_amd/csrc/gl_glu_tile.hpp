@@ -46,18 +46,91 @@ constexpr int kHalfBytes = kHalf * kStageB;  // a half operand of a stage in LDS
 constexpr int kRingBytes = 4 * kHalfBytes;   // A0, A1, B0, B1
 constexpr uint32_t kOutside = 0x80000000u;   // past every resource's end
 
+// 16 rows by 64 columns of a wave's part of an output between registers, where a lane has four
+// columns of a row in each of four blocks, and memory, as whole lines: through the wave's own 4 KiB
+// of LDS behind the ring.  Stored straight from the registers, 16 rows by 32 bytes an instruction,
+// the lines came together in L2 from quarters.  A row is kRow bytes there; its 16-byte slots are
+// permuted by the row so that neither side's accesses meet in a bank.  Rows and columns outside
+// go to an offset past the resource's end, which drops stores and loads zeros.
+constexpr int kStoreBytes = 4096;
+template <int EL>
+struct TileStore {
+  typedef typename Quad<EL>::raw raw_t;
+  typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+  char *buf;
+  int lane, row, rows, col;  // the piece's first row in the tile, rows of the tile, first column
+  static constexpr int E = elem_bytes(EL), kRow = 64 * E, kSlots = kRow / 16;
+  static constexpr int kMoves = 16 * kRow / 1024;  // of 16 bytes a lane
+  __device__ __forceinline__ static int slot(int r, int s) {
+    return (EL == EL_F32 ? s ^ (r & 15) : s ^ ((r >> 1) & 7)) << 4;
+  }
+  // the lane's four columns of block j
+  __device__ __forceinline__ raw_t *quad(int j) const {
+    const int r = lane & 15, q = lane >> 4;
+    return (raw_t *)(buf + r * kRow + (EL == EL_F32 ? slot(r, 4 * j + q) : slot(r, 2 * j + (q >> 1)) + (q & 1) * 8));
+  }
+  // the lane's 16 bytes of move k: in LDS, and their offset from the tile's first row
+  __device__ __forceinline__ u32x4_t *moved(int k) const {
+    const int r = k * (64 / kSlots) + lane / kSlots;
+    return (u32x4_t *)(buf + r * kRow + slot(r, lane % kSlots));
+  }
+  __device__ __forceinline__ uint32_t place(int k, int64_t ld, int width) const {
+    const int r = row + k * (64 / kSlots) + lane / kSlots, c = col + (lane % kSlots) * (16 / E);
+    return r < rows && c < width ? (uint32_t)((r * (int)ld + c) * E) : 0x80000000u;
+  }
+  __device__ __forceinline__ static void order() {  // lanes' accesses on either side stay there
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t block(const void *base, int64_t row0, int64_t ld, int64_t col0) const {
+    return gemm::rsrc_at(gemm::uniform_ptr((const char *)base + (row0 * ld + col0) * E));
+  }
+  template <class F>
+  __device__ __forceinline__ void put(void *base, int64_t row0, int64_t ld, int64_t col0, int width, F value) const {
+    const __amdgpu_buffer_rsrc_t rs = block(base, row0, ld, col0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *quad(j) = value(j);
+      __builtin_amdgcn_sched_barrier(0);  // one value's registers at a time
+    }
+    order();
+    u32x4_t v[kMoves];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) v[k] = *moved(k);
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], rs, place(k, ld, width), 0, 0);
+    order();
+  }
+  __device__ __forceinline__ void get(const void *base, int64_t row0, int64_t ld, int64_t col0, int width,
+                                      raw_t (&out)[4]) const {
+    const __amdgpu_buffer_rsrc_t rs = block(base, row0, ld, col0);
+    u32x4_t v[kMoves];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k)
+      v[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, place(k, ld, width), 0, 0));
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k) *moved(k) = v[k];
+    order();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = *quad(j);
+    order();
+  }
+};
+
 struct TilePlace {
   int g, jt;
   int rows;      // of the tile, 1 .. 256
   int64_t row0;  // the first in the packed rows
 };
 
-template <int IN, int EL, int EPI>
+// ACT: a run-time activation would be three copies of the epilogue, whose common values the
+// compiler computes ahead of them all and spills.
+template <int IN, int EL, int EPI, int ACT>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
   constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;  // output columns of a tile
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes];
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes + kTileWaves * kStoreBytes];
 
   const WsView ws = ws_view(p.ws, p.G);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
@@ -240,7 +313,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     barrier();
   };
 
-  // ---- the first two stages, then B0 of the first
+  // ---- the first two stages
   aim();
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -253,13 +326,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   fence();
   gemm::wait_vm<12>();
   barrier();
-  read_b(0, 2, 0);
-  gemm::wait_lgkm0();
-  barrier();
 
   int ring = 0;
   for (int n = 0; n < count; ++n) {
     zero();
+    // B0 of the first stage (again: the last tile's last stage read it, but held through the
+    // epilogue it would cost 32 registers), by all waves before the first loads may replace it
+    read_b(0, 2, ring);
+    gemm::wait_lgkm0();
+    barrier();
     if (wave >= 4) barrier();  // one barrier behind
     int k = 0;
     for (; k + 1 < nk; k += 2) {
@@ -269,45 +344,67 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     if (k < nk) {
       stage(std::integral_constant<int, 0>{}, ring);
       ring ^= 1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) fb[0][j][s] = fb[1][j][s];
     }
     if (wave < 4) barrier();  // in step again: both groups' epilogues at the same time
 
     const TilePlace t = place(n);
-    auto epilogue = [&](auto act_tag) __attribute__((always_inline)) {
-      constexpr int ACT = decltype(act_tag)::value;
+    // the lane index, opaque here, so that nothing of the epilogue's addresses is kept in registers
+    // through the stages
+    int le = lane;
+    asm volatile("" : "+v"(le));
+    const int er = le & 15, eq = le >> 4;
+    const int64_t col0 = (int64_t)t.jt * kColsB;
+    const int width = (int)min64(kHalf, p.F - col0);  // columns of the first set
+    const int width1 = EPI == EPI_PLAIN ? (int)min64(kHalf, p.F - col0 - kHalf) : width;
+    const int64_t second = EPI == EPI_PLAIN ? col0 + kHalf : p.F + col0;  // the second set's first column
+    ColumnTerms<IN, EL> ct[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int cl = wn * 64 + j * 16 + fq * 4;
-        const int64_t col = (int64_t)t.jt * kColsB + cl;
-        const int64_t col1 = EPI == EPI_PLAIN ? col + kHalf : p.F + col;
-        const bool in0 = col < p.F, in1 = EPI == EPI_PLAIN ? col1 < p.F : in0;
-        if (!in0) continue;
-        const ColumnTerms c0 = column_terms<IN, EL, EPI>(p, t.g, col);
-        const ColumnTerms c1 = column_terms<IN, EL, EPI>(p, t.g, in1 ? col1 : col);
+    for (int j = 0; j < 4; ++j) {
+      const int c = wn * 64 + j * 16 + eq * 4;  // a lane past the last column takes the last four, and is not stored
+      ct[0][j] = column_terms<IN, EL, EPI>(p, t.g, col0 + min(c, width - 4));
+      ct[1][j] = column_terms<IN, EL, EPI>(p, t.g, width1 > 0 ? second + min(c, width1 - 4) : col0);
+    }
+    float rs[2][2];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rl = a * kHalf + wm * 32 + i * 16 + fr;
-            if (rl >= t.rows) continue;
-            const int64_t row = t.row0 + rl;
-            const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
-            const float4 v0 = finish<IN>(acc[a][0][i][j], rs, c0), v1 = finish<IN>(acc[a][1][i][j], rs, c1);
-            if constexpr (EPI == EPI_PLAIN) {
-              put4<EL>(p.out, row * p.F + col, v0);
-              if (in1) put4<EL>(p.out, row * p.F + col1, v1);
-            } else {
-              gated4<EL, EPI, ACT>(p, row, col, v0, v1);
-            }
+      for (int i = 0; i < 2; ++i)
+        rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + wm * 32 + i * 16 + er, t.rows - 1)] : 0.f;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        typedef Quad<EL> Q;
+        const TileStore<EL> st{lds + 2 * kRingBytes + wave * kStoreBytes, le, a * kHalf + wm * 32 + i * 16, t.rows, wn * 64};
+        auto value = [&](int b, int j) { return finish<IN, EL>(acc[a][b][i][j], rs[a][i], ct[b][j]); };
+        auto gate = [&](int j) { return Q::pack(value(0, j)); };
+        auto other = [&](int j) { return Q::pack(value(1, j)); };
+        if constexpr (EPI == EPI_PLAIN) {
+          st.put(p.out, t.row0, p.F, col0, width, gate);
+          if (width1 > 0) st.put(p.out, t.row0, p.F, second, width1, other);
+        } else if constexpr (EPI == EPI_GLU) {
+          st.put(p.out, t.row0, p.F, col0, width, [&](int j) {
+            float4 none;
+            return Q::pack(mul4(activate4<false, ACT>(value(0, j), none), value(1, j)));
+          });
+          if (p.h) {
+            st.put(p.h, t.row0, 2 * p.F, col0, width, gate);
+            st.put(p.h, t.row0, 2 * p.F, second, width, other);
           }
+        } else {
+          typename Q::raw da[4], out[4];  // da, then da h_u act'(h_g); the forward's output
+          st.get(p.da, t.row0, p.F, col0, width, da);
+          st.put(p.out, t.row0, 2 * p.F, second, width, [&](int j) {
+            float4 slope;
+            const float4 y = activate4<true, ACT>(value(0, j), slope), u = value(1, j), d = Q::value(da[j]);
+            da[j] = Q::pack(mul4(mul4(d, u), slope));
+            out[j] = Q::pack(mul4(y, u));
+            return Q::pack(mul4(d, y));
+          });
+          if (p.a) st.put(p.a, t.row0, p.F, col0, width, [&](int j) { return out[j]; });
+          st.put(p.out, t.row0, 2 * p.F, col0, width, [&](int j) { return da[j]; });
+        }
       }
-    };
-    if constexpr (EPI == EPI_PLAIN) epilogue(std::integral_constant<int, ACT_SILU>{});
-    else with_activation(p.act, epilogue);
     if (n + 3 - base >= 64) {  // the loads are at most two tiles ahead
       base = n + 1;
       fill();
@@ -321,7 +418,13 @@ inline hipError_t launch_glu_tile(const GluParams &p, hipStream_t s) {
   constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;
   const int64_t groups = p.T < p.G ? p.T : p.G;
   const int64_t items = ((p.T + kTileRowsM - 1) / kTileRowsM + groups) * ((p.F + kColsB - 1) / kColsB);
-  hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI>), dim3(gemm::persistent_grid(items)), dim3(kTileThreads), 0, s, p);
+  const dim3 grid(gemm::persistent_grid(items)), block(kTileThreads);
+  if (EPI == EPI_PLAIN || p.act == ACT_SILU)
+    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT_SILU>), grid, block, 0, s, p);
+  else if (p.act == ACT_GELU)
+    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, EPI == EPI_PLAIN ? ACT_SILU : ACT_GELU>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, EPI == EPI_PLAIN ? ACT_SILU : ACT_GELU_TANH>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
