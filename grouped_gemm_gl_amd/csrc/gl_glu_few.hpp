@@ -1,13 +1,13 @@
-// Grouped products with a gated or scaled epilogue for few rows a group (decoding): bound by
-// reading the used groups' weights once.
+// Grouped products with a gated or scaled epilogue for at most 16 rows in all and few columns:
+// one row tile a group, and not enough of it to fill the chip, so the contraction is split too.
 //
 // A workgroup of four waves takes 16 columns of the gate and the 16 of the other half that
-// belong to them (plain: 32 columns), for up to 16 NB rows of one group.  Its waves split the
-// contraction: wave v takes units v, v + 4, .., a unit being 128 bytes of every row, straight
-// from memory to registers as whole 128-byte lines (8 rows a load, and a rotation of 8 lanes
-// gives the matrix instruction its layout).  The weights are the instruction's first operand
-// and the rows its second, so a lane ends with four neighbouring columns of a row.  The four
-// waves' sums meet in LDS and are added in a fixed order.
+// belong to them (plain: 32 columns) of one group.  Its waves split the contraction: wave v takes
+// units v, v + 4, .., a unit being 128 bytes of every row, straight from memory to registers as
+// whole 128-byte lines (8 rows a load, and a rotation of 8 lanes gives the matrix instruction its
+// layout).  The weights are the instruction's first operand and the rows its second, so a lane
+// ends with four neighbouring columns of a row.  The four waves' sums meet in LDS and are added in
+// a fixed order.
 #pragma once
 
 #include "gl_glu.hpp"
@@ -43,18 +43,16 @@ struct RowBlock {
   }
 };
 
-// NB: blocks of 16 rows that an item takes at most; 16 NB <= tile_rows, the height of the row
-// tiles that the items are counted in.
-template <int IN, int EL, int EPI, int NB>
-__global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p, int tile_rows) {
+template <int IN, int EL, int EPI>
+__global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
   constexpr int kCols = EPI == EPI_PLAIN ? 32 : 16;
-  __shared__ acc_t part[kFewWaves][2][NB][64];
+  __shared__ acc_t part[kFewWaves][2][64];
   const WsView ws = ws_view(p.ws, p.G);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
   const int64_t *__restrict__ off = ws.off;
-  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(tile_rows)];
+  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(32)];
   const int tiles_j = (int)((p.F + kCols - 1) / kCols);
   const int64_t total = (int64_t)pre[p.G] * tiles_j;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -66,9 +64,9 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p, int t
     const int qt = (int)(w / tiles_j), jt = (int)(w - (int64_t)qt * tiles_j);
     const int g = find_group(pre, p.G, qt);
     if (!device_check(g >= 0 && g < p.G, p.ws)) continue;
-    const int64_t g_off = off[g], in_group = (int64_t)(qt - pre[g]) * tile_rows;
-    const int64_t rows = min64(tile_rows, off[g + 1] - g_off - in_group), row0 = g_off + in_group;
-    if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T, p.ws)) continue;
+    const int64_t row0 = off[g];
+    const int rows = (int)min64(16, off[g + 1] - row0);
+    if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T && qt == pre[g], p.ws)) continue;
     const int64_t col0 = (int64_t)jt * kCols;
     // weight rows of the first 16 columns and of the second: the other half, or the next 16
     const char *wg = group_weights<IN, EPI>(p, g);
@@ -81,99 +79,71 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p, int t
     const bool low0 = (r & 7) < cols0, high0 = (r & 7) + 8 < cols0;
     const bool low1 = (r & 7) < cols1, high1 = (r & 7) + 8 < cols1;
 
-    for (int64_t first = 0; first < rows; first += 16 * NB) {
-      const __amdgpu_buffer_rsrc_t xr = few_rsrc(p.x + (row0 + first) * kb);
-      const int left = (int)min64(16 * NB, rows - first);
-      acc_t acc[2][NB];
+    const __amdgpu_buffer_rsrc_t xr = few_rsrc(p.x + row0 * kb);
+    const bool lowx = (r & 7) < rows, highx = (r & 7) + 8 < rows;
+    acc_t acc[2] = {acc_t{0, 0, 0, 0}, acc_t{0, 0, 0, 0}};
+    struct Unit {
+      RowBlock g, u, x;
+    };
+    auto load = [&](Unit &n, uint32_t at) {
+      const bool in = at + chunk < kb;
+      n.g.load(w0, in && low0 ? low + at : kPastEnd, in && high0 ? high + at : kPastEnd);
+      n.u.load(w1, in && low1 ? low + at : kPastEnd, in && high1 ? high + at : kPastEnd);
+      n.x.load(xr, in && lowx ? low + at : kPastEnd, in && highx ? high + at : kPastEnd);
+    };
+    auto multiply = [&](const Unit &n) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[h][b] = acc_t{0, 0, 0, 0};
-      struct Unit {
-        RowBlock g, u, x[NB];
-      };
-      auto load = [&](Unit &n, uint32_t at) {
-        const bool in = at + chunk < kb;
-        n.g.load(w0, in && low0 ? low + at : kPastEnd, in && high0 ? high + at : kPastEnd);
-        n.u.load(w1, in && low1 ? low + at : kPastEnd, in && high1 ? high + at : kPastEnd);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int xl = b * 16 + (r & 7);
-          n.x[b].load(xr, in && xl < left ? (uint32_t)xl * kb + chunk + at : kPastEnd,
-                      in && xl + 8 < left ? (uint32_t)(xl + 8) * kb + chunk + at : kPastEnd);
-        }
-      };
-      auto multiply = [&](const Unit &n) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const i32x4_t wg_ = n.g.chunk(c), wu_ = n.u.chunk(c);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const i32x4_t xv = n.x[b].chunk(c);
-            acc[0][b] = Op::mma(wg_, xv, acc[0][b]);
-            acc[1][b] = Op::mma(wu_, xv, acc[1][b]);
-          }
-        }
-      };
-      // two units in turn, so the next one's loads are in flight during a unit's products; a
-      // unit past the row's end loads zeros
-      constexpr uint32_t step = kFewWaves * 128;
-      Unit u0, u1;
-      uint32_t at = wave * 128;
-      load(u0, at);
-      load(u1, at + step);
-      for (; at < kb; at += 2 * step) {
-        multiply(u0);
-        load(u0, at + 2 * step);
-        multiply(u1);
-        load(u1, at + 3 * step);
+      for (int c = 0; c < 2; ++c) {
+        const i32x4_t xv = n.x.chunk(c);
+        acc[0] = Op::mma(n.g.chunk(c), xv, acc[0]);
+        acc[1] = Op::mma(n.u.chunk(c), xv, acc[1]);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) part[wave][h][b][lane] = acc[h][b];
-      __syncthreads();
-      for (int b = wave; b < NB; b += kFewWaves) {
-        acc_t s[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[h] = part[0][h][b][lane];
-#pragma unroll
-          for (int v = 1; v < kFewWaves; ++v) s[h] += part[v][h][b][lane];
-        }
-        const int xl = b * 16 + r;
-        if (xl >= left) continue;
-        const int64_t row = row0 + first + xl;
-        const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
-        const int c = 4 * q;
-        if constexpr (EPI == EPI_PLAIN) {
-          if (c < cols0)
-            put4<EL>(p.out, row * p.F + col0 + c, finish<IN, EL>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)));
-          if (c < cols1)
-            put4<EL>(p.out, row * p.F + second + c, finish<IN, EL>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
-        } else if (c < cols0) {
-          const float4 v0 = finish<IN, EL>(s[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
-          const float4 v1 = finish<IN, EL>(s[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
-          with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
-        }
-      }
-      __syncthreads();
+    };
+    // two units in turn, so the next one's loads are in flight during a unit's products; a
+    // unit past the row's end loads zeros
+    constexpr uint32_t step = kFewWaves * 128;
+    Unit u0, u1;
+    uint32_t at = wave * 128;
+    load(u0, at);
+    load(u1, at + step);
+    for (; at < kb; at += 2 * step) {
+      multiply(u0);
+      load(u0, at + 2 * step);
+      multiply(u1);
+      load(u1, at + 3 * step);
     }
+    part[wave][0][lane] = acc[0];
+    part[wave][1][lane] = acc[1];
+    __syncthreads();
+    if (wave == 0 && r < rows) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v) acc[h] += part[v][h][lane];
+      const int64_t row = row0 + r;
+      const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
+      const int c = 4 * q;
+      if constexpr (EPI == EPI_PLAIN) {
+        if (c < cols0)
+          put4<EL>(p.out, row * p.F + col0 + c, finish<IN, EL>(acc[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)));
+        if (c < cols1)
+          put4<EL>(p.out, row * p.F + second + c, finish<IN, EL>(acc[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
+      } else if (c < cols0) {
+        const float4 v0 = finish<IN, EL>(acc[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
+        const float4 v1 = finish<IN, EL>(acc[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
+        with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
+      }
+    }
+    __syncthreads();
   }
 }
 
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu_few(const GluParams &p, hipStream_t s) {
   constexpr int kCols = EPI == EPI_PLAIN ? 32 : 16;
-  const int64_t groups = p.T < p.G ? p.T : p.G;
-  auto grid = [&](int tile) {
-    const int64_t items = ((p.T + tile - 1) / tile + groups) * ((p.F + kCols - 1) / kCols);
-    return dim3((unsigned)(items < 4096 ? items : 4096));
-  };
-  if (p.T <= 16)
-    hipLaunchKernelGGL((glu_few_kernel<IN, EL, EPI, 1>), grid(32), dim3(kFewThreads), 0, s, p, 32);
-  else
-    hipLaunchKernelGGL((glu_few_kernel<IN, EL, EPI, 4>), grid(64), dim3(kFewThreads), 0, s, p, 64);
+  const int64_t items = (p.T < p.G ? p.T : p.G) * ((p.F + kCols - 1) / kCols);
+  hipLaunchKernelGGL((glu_few_kernel<IN, EL, EPI>), dim3((unsigned)(items < 4096 ? items : 4096)), dim3(kFewThreads), 0,
+                     s, p);
   return hipGetLastError();
 }
 

@@ -1,0 +1,161 @@
+// Grouped products with a gated or scaled epilogue on small tiles, where 256-row tiles would be
+// too few to fill the chip: 64 rows by 64 weight rows (4 waves, two workgroups a CU) or 128 by
+// 128 (8 waves), half of the weight rows the gate's and half the other's of the same columns
+// (plain: neighbouring columns).
+//
+// Stages of 128 bytes of every row go straight to a ring of kStages in LDS, kStages - 1 ahead, and
+// one barrier a stage does for both sides: after it every wave's loads of the stage are there,
+// and every wave has read the stage before, whose place the next loads take.  Waves are 2 by
+// WAVES / 2; a wave has every other block of 16 rows (those past the tile's last row are skipped)
+// by 16 columns of either half, so h_g and h_u are in the same lane.
+#pragma once
+
+#include "gl_gemm_tile.hpp"
+#include "gl_glu_few.hpp"
+
+namespace gl {
+
+template <int ROWS>
+struct MidTile {
+  static constexpr int kWaves = ROWS / 16, kThreads = 64 * kWaves;
+  static constexpr int kStages = 4;
+  static constexpr int kStageBytes = 2 * ROWS * 128;  // rows, then weight rows
+  static constexpr int kPieces = kStageBytes / 1024 / kWaves;
+  static constexpr int kBlocks = ROWS / 32;  // of 16 rows, of a wave
+  static constexpr int kColsHalf = ROWS / 2;  // weight rows of a half
+  static_assert(kPieces == 4 && kColsHalf == 16 * (kWaves / 2), "waves cover the tile");
+};
+
+template <int IN, int EL, int EPI, int ROWS>
+__global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(GluParams p) {
+  using Op = Operand<IN>;
+  using acc_t = typename Op::acc_t;
+  using M = MidTile<ROWS>;
+  constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
+  __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
+
+  const WsView ws = ws_view(p.ws, p.G);
+  if (!ws_usable(ws.hdr, p.G, p.T)) return;
+  const int64_t *__restrict__ off = ws.off;
+  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(ROWS)];
+  const int tiles_j = (int)((p.F + kCols - 1) / kCols);
+  const int64_t total = (int64_t)pre[p.G] * tiles_j;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int fr = lane & 15, fq = lane >> 4;
+  const int kb = (int)(p.K * in_bytes(IN));
+  const int nk = (kb + 127) / 128;
+  // pieces of 8 rows: wave w has the pieces w, w + kWaves (of the rows), and so of the weight rows
+  const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;
+  const uint32_t voff = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)kb + (uint32_t)c16;
+
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int qt = (int)(w / tiles_j), jt = (int)(w - (int64_t)qt * tiles_j);
+    const int g = find_group(pre, p.G, qt);
+    if (!device_check(g >= 0 && g < p.G, p.ws)) continue;
+    const int64_t row0 = off[g] + (int64_t)(qt - pre[g]) * ROWS;
+    const int rows = (int)min64(ROWS, off[g + 1] - row0);
+    if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T, p.ws)) continue;
+    const int64_t col0 = (int64_t)jt * kCols, left = p.F - col0;
+    const int64_t second = EPI == EPI_PLAIN ? col0 + M::kColsHalf : p.F + col0;
+    const char *wg = group_weights<IN, EPI>(p, g);
+    auto rsrc = [&](const char *at, int64_t n) {
+      return __builtin_amdgcn_make_buffer_rsrc((void *)gemm::uniform_ptr(at), (short)0, (int)n * kb, 0x00020000);
+    };
+    const bool has1 = EPI != EPI_PLAIN || left > M::kColsHalf;
+    const __amdgpu_buffer_rsrc_t rx = rsrc(p.x + row0 * kb, rows);
+    const __amdgpu_buffer_rsrc_t r0 = rsrc(wg + col0 * kb, min64(M::kColsHalf, left));
+    // (no second half: one row of the first, whose products are not stored)
+    const __amdgpu_buffer_rsrc_t r1 =
+        has1 ? rsrc(wg + second * kb, min64(M::kColsHalf, EPI == EPI_PLAIN ? left - M::kColsHalf : left))
+             : rsrc(wg + col0 * kb, 1);
+    auto issue = [&](int s) {
+      char *st = lds + (s % M::kStages) * M::kStageBytes;
+      const int at = s * 128, lim = s < nk ? kb - at : 0;
+      const uint32_t far = (uint32_t)(8 * M::kWaves) * (uint32_t)kb;  // from a wave's piece of a half to its next
+      const uint32_t o0 = c16 < lim ? voff : kPastEnd, o1 = c16 < lim ? voff + far : kPastEnd;
+      const int soff = lim > 0 ? at : 0;
+      // a half of weight rows is kWaves pieces, the rows 2 kWaves
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + wave * 1024), 16, o0, soff, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + (wave + M::kWaves) * 1024), 16, o1, soff, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (GL_LDS void *)(st + (wave + 2 * M::kWaves) * 1024), 16, o0, soff, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, (GL_LDS void *)(st + (wave + 3 * M::kWaves) * 1024), 16, o0, soff, 0, 0);
+    };
+    const int blocks = (rows - wm * 16 + 31) / 32;  // of the wave that hold rows
+    acc_t acc[2][M::kBlocks];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < M::kBlocks; ++i) acc[h][i] = acc_t{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < M::kStages - 1; ++s) issue(s);
+    for (int s = 0; s < nk; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      gemm::wait_vm<(M::kStages - 2) * M::kPieces>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue(s + M::kStages - 1);
+      const char *st = lds + (s % M::kStages) * M::kStageBytes;
+      auto frag = [&](int row, int c) {
+        const int r = row + fr;
+        return *(const i32x4_t *)(st + r * 128 + (((4 * c + fq) ^ ((r >> 1) & 7)) << 4));
+      };
+      i32x4_t b[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) b[h][c] = frag(ROWS + h * M::kColsHalf + wn * 16, c);
+#pragma unroll
+      for (int i = 0; i < M::kBlocks; ++i) {
+        if (i >= blocks) break;
+        const i32x4_t a0 = frag(i * 32 + wm * 16, 0), a1 = frag(i * 32 + wm * 16, 1);
+        acc[0][i] = Op::mma(b[0][0], a0, acc[0][i]);
+        acc[1][i] = Op::mma(b[1][0], a0, acc[1][i]);
+        acc[0][i] = Op::mma(b[0][1], a1, acc[0][i]);
+        acc[1][i] = Op::mma(b[1][1], a1, acc[1][i]);
+      }
+    }
+    const int c = wn * 16 + fq * 4;
+    const bool in0 = c < left, in1 = EPI == EPI_PLAIN ? c + M::kColsHalf < left : in0;
+    if (in0) {
+      const ColumnTerms<IN, EL> t0 = column_terms<IN, EL, EPI>(p, g, col0 + c);
+      const ColumnTerms<IN, EL> t1 = column_terms<IN, EL, EPI>(p, g, in1 ? second + c : col0 + c);
+      auto finish_all = [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < M::kBlocks; ++i) {
+          const int rl = i * 32 + wm * 16 + fr;
+          if (rl >= rows) break;
+          const int64_t row = row0 + rl;
+          const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
+          const float4 v0 = finish<IN, EL>(acc[0][i], rs, t0), v1 = finish<IN, EL>(acc[1][i], rs, t1);
+          if constexpr (EPI == EPI_PLAIN) {
+            put4<EL>(p.out, row * p.F + col0 + c, v0);
+            if (in1) put4<EL>(p.out, row * p.F + second + c, v1);
+          } else {
+            gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1);
+          }
+        }
+      };
+      if constexpr (EPI == EPI_PLAIN) finish_all(std::integral_constant<int, ACT_SILU>{});
+      else with_activation(p.act, finish_all);
+    }
+    // the loads past the last stage (zeros) are done, and every wave has read, before the ring is
+    // filled again or the workgroup ends
+    gemm::wait_vm0();
+    __syncthreads();
+  }
+}
+
+template <int IN, int EL, int EPI, int ROWS>
+inline hipError_t launch_glu_mid(const GluParams &p, hipStream_t s) {
+  using M = MidTile<ROWS>;
+  constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
+  const int64_t groups = p.T < p.G ? p.T : p.G;
+  const int64_t items = ((p.T + ROWS - 1) / ROWS + groups) * ((p.F + kCols - 1) / kCols);
+  hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS>), dim3((unsigned)(items < 8192 ? items : 8192)),
+                     dim3(M::kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace gl

@@ -5,7 +5,9 @@
 // columns).  So h_g and h_u of an output are in the same lane, and the epilogue is in registers.
 // The contraction goes by stages of 128 bytes of every row (64 values of 16 bits, 128 of 8, 32
 // of 32: the same kernel for each, but for the matrix instruction).  Waves are 4 x 2; a wave has
-// 32 + 32 rows (of A0 and A1, the tile's halves) by 64 + 64 columns (of B0 and B1).
+// two blocks of 16 rows, 64 rows apart, of each half of the tile's rows, A0 and A1, by 64 columns
+// of each of B0 and B1 (so where blocks past the tile's last row are skipped, 64 rows are a quarter
+// of the work for every wave).
 //
 // A stage is four phases, one quadrant of the wave's outputs each, and each phase reads half
 // an operand from LDS, asks for half an operand of the stage after next, and multiplies:
@@ -35,7 +37,7 @@
 #pragma once
 
 #include "gl_gemm_tile.hpp"
-#include "gl_glu_few.hpp"
+#include "gl_glu_mid.hpp"
 
 namespace gl {
 
@@ -125,7 +127,9 @@ struct TilePlace {
 
 // ACT: a run-time activation would be three copies of the epilogue, whose common values the
 // compiler computes ahead of them all and spills.
-template <int IN, int EL, int EPI, int ACT>
+// RAGGED: row blocks past a tile's rows are neither read from LDS nor multiplied, which costs full
+// tiles a tenth of their speed in branches.
+template <int IN, int EL, int EPI, int ACT, bool RAGGED>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
@@ -244,11 +248,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
                               (((4 * s + fq) ^ ((r >> 1) & 7)) << 4));
   };
   i32x4_t fa[2][2], fb[2][4][2];  // [block][half of the stage]; two sets of B
+  int blocks = 4;  // row blocks of the wave that hold rows: (A half, i) in turn are 64 rows apart
   auto read_a = [&](int half, int ring) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
+      if (!RAGGED || 2 * half + i < blocks)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) fa[i][s] = frag(half, wm * 32 + i * 16, ring, s);
+        for (int s = 0; s < 2; ++s) fa[i][s] = frag(half, i * 64 + wm * 16, ring, s);
   };
   auto read_b = [&](int set, int half, int ring) {
 #pragma unroll
@@ -267,13 +273,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
 #pragma unroll
           for (int l = 0; l < 4; ++l) acc[i][j][k][l] = acc_t{0, 0, 0, 0};
   };
-  auto multiply = [&](int set, acc_t(&c)[2][4]) {
+  auto multiply = [&](int set, int half, acc_t(&c)[2][4]) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < 2; ++i)
+      if (!RAGGED || 2 * half + i < blocks)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = Op::mma(fb[set][j][s], fa[i][s], c[i][j]);
+          for (int j = 0; j < 4; ++j) c[i][j] = Op::mma(fb[set][j][s], fa[i][s], c[i][j]);
   };
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
   auto barrier = [&] {
@@ -293,23 +300,23 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     read_a(0, ring);
     issue(2, ring);
     read_done();
-    multiply(S, acc[0][0]);
+    multiply(S, 0, acc[0][0]);
     barrier();
     read_b(1 - S, 3, ring);
     issue(0, ring);
     read_done();
-    multiply(1 - S, acc[0][1]);
+    multiply(1 - S, 0, acc[0][1]);
     barrier();
     read_a(1, ring);
     issue(3, ring);
     read_done();
-    multiply(1 - S, acc[1][1]);
+    multiply(1 - S, 1, acc[1][1]);
     barrier();
     read_b(1 - S, 2, ring ^ 1);
     issue(1, ring);
     next_stage();
     read_done();
-    multiply(S, acc[1][0]);
+    multiply(S, 1, acc[1][0]);
     barrier();
   };
 
@@ -330,6 +337,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   int ring = 0;
   for (int n = 0; n < count; ++n) {
     zero();
+    const TilePlace t = place(n);
+    blocks = (t.rows - wm * 16 + 63) / 64;
     // B0 of the first stage (again: the last tile's last stage read it, but held through the
     // epilogue it would cost 32 registers), by all waves before the first loads may replace it
     read_b(0, 2, ring);
@@ -347,7 +356,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     }
     if (wave < 4) barrier();  // in step again: both groups' epilogues at the same time
 
-    const TilePlace t = place(n);
     // the lane index, opaque here, so that nothing of the epilogue's addresses is kept in registers
     // through the stages
     int le = lane;
@@ -369,13 +377,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + wm * 32 + i * 16 + er, t.rows - 1)] : 0.f;
+        rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, t.rows - 1)] : 0.f;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         typedef Quad<EL> Q;
-        const TileStore<EL> st{lds + 2 * kRingBytes + wave * kStoreBytes, le, a * kHalf + wm * 32 + i * 16, t.rows, wn * 64};
+        const TileStore<EL> st{lds + 2 * kRingBytes + wave * kStoreBytes, le, a * kHalf + i * 64 + wm * 16, t.rows, wn * 64};
+        if (2 * a + i >= blocks) continue;
         auto value = [&](int b, int j) { return finish<IN, EL>(acc[a][b][i][j], rs[a][i], ct[b][j]); };
         auto gate = [&](int j) { return Q::pack(value(0, j)); };
         auto other = [&](int j) { return Q::pack(value(1, j)); };
@@ -413,26 +422,47 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   gemm::wait_vm0();  // no load may be under way to the LDS of a workgroup that has ended
 }
 
-template <int IN, int EL, int EPI>
-inline hipError_t launch_glu_tile(const GluParams &p, hipStream_t s) {
-  constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;
-  const int64_t groups = p.T < p.G ? p.T : p.G;
-  const int64_t items = ((p.T + kTileRowsM - 1) / kTileRowsM + groups) * ((p.F + kColsB - 1) / kColsB);
+template <int IN, int EL, int EPI, int ACT>
+inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, bool ragged, hipStream_t s) {
   const dim3 grid(gemm::persistent_grid(items)), block(kTileThreads);
-  if (EPI == EPI_PLAIN || p.act == ACT_SILU)
-    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT_SILU>), grid, block, 0, s, p);
-  else if (p.act == ACT_GELU)
-    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, EPI == EPI_PLAIN ? ACT_SILU : ACT_GELU>), grid, block, 0, s, p);
+  if (ragged)
+    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, true>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, EPI == EPI_PLAIN ? ACT_SILU : ACT_GELU_TANH>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
-// Few rows a group (up to 32 on average, or 64 in all): the kernel that only streams weights.
+// Which kernel, by the rows of a group that has any (on average: the splits are on the device) and
+// the most tiles there can be.  The tiles of 256 rows multiply at the rate of the matrix cores, those
+// of 128 and 64 are enough for the chip in smaller problems and waste less on groups of few rows.
+// Measured (us; 64 / 128 / 256 rows):
+//   by rows a group, K 4096 F 7168, 8 groups, bf16:    16 rows 183 / 195 / 196   32 rows 217 / 189 / 208
+//                                                     128 rows 418 / 250 / 254  512 rows 1350 / 656 / 444
+//   by tiles, one group, K 4096 F 4096: 512 rows (96 tiles of 256) 66 / 39 / 70   1024 (160) 130 / 76 / 71
+//     K 1024 F 1024: 512 rows (80 tiles of 128, 24 of 256) 8.8 / 12.8 / 23        2048 (272, 72) 19 / 15 / 25
+//   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
+//     4 groups, 333 rows, K 1024 F 2048 37 / 69 / 216;  8 groups, 16384 rows, K 4096 F 7168
+//     (4032 tiles of 256) 16504 / 14747 / 14029
+// and at most 16 rows with few columns: 4 of 4 groups, K 1024 F 512, fp32, 9.5 by splitting the
+// contraction and 16 by 64 rows (64 workgroups); 8 of 64 groups, K 2048 F 768 16.1 and 11.8 (192).
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
-  if (p.T <= 64 || p.T <= (int64_t)32 * p.G) return launch_glu_few<IN, EL, EPI>(p, s);
-  return launch_glu_tile<IN, EL, EPI>(p, s);
+  const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
+  constexpr int64_t kWide = EPI == EPI_PLAIN ? 1 : 2;  // weight rows a column
+  auto tiles = [&](int64_t r) { return ((p.T + r - 1) / r + groups) * ((kWide * p.F + r - 1) / r); };
+  if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= 128) return launch_glu_few<IN, EL, EPI>(p, s);
+  const bool large = IN == IN_F32 ? tiles(256) >= 2048 : rows > 96 && tiles(256) >= 160;
+  if (!large) {
+    if constexpr (IN != IN_F32)
+      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128>(p, s);
+    return launch_glu_mid<IN, EL, EPI, 64>(p, s);
+  }
+  const bool ragged = rows <= 256;  // 8 groups of 256 rows: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
+  if constexpr (EPI != EPI_PLAIN) {
+    if (p.act == ACT_GELU) return launch_glu_tile<IN, EL, EPI, ACT_GELU>(p, tiles(256), ragged, s);
+    if (p.act == ACT_GELU_TANH) return launch_glu_tile<IN, EL, EPI, ACT_GELU_TANH>(p, tiles(256), ragged, s);
+  }
+  return launch_glu_tile<IN, EL, EPI, ACT_SILU>(p, tiles(256), ragged, s);
 }
 
 }  // namespace gl

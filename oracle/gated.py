@@ -6,9 +6,9 @@ from __future__ import annotations
 import math
 
 import numpy as np
+from scipy.special import erf as _erf
 
 ACTS = ("silu", "gelu", "gelu_tanh")
-_erf = np.vectorize(math.erf, otypes=[np.float64])
 
 
 def _sigmoid(v):
