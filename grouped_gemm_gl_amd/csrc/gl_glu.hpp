@@ -112,6 +112,19 @@ struct GluParams {
   int64_t T, K, F;
 };
 
+// The products of the backward, out = dh w (dx) or dh^T x (dW), for each group.
+struct BackParams {
+  const char *a;  // dh [T, 2F]
+  const char *b;  // dx: w [G, 2F, K] or
+  const char *const *b_ptrs;
+  const char *x;  // dW: x [T, K]
+  void *out;      // dx [T, K]; dW [G, 2F, K] or
+  void *const *out_ptrs;
+  const void *ws;
+  int G, accumulate;
+  int64_t T, K, N;  // N = 2F
+};
+
 template <int IN, int EPI>
 __device__ __forceinline__ const char *group_weights(const GluParams &p, int g) {
   const int64_t n = EPI == EPI_PLAIN ? p.F : 2 * p.F;

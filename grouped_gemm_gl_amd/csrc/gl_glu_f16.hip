@@ -1,10 +1,16 @@
-// The gated grouped product and its gradient for f16 operands and outputs.
+// The gated grouped product and its gradient for f16 operands and outputs, and the products of its
+// backward on small tiles.
+#include "gl_glu_back.hpp"
 #include "gl_glu_tile.hpp"
 
 namespace gl {
 
 hipError_t launch_glu_f16(const GluParams &p, bool grad, hipStream_t s) {
   return grad ? launch_glu<IN_F16, EL_F16, EPI_GLU_GRAD>(p, s) : launch_glu<IN_F16, EL_F16, EPI_GLU>(p, s);
+}
+
+hipError_t launch_glu_back_f16(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s) {
+  return launch_glu_back<IN_F16, EL_F16>(p, wgrad, out_f32, s);
 }
 
 }  // namespace gl

@@ -112,3 +112,69 @@ def test_every_split_of_the_rows_gives_the_same_rows():
         a = L.new(361, F)
         gl.gl_glu_forward(L.dx_, [L.dw_[0]] * len(m), a, ws)
         check(a, *glu_limits("silu", ref_h, e, BF), str(m))
+
+
+# products of the backward: (rows of the groups, K, F) by the tile of dx / of dW that they take
+BACK = {
+    "64": ([5, 0, 70, 20], 264, 72),
+    "128": ([130, 0, 400, 257, 300], 2056, 520),       # dx 192 tiles of 128, dW more
+    "dw256": ([3, 0, 129, 0, 66, 1], 2312, 2312),      # dW over 1024 tiles of 256
+    "dx256": ([300, 2, 513], 8200, 40),                # dx 165 tiles of 256
+}
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("path", BACK)
+def test_backward_products(path, dtype, wide):
+    m, K, F = BACK[path]
+    L = Layer(m, K, F, dtype, bias=False, seed=K)
+    h = torch.randn(L.T, 2 * F, generator=torch.Generator().manual_seed(1)).to(dtype)
+    dw0 = torch.randn(L.G, 2 * F, K, generator=torch.Generator().manual_seed(2))
+    dw = dw0.to(DEV) if wide else L.new(L.G, 2 * F, K)
+    dh, dx, db = L.new(L.T, 2 * F), nan_tail(L.T + 1, K, L.T, dtype, DEV), L.new(L.G, 2 * F)
+    gl.gl_glu_backward(L.dx_, L.dw_, L.dda, dh, dx, [v for v in dw] if wide else dw, L.ws, h=h.to(DEV), db=db,
+                       accumulate=wide)
+    check(dh, *grad_limits("silu", to64(h), np.zeros(h.shape), to64(L.da), dtype), "dh")
+    x, w, d = to64(L.x), to64(L.w), to64(dh)
+    rx, rw, rb = gated.glu_backward(x, w, d, m)
+    mx, mw, mb = gated.glu_backward(np.abs(x), np.abs(w), np.abs(d), m)
+    n = np.array(m)[:, None, None]
+    v = 2.0 ** -23
+    check(dx[:L.T], rx, (2 * F + 2) * v * mx + half_step(dtype, rx), "dx")
+    assert torch.isnan(dx[L.T:]).all()
+    if wide:
+        rw, mw = rw + to64(dw0), mw + np.abs(to64(dw0))
+    check(dw, rw, (n + 3) * v * mw + half_step(F32 if wide else dtype, rw), "dw")
+    check(db, rb, (n[..., 0] + 2) * v * mb + half_step(dtype, rb), "db")
+
+
+def test_backward_products_f32():
+    m, K, F = [130, 0, 1, 257], 516, 260
+    L = Layer(m, K, F, F32, bias=False, seed=3)
+    h = torch.randn(L.T, 2 * F, generator=torch.Generator().manual_seed(1))
+    dw, dh, dx = L.new(L.G, 2 * F, K), L.new(L.T, 2 * F), L.new(L.T, K)
+    gl.gl_glu_backward(L.dx_, L.dw_, L.dda, dh, dx, dw, L.ws, h=h.to(DEV))
+    x, w, d = to64(L.x), to64(L.w), to64(dh)
+    rx, rw, _ = gated.glu_backward(x, w, d, m)
+    mx, mw, _ = gated.glu_backward(np.abs(x), np.abs(w), np.abs(d), m)
+    v = 2.0 ** -24
+    check(dx, rx, (2 * F + 2) * v * mx + half_step(F32, rx), "dx")
+    check(dw, rw, (np.array(m)[:, None, None] + 2) * v * mw + half_step(F32, rw), "dw")
+
+
+def test_backward_keeps_nan_in_its_group():
+    """Rows and weights of other groups that are NaN reach neither product of a group."""
+    m, K, F = [30, 41, 9], 264, 72
+    L = Layer(m, K, F, BF, bias=False)
+    h = torch.randn(L.T, 2 * F, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    outs = []
+    for bad in (False, True):
+        x, w, da = L.dx_.clone(), L.dw_.clone(), L.dda.clone()
+        if bad:
+            x[:30], x[71:], w[0], w[2], da[:30], da[71:] = [float("nan")] * 6
+        dh, dx, dw = L.new(L.T, 2 * F), L.new(L.T, K), L.new(3, 2 * F, K)
+        gl.gl_glu_backward(x, w, da, dh, dx, dw, L.ws, h=h)
+        outs.append((dx, dw))
+    assert torch.equal(outs[0][0][30:71], outs[1][0][30:71]) and torch.equal(outs[0][1][1], outs[1][1][1])
+    assert torch.isnan(outs[1][0][:30]).all() and torch.isnan(outs[1][1][0]).all()
