@@ -70,7 +70,6 @@ hipError_t launch_glu_f32(const GluParams &p, bool grad, hipStream_t s);
 hipError_t launch_glu_back_bf16(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s);
 hipError_t launch_glu_back_f16(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s);
 hipError_t launch_glu_back_f32(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s);
-bool glu_back_small_tiles(const BackParams &p, bool wgrad);
 hipError_t launch_glu_int8(int el_out, const GluParams &p, bool gated, hipStream_t s);
 hipError_t launch_glu_grad(int el, int64_t T, int64_t F, int act, const void *h, const void *da, void *dh, void *a,
                            hipStream_t s);
@@ -816,7 +815,7 @@ int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, i
   gl::BackParams bp{};
   bp.a = (const char *)dh; bp.b = (const char *)w; bp.b_ptrs = (const char *const *)w_ptrs; bp.x = (const char *)x;
   bp.ws = workspace; bp.G = G; bp.T = T; bp.K = K; bp.N = 2 * F;
-  auto small = [&](bool wgrad, void *out, void *const *out_ptrs) {
+  auto product = [&](bool wgrad, void *out, void *const *out_ptrs) {
     gl::BackParams q = bp;
     q.out = out; q.out_ptrs = out_ptrs; q.accumulate = wgrad && accumulate;
     const bool out_f32 = wgrad && wgrad_dtype == GL_F32;
@@ -826,8 +825,8 @@ int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, i
                       who);
   };
   auto wgrad = [&](bool launch) {
-    if (launch && T > 0 && (dtype == GL_F32 || gl::glu_back_small_tiles(bp, true))) {
-      GL_TRY(small(true, dw, dw_ptrs));
+    if (launch && T > 0) {
+      GL_TRY(product(true, dw, dw_ptrs));
       if (!with_db) return ok();
       return hip_result(gl::launch_bgrad(G, 2 * F, T, el_code(dtype), dh, db, db_ptrs, workspace, stream), who);
     }
@@ -835,7 +834,7 @@ int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, i
                       db_ptrs, workspace, stream, launch);
   };
   auto dgrad = [&](bool launch) {
-    if (launch && T > 0 && (dtype == GL_F32 || gl::glu_back_small_tiles(bp, false))) return small(false, dx, nullptr);
+    if (launch && T > 0) return product(false, dx, nullptr);
     return dgrad_impl(G, K, 2 * F, T, dtype, dh, w, w_ptrs, dx, dx_rows, workspace, stream, launch);
   };
   // every step is checked before any is launched

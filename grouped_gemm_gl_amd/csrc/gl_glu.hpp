@@ -36,11 +36,12 @@ __device__ __forceinline__ float activate(float v, float &slope) {
     if (SLOPE) slope = p + times(v, 0.3989422804014327f * __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f));
     return times(v, p);
   } else if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)
-    const float v2 = v * v;
-    const float p = sigmoid_fast(v * (1.5957691216057308f + 0.07135481282651713f * v2));
+    // each step with one literal: two would hold a register each
+    const float v3 = v * v * v;
+    const float p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fmaf(v, -2.3022081983f, v3 * -0.1029432397f)));
     if (SLOPE) {
       const float q = p * (1.f - p);
-      slope = p + (q == 0.f ? 0.f : v * q * (1.5957691216057308f + 0.21406443847955140f * v2));
+      slope = p + (q == 0.f ? 0.f : q * fmaf(v, 1.5957691216f, v3 * 0.2140644385f));
     }
     return times(v, p);
   } else {
@@ -92,7 +93,7 @@ struct Operand<IN_I8> {
 };
 
 // ------------------------------------------------------------- a launch --
-enum { EPI_GLU = 0, EPI_GLU_GRAD = 1, EPI_PLAIN = 2 };
+enum { EPI_GLU = 0, EPI_GLU_GRAD = 1, EPI_PLAIN = 2, EPI_DX = 3, EPI_DW = 4 };
 
 struct GluParams {
   const char *x;              // [T, K]
@@ -110,6 +111,11 @@ struct GluParams {
   const void *ws;
   int G, act;
   int64_t T, K, F;
+  // The backward's products on the same tiles.  dx [T, F] = x [T, K] w [G, K, F], x being the
+  // gradient of h; dW [G, N, F] = x^T w for each group's rows of x [T, N] and w [T, F].
+  void *const *out_ptrs;  // dW: G x [N, F], or out
+  int64_t N;
+  int accumulate;
 };
 
 // The products of the backward, out = dh w (dx) or dh^T x (dW), for each group.
@@ -127,7 +133,7 @@ struct BackParams {
 
 template <int IN, int EPI>
 __device__ __forceinline__ const char *group_weights(const GluParams &p, int g) {
-  const int64_t n = EPI == EPI_PLAIN ? p.F : 2 * p.F;
+  const int64_t n = EPI == EPI_GLU || EPI == EPI_GLU_GRAD ? 2 * p.F : p.F;
   return p.w ? p.w + (int64_t)g * n * p.K * in_bytes(IN) : p.w_ptrs[g];
 }
 

@@ -15,48 +15,9 @@
 // past the matrix take an offset outside.  Sums are fp32 in a fixed order (deterministic).
 #pragma once
 
-#include "gl_glu_mid.hpp"
+#include "gl_glu_tile.hpp"
 
 namespace gl {
-
-// 64 (or 32) contraction rows of TILE columns in LDS, as they lie in memory.
-template <int IN, int TILE>
-struct Turned {
-  static constexpr int E = in_bytes(IN), kRow = TILE * E, kRows = 128 / E;
-  static constexpr int kPieceRows = 1024 / kRow, kSlots = kRow / 16;
-  // slot of the 16-byte chunk c of row p.  16-bit: a read's half wave touches 2 chunks of the rows
-  // 4 t + 0..3 and 8 + 4 t + 0..3; 32-bit: 4 chunks of four rows that are 4 apart.
-  __device__ static __forceinline__ int slot(int p, int c) {
-    if (IN == IN_F32) return c ^ (((p >> 2) & 3) << 2);
-    if (kRow == 128) return c ^ ((((p >> 1) & 1) | (((p >> 3) & 1) << 1)) << 1);
-    return c ^ (((p & 3) | (((p >> 3) & 1) << 2)) << 1);
-  }
-  // 16 bytes of column col + l % 16: 16-bit, contraction values 8 (l / 16) .. + 7 of the stage's half c
-  // (of 32); 32-bit, 4 (l / 16) .. + 3 of the half (of 16)
-  __device__ static __forceinline__ i32x4_t frag(const char *st, int col, int c, int lane) {
-    const int q = lane & 15, g = lane >> 4;
-    i32x4_t o;
-    if constexpr (IN == IN_F32) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = 16 * c + 4 * g + e, at = (col + q) * 4;
-        o[e] = *(const int *)(st + p * kRow + (slot(p, at >> 4) << 4) + (at & 15));
-      }
-    } else {
-      const int at = (col + ((q & 3) << 2)) * 2;
-      gemm::v4i16 h[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int p = 32 * c + 8 * g + 4 * t + (q >> 2);
-        h[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (GL_LDS gemm::v4i16 *)(st + p * kRow + (slot(p, at >> 4) << 4) + (at & 15)));
-      }
-      const gemm::v8i16 v = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
-      o = __builtin_bit_cast(i32x4_t, v);
-    }
-    return o;
-  }
-};
 
 template <int IN, int EL, bool WGRAD, int TILE>
 __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(BackParams p) {
@@ -154,25 +115,36 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
       __builtin_amdgcn_sched_barrier(0);
       issue(s + M::kStages - 1);
       const char *st = lds + (s % M::kStages) * M::kStageBytes;
-      i32x4_t fb[2][2];
+      // read_turned waits for its reads, so what is multiplied next is read before
+      i32x4_t fb[2][2], fa[M::kBlocks][2];
+      if constexpr (IN != IN_F32) {
+        const uint32_t at[2] = {Tn::address(st + TILE * 128, wn * 32, lane), Tn::address(st + TILE * 128, wn * 32 + 16, lane)};
+        if constexpr (WGRAD) {
+          uint32_t ata[M::kBlocks];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < M::kBlocks; ++i) ata[i] = Tn::address(st, i * 32 + wm * 16, lane);
+          read_turned<Tn::kRow>(ata, fa);
+        }
+        read_turned<Tn::kRow>(at, fb);
+      } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) fb[h][c] = Tn::frag(st + TILE * 128, wn * 32 + h * 16, c, lane);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) fb[h][c] = Tn::frag(st + TILE * 128, wn * 32 + h * 16, c, lane);
+      }
 #pragma unroll
       for (int i = 0; i < M::kBlocks; ++i) {
         if (i >= blocks) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          i32x4_t fa;
-          if constexpr (WGRAD) {
-            fa = Tn::frag(st, i * 32 + wm * 16, c, lane);
-          } else {
+          if constexpr (!WGRAD) {
             const int r = i * 32 + wm * 16 + fr;
-            fa = *(const i32x4_t *)(st + r * 128 + (((4 * c + fq) ^ ((r >> 1) & 7)) << 4));
+            fa[i][c] = *(const i32x4_t *)(st + r * 128 + (((4 * c + fq) ^ ((r >> 1) & 7)) << 4));
+          } else if constexpr (IN == IN_F32) {
+            fa[i][c] = Tn::frag(st, i * 32 + wm * 16, c, lane);
           }
-          acc[0][i] = Op::mma(fb[0][c], fa, acc[0][i]);
-          acc[1][i] = Op::mma(fb[1][c], fa, acc[1][i]);
+          acc[0][i] = Op::mma(fb[0][c], fa[i][c], acc[0][i]);
+          acc[1][i] = Op::mma(fb[1][c], fa[i][c], acc[1][i]);
         }
       }
     }
@@ -209,35 +181,41 @@ inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether a product goes by the small tiles: fp32 always (the grouped calls' fp32 kernel works on the
-// vector units: 4 groups, 333 rows, K 1024, F 1024, both products 386 us; here 81), and 16-bit types
-// where 256 x 256 tiles are few.  Measured (us, bf16; tiles of 64 / 128 / 256):
-//   dx by tiles of 256:   16 (1 group, 256 rows, K 2048 F 2048) 41 / 60 / 59     64 (4, 1024, 2048, 2048) 79 / 62 / 86
-//                        132 (1, 8192, 1024, 1024) 92 / 73 / 49                  272 (64, 1024, 1024, 512) 42 / 43 / 31
-//   dW  by tiles of 256: 128 (1, 2048, 2048, 2048) 104 / 79 / 189                512 (4, 1024, 2048, 2048) 96 / 72 / 176
-//                        512 (1, 4096, 4096, 4096) 719 / 540 / 261              1024 (16, 1024, 2048, 1024) 112 / 89 / 56
-// (between, the 256-row kernel cuts long groups' tiles into parts that meet in memory)
-inline bool glu_back_small(const BackParams &p, bool wgrad) {
-  const int64_t groups = p.T < p.G ? p.T : p.G, tj = (p.K + 255) / 256;
-  if (!wgrad) return ((p.T + 255) / 256 + groups) * tj < 128;
-  const int64_t tiles = groups * ((p.N + 255) / 256) * tj;
-  return tiles < 512 || (tiles < 1024 && p.T / groups < 2048);
-}
-
-// Tiles of 128 where there are enough of them: dx 192 (4 groups, 1024 rows, K 2048 F 2048) 62 us, of
-// 64 79; 144 (16, 256, 1024, 512) 16.3 and 13.7.  dW 128 (1, 8192, 1024, 1024) 140 and 104; 1024 (4,
-// 1024, 2048, 2048) 72 and 96.  fp32 tiles of 128 are up to twice as slow and at most a tenth faster.
+// Which tiles.  fp32 always takes those of 64 (of 128 up to twice as slow, at most a tenth faster; the
+// grouped calls' fp32 kernel works on the vector units: 4 groups, 333 rows, K 1024 F 1024, both
+// products 386 us, here 82).  Measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
+//   dx by tiles of 256:  16 (1, 256, 2048, 2048) 25 / 41 / 88     64 (4, 1024, 2048, 2048) 50 / 41 / 87
+//                       144 (2, 4096, 2048, 2048) 116 / 89 / 89  272 (1, 4096, 4096, 4096) 439 / 318 / 220
+//      and rows a group: 16 (64, 1024, 1024, 512) 36 / 34 / 27    64 (64, 4096, 2048, 768) 119 / 103 / 130
+//      by tiles of 128: 144 (16, 256, 1024, 512) 9.9 / 11.9      192 (4, 1024, 2048, 2048) 50 / 41
+//   dW by tiles of 256:  32 (1, 8192, 1024, 1024) 81 / 92 / 196  128 (1, 2048, 2048, 2048) 75 / 59 / 63
+//                       256 (16, 256, 1024, 512) 32 / 25 / 17   1024 (16, 1024, 2048, 1024) 107 / 87 / 44
 template <int IN, int EL>
 inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s) {
   if constexpr (IN == IN_F32) {
     return wgrad ? launch_glu_back_tile<IN, EL, true, 64>(p, s) : launch_glu_back_tile<IN, EL, false, 64>(p, s);
   } else {
-    const int64_t groups = p.T < p.G ? p.T : p.G, tj = (p.K + 127) / 128;
+    const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
+    auto tiles = [&](int64_t r) {
+      return (wgrad ? groups * ((p.N + r - 1) / r) : (p.T + r - 1) / r + groups) * ((p.K + r - 1) / r);
+    };
+    GluParams q{};
+    q.x = p.a; q.ws = p.ws; q.G = p.G; q.T = p.T; q.F = p.K; q.out = p.out; q.out_ptrs = p.out_ptrs;
     if (!wgrad) {
-      if (((p.T + 127) / 128 + groups) * tj >= 192) return launch_glu_back_tile<IN, EL, false, 128>(p, s);
+      if (tiles(256) >= 160 && (rows <= 24 || rows > 96)) {
+        q.w = p.b; q.w_ptrs = p.b_ptrs; q.K = p.N;
+        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256), rows <= 256, s);
+      }
+      if (tiles(128) >= 192) return launch_glu_back_tile<IN, EL, false, 128>(p, s);
       return launch_glu_back_tile<IN, EL, false, 64>(p, s);
     }
-    if (groups * ((p.N + 127) / 128) * tj >= 192)
+    if (tiles(256) >= 128) {
+      q.w = p.x; q.N = p.N; q.accumulate = p.accumulate;
+      const int64_t items = (int64_t)p.G * ((p.N + 255) / 256) * ((p.K + 255) / 256);
+      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, false, s)
+                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, false, s);
+    }
+    if (tiles(128) >= 192)
       return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 128>(p, s) : launch_glu_back_tile<IN, EL, true, 128>(p, s);
     return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 64>(p, s) : launch_glu_back_tile<IN, EL, true, 64>(p, s);
   }

@@ -9,8 +9,6 @@ hipError_t launch_glu_bf16(const GluParams &p, bool grad, hipStream_t s) {
   return grad ? launch_glu<IN_BF16, EL_BF16, EPI_GLU_GRAD>(p, s) : launch_glu<IN_BF16, EL_BF16, EPI_GLU>(p, s);
 }
 
-bool glu_back_small_tiles(const BackParams &p, bool wgrad) { return glu_back_small(p, wgrad); }
-
 hipError_t launch_glu_back_bf16(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s) {
   return launch_glu_back<IN_BF16, EL_BF16>(p, wgrad, out_f32, s);
 }

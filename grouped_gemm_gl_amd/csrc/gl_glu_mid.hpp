@@ -15,6 +15,85 @@
 
 namespace gl {
 
+// 64 (or 32) contraction rows of TILE columns in LDS, as they lie in memory.
+template <int IN, int TILE>
+struct Turned {
+  static constexpr int E = in_bytes(IN), kRow = TILE * E, kRows = 128 / E;
+  static constexpr int kPieceRows = 1024 / kRow, kSlots = kRow / 16;
+  // slot of the 16-byte chunk c of row p.  16-bit: a read's half wave touches 2 chunks of the rows
+  // 4 t + 0..3 and 8 + 4 t + 0..3; 32-bit: 4 chunks of four rows that are 4 apart.
+  __device__ static __forceinline__ int slot(int p, int c) {
+    if (IN == IN_F32) return c ^ (((p >> 2) & 3) << 2);
+    if (kRow == 128) return c ^ ((((p >> 1) & 1) | (((p >> 3) & 1) << 1)) << 1);
+    return c ^ (((p & 3) | (((p >> 3) & 1) << 2)) << 1);
+  }
+  // 32-bit: 16 bytes of column col + l % 16, contraction values 4 (l / 16) .. + 3 of the stage's half c
+  // (of 16)
+  __device__ static __forceinline__ i32x4_t frag(const char *st, int col, int c, int lane) {
+    const int q = lane & 15, g = lane >> 4;
+    i32x4_t o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = 16 * c + 4 * g + e, at = (col + q) * 4;
+      o[e] = *(const int *)(st + p * kRow + (slot(p, at >> 4) << 4) + (at & 15));
+    }
+    return o;
+  }
+  // 16-bit: the lane's place in the stage for the transposing reads of columns col .. + 15.  Lane q of a group of
+  // 16 names row q / 4 and columns 4 (q % 4) .. + 3 of four rows, and gets column q of them; group g
+  // takes the rows 8 g .. + 7 of a half of 32 in two reads.
+  __device__ static __forceinline__ uint32_t place(int col, int lane) {
+    const int q = lane & 15, g = lane >> 4, p = 8 * g + (q >> 2), at = (col + ((q & 3) << 2)) * 2;
+    return p * kRow + (slot(p, at >> 4) << 4) + (at & 15);
+  }
+  __device__ static __forceinline__ uint32_t address(const char *st, int col, int lane) {
+    return (uint32_t)(uintptr_t)(GL_LDS const char *)st + place(col, lane);
+  }
+};
+
+// The fragments of B blocks of 16 columns, both halves of a stage: contraction values 8 (l / 16) ..
+// + 7 of column l % 16.  In one asm block with its wait: before the builtin the compiler waits for all
+// loads to LDS that are under way, the next stages' too.
+template <int ROW, int B>
+__device__ __forceinline__ void read_turned(const uint32_t (&at)[B], i32x4_t (&o)[B][2]) {
+  typedef __attribute__((ext_vector_type(2))) int i32x2_t;
+  i32x2_t v[B][4];
+#define GL_TR(n) "ds_read_b64_tr_b16 %" #n ", "
+  if constexpr (B == 1) {
+    asm volatile(GL_TR(0) "%4\n\t" GL_TR(1) "%4 offset:%c5\n\t" GL_TR(2) "%4 offset:%c6\n\t" GL_TR(3) "%4 offset:%c7\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3])
+                 : "v"(at[0]), "n"(4 * ROW), "n"(32 * ROW), "n"(36 * ROW)
+                 : "memory");
+  } else if constexpr (B == 2) {
+    asm volatile(GL_TR(0) "%8\n\t" GL_TR(1) "%8 offset:%c10\n\t" GL_TR(2) "%8 offset:%c11\n\t" GL_TR(3) "%8 offset:%c12\n\t"
+                 GL_TR(4) "%9\n\t" GL_TR(5) "%9 offset:%c10\n\t" GL_TR(6) "%9 offset:%c11\n\t" GL_TR(7) "%9 offset:%c12\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]), "=&v"(v[1][1]),
+                   "=&v"(v[1][2]), "=&v"(v[1][3])
+                 : "v"(at[0]), "v"(at[1]), "n"(4 * ROW), "n"(32 * ROW), "n"(36 * ROW)
+                 : "memory");
+  } else {
+    static_assert(B == 4, "blocks");
+    asm volatile(GL_TR(0) "%16\n\t" GL_TR(1) "%16 offset:%c20\n\t" GL_TR(2) "%16 offset:%c21\n\t" GL_TR(3) "%16 offset:%c22\n\t"
+                 GL_TR(4) "%17\n\t" GL_TR(5) "%17 offset:%c20\n\t" GL_TR(6) "%17 offset:%c21\n\t" GL_TR(7) "%17 offset:%c22\n\t"
+                 GL_TR(8) "%18\n\t" GL_TR(9) "%18 offset:%c20\n\t" GL_TR(10) "%18 offset:%c21\n\t" GL_TR(11) "%18 offset:%c22\n\t"
+                 GL_TR(12) "%19\n\t" GL_TR(13) "%19 offset:%c20\n\t" GL_TR(14) "%19 offset:%c21\n\t" GL_TR(15) "%19 offset:%c22\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]), "=&v"(v[1][1]),
+                   "=&v"(v[1][2]), "=&v"(v[1][3]), "=&v"(v[2][0]), "=&v"(v[2][1]), "=&v"(v[2][2]), "=&v"(v[2][3]),
+                   "=&v"(v[3][0]), "=&v"(v[3][1]), "=&v"(v[3][2]), "=&v"(v[3][3])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(4 * ROW), "n"(32 * ROW), "n"(36 * ROW)
+                 : "memory");
+  }
+#undef GL_TR
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      o[b][c] = i32x4_t{v[b][2 * c][0], v[b][2 * c][1], v[b][2 * c + 1][0], v[b][2 * c + 1][1]};
+}
+
 template <int ROWS>
 struct MidTile {
   static constexpr int kWaves = ROWS / 16, kThreads = 64 * kWaves;

@@ -26,9 +26,9 @@
 // barrier that ends its reading, so the loads that the other group sends after it may write there.
 //
 // The pipeline runs on over tiles: the last two stages of a tile ask for the first two of the
-// next, whose loads are under way during the epilogue.  So the tiles' addresses are found in
-// registers: lane i holds the place of the workgroup's i-th tile of 64 (filled by all lanes at
-// once), and nothing in the loop loads to registers or waits for it.
+// next, whose loads are under way during the epilogue.  So the tiles' places are
+// found ahead, 64 at a time by the lanes of each wave, and kept in LDS: nothing in the loop loads from
+// memory to registers, or waits for it.
 //
 // Addresses: every stream is a buffer resource on a half's first row whose length ends with the
 // last valid row, so rows past the group's or the matrix's end load zeros without a test; a lane's
@@ -49,35 +49,33 @@ constexpr int kRingBytes = 4 * kHalfBytes;   // A0, A1, B0, B1
 constexpr uint32_t kOutside = 0x80000000u;   // past every resource's end
 
 // 16 rows by 64 columns of a wave's part of an output between registers, where a lane has four
-// columns of a row in each of four blocks, and memory, as whole lines: through the wave's own 4 KiB
-// of LDS behind the ring.  Stored straight from the registers, 16 rows by 32 bytes an instruction,
-// the lines came together in L2 from quarters.  A row is kRow bytes there; its 16-byte slots are
-// permuted by the row so that neither side's accesses meet in a bank.  Rows and columns outside
-// go to an offset past the resource's end, which drops stores and loads zeros.
-constexpr int kStoreBytes = 4096;
+// columns of a row in each of four blocks, and memory, as whole lines: through the wave's own 2 KiB
+// of LDS behind the ring, 128 bytes of a row at a time (all 64 columns of 16-bit values, 32 of
+// 32-bit ones).  Stored straight from the registers, 16 rows by 32 bytes an instruction, the lines
+// came together in L2 from quarters.  The 16-byte slots of a row are permuted by the row so that
+// neither side's accesses meet in a bank.  Rows and columns outside go to an offset past the
+// resource's end, which drops stores and loads zeros.
+constexpr int kStoreBytes = 2048;
 template <int EL>
 struct TileStore {
   typedef typename Quad<EL>::raw raw_t;
   typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
   char *buf;
   int lane, row, rows, col;  // the piece's first row in the tile, rows of the tile, first column
-  static constexpr int E = elem_bytes(EL), kRow = 64 * E, kSlots = kRow / 16;
-  static constexpr int kMoves = 16 * kRow / 1024;  // of 16 bytes a lane
-  __device__ __forceinline__ static int slot(int r, int s) {
-    return (EL == EL_F32 ? s ^ (r & 15) : s ^ ((r >> 1) & 7)) << 4;
-  }
-  // the lane's four columns of block j
+  static constexpr int E = elem_bytes(EL), kBlocks = 8 / E, kPieces = 4 / kBlocks;
+  __device__ __forceinline__ static int slot(int r, int s) { return (s ^ ((r >> 1) & 7)) << 4; }
+  // the lane's four columns of block j of a piece
   __device__ __forceinline__ raw_t *quad(int j) const {
     const int r = lane & 15, q = lane >> 4;
-    return (raw_t *)(buf + r * kRow + (EL == EL_F32 ? slot(r, 4 * j + q) : slot(r, 2 * j + (q >> 1)) + (q & 1) * 8));
+    return (raw_t *)(buf + r * 128 + (E == 4 ? slot(r, 4 * j + q) : slot(r, 2 * j + (q >> 1)) + (q & 1) * 8));
   }
   // the lane's 16 bytes of move k: in LDS, and their offset from the tile's first row
   __device__ __forceinline__ u32x4_t *moved(int k) const {
-    const int r = k * (64 / kSlots) + lane / kSlots;
-    return (u32x4_t *)(buf + r * kRow + slot(r, lane % kSlots));
+    const int r = k * 8 + (lane >> 3);
+    return (u32x4_t *)(buf + r * 128 + slot(r, lane & 7));
   }
-  __device__ __forceinline__ uint32_t place(int k, int64_t ld, int width) const {
-    const int r = row + k * (64 / kSlots) + lane / kSlots, c = col + (lane % kSlots) * (16 / E);
+  __device__ __forceinline__ uint32_t place(int s, int k, int64_t ld, int width) const {
+    const int r = row + k * 8 + (lane >> 3), c = col + s * (128 / E) + (lane & 7) * (16 / E);
     return r < rows && c < width ? (uint32_t)((r * (int)ld + c) * E) : 0x80000000u;
   }
   __device__ __forceinline__ static void order() {  // lanes' accesses on either side stay there
@@ -91,38 +89,43 @@ struct TileStore {
   __device__ __forceinline__ void put(void *base, int64_t row0, int64_t ld, int64_t col0, int width, F value) const {
     const __amdgpu_buffer_rsrc_t rs = block(base, row0, ld, col0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *quad(j) = value(j);
-      __builtin_amdgcn_sched_barrier(0);  // one value's registers at a time
+    for (int s = 0; s < kPieces; ++s) {
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        *quad(j) = value(s * kBlocks + j);
+        __builtin_amdgcn_sched_barrier(0);  // one value's registers at a time
+      }
+      order();
+      const u32x4_t v0 = *moved(0), v1 = *moved(1);
+      __builtin_amdgcn_raw_buffer_store_b128(v0, rs, place(s, 0, ld, width), 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v1, rs, place(s, 1, ld, width), 0, 0);
+      order();
     }
-    order();
-    u32x4_t v[kMoves];
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) v[k] = *moved(k);
-#pragma unroll
-    for (int k = 0; k < kMoves; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], rs, place(k, ld, width), 0, 0);
-    order();
   }
   __device__ __forceinline__ void get(const void *base, int64_t row0, int64_t ld, int64_t col0, int width,
                                       raw_t (&out)[4]) const {
     const __amdgpu_buffer_rsrc_t rs = block(base, row0, ld, col0);
-    u32x4_t v[kMoves];
 #pragma unroll
-    for (int k = 0; k < kMoves; ++k)
-      v[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, place(k, ld, width), 0, 0));
+    for (int s = 0; s < kPieces; ++s) {
+      const u32x4_t v0 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, place(s, 0, ld, width), 0, 0));
+      const u32x4_t v1 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, place(s, 1, ld, width), 0, 0));
+      *moved(0) = v0;
+      *moved(1) = v1;
+      order();
 #pragma unroll
-    for (int k = 0; k < kMoves; ++k) *moved(k) = v[k];
-    order();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = *quad(j);
-    order();
+      for (int j = 0; j < kBlocks; ++j) out[s * kBlocks + j] = *quad(j);
+      order();
+    }
   }
 };
+
+constexpr int kPlacesBytes = 64 * 16;  // places of a wave's next 64 tiles
 
 struct TilePlace {
   int g, jt;
   int rows;      // of the tile, 1 .. 256
-  int64_t row0;  // the first in the packed rows
+  int64_t row0;  // the first in the packed rows; dW: of the group's
+  int from, len;  // dW: the contraction, the group's rows
 };
 
 // ACT: a run-time activation would be three copies of the epilogue, whose common values the
@@ -133,15 +136,20 @@ template <int IN, int EL, int EPI, int ACT, bool RAGGED>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
-  constexpr int kColsB = EPI == EPI_PLAIN ? 2 * kHalf : kHalf;  // output columns of a tile
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes + kTileWaves * kStoreBytes];
+  constexpr bool kTurnA = EPI == EPI_DW, kTurnB = EPI == EPI_DW || EPI == EPI_DX;
+  constexpr bool kGated = EPI == EPI_GLU || EPI == EPI_GLU_GRAD;
+  constexpr int kColsB = kGated ? kHalf : 2 * kHalf;  // output columns of a tile
+  constexpr int kStageRows = kStageB / in_bytes(IN);  // contraction values of a stage
+  using Tn = Turned<IN, kHalf>;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes + kTileWaves * (kStoreBytes + kPlacesBytes)];
 
   const WsView ws = ws_view(p.ws, p.G);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
   const int64_t *__restrict__ off = ws.off;
   const int32_t *__restrict__ pre = ws.pre[tile_rows_index(kTileRowsM)];
   const int tiles_j = (int)((p.F + kColsB - 1) / kColsB);
-  const int total = pre[p.G] * tiles_j;
+  const int tiles_i = EPI == EPI_DW ? (int)((p.N + kTileRowsM - 1) / kTileRowsM) : 0;
+  const int total = EPI == EPI_DW ? p.G * tiles_i * tiles_j : pre[p.G] * tiles_j;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -150,117 +158,201 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   const int first = (grid & 7) == 0 ? (b & 7) * (grid >> 3) + (b >> 3) : b;
   if (first >= total) return;
   const int count = (total - first + grid - 1) / grid;  // tiles of this workgroup
-  const int kb = (int)(p.K * in_bytes(IN));
-  const int nk = max(2, (kb + kStageB - 1) / kStageB);  // (two at least: loads are two stages ahead)
+  const int kb = (int)((EPI == EPI_DW ? p.N : p.K) * in_bytes(IN));  // bytes of a row of A
+  const int fb_ = (int)(p.F * in_bytes(IN));                         // of a turned B
+  // stages of a tile (two at least: loads are two stages ahead)
+  auto stages_of = [&](int len) { return max(2, EPI == EPI_DW ? (len + kStageRows - 1) / kStageRows : (kb + kStageB - 1) / kStageB); };
 
-  // ---- places of 64 tiles, one a lane
+  // ---- places of 64 tiles, found one a lane, in LDS: (group, first row, tile indices, contraction)
   int base = 0;
-  int t_g = 0, t_row0 = 0, t_jr = 0;
+  int4 *const places = (int4 *)(lds + 2 * kRingBytes + kTileWaves * kStoreBytes + wave * kPlacesBytes);
   auto fill = [&]() {
     const int w = first + min(base + lane, count - 1) * grid;
-    const int q = w / tiles_j;
-    int lo = 0, hi = p.G;  // the last g with pre[g] <= q
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= q) lo = mid;
-      else hi = mid;
+    int lo = 0, local, mt;
+    if constexpr (EPI == EPI_DW) {
+      const int per = tiles_i * tiles_j;
+      lo = w / per;
+      local = w - lo * per;
+      mt = tiles_i;
+    } else {
+      const int q = w / tiles_j;
+      int hi = p.G;  // the last g with pre[g] <= q
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= q) lo = mid;
+        else hi = mid;
+      }
+      local = w - pre[lo] * tiles_j;
+      mt = pre[lo + 1] - pre[lo];
     }
-    const int local = w - pre[lo] * tiles_j, mt = pre[lo + 1] - pre[lo];
     // bands of kOrdN column tiles, in a band blocks of kOrdM row tiles, row tiles fastest
     const int cb = local / (mt * gemm::kOrdN), bw = min(gemm::kOrdN, tiles_j - cb * gemm::kOrdN);
     const int l2 = local - cb * mt * gemm::kOrdN;
     const int rb = l2 / (gemm::kOrdM * bw), bh = min(gemm::kOrdM, mt - rb * gemm::kOrdM);
     const int l3 = l2 - rb * gemm::kOrdM * bw;
     const int it = rb * gemm::kOrdM + l3 % bh, jt = cb * gemm::kOrdN + l3 / bh;
-    const int64_t r0 = off[lo] + (int64_t)it * kTileRowsM;
-    t_g = lo;
-    t_row0 = (int)r0;
-    t_jr = (jt << 9) | (int)min64(kTileRowsM, off[lo + 1] - r0);
-    if (GL_DEVICE_CHECKS) {
-      const int rows = t_jr & 511;
-      const bool good = mt > 0 && local >= 0 && it < mt && jt < tiles_j && rows > 0 && rows <= kTileRowsM && r0 >= 0 &&
-                        r0 + rows <= p.T;
-      if (!device_check(good, p.ws)) t_g = t_row0 = t_jr = 0;  // the first row is loaded, nothing stored
+    int4 e;
+    e.x = lo;
+    bool good;
+    if constexpr (EPI == EPI_DW) {  // the group's first row; both tile indices; the group's rows
+      e.y = (int)off[lo];
+      e.z = (jt << 13) | it;
+      e.w = (int)(off[lo + 1] - off[lo]);
+      good = e.w >= 0 && e.y >= 0 && (int64_t)e.y + e.w <= p.T && it < tiles_i && jt < tiles_j;
+    } else {  // the tile's first row; its column and rows
+      const int64_t r0 = off[lo] + (int64_t)it * kTileRowsM;
+      const int rows = (int)min64(kTileRowsM, off[lo + 1] - r0);
+      e.y = (int)r0;
+      e.z = (jt << 9) | rows;
+      e.w = 0;
+      good = mt > 0 && local >= 0 && it < mt && jt < tiles_j && rows > 0 && r0 >= 0 && r0 + rows <= p.T;
     }
+    if (GL_DEVICE_CHECKS && !device_check(good, p.ws)) e = make_int4(0, 0, 0, 0);  // a first tile without rows: nothing stored
+    places[lane] = e;
+    TileStore<EL>::order();
   };
   fill();
   auto place = [&](int n) {  // of the workgroup's n-th tile
+    // (as asm: the compiler would wait for all loads to LDS that are under way)
+    i32x4_t v;
+    asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v)
+                 : "v"((uint32_t)(uintptr_t)(GL_LDS int4 *)(places + (n - base)))
+                 : "memory");
+    const int4 e = make_int4(v[0], v[1], v[2], v[3]);
     TilePlace t;
-    const int i = n - base;
-    t.g = __builtin_amdgcn_readlane(t_g, i);
-    t.row0 = __builtin_amdgcn_readlane(t_row0, i);
-    const int jr = __builtin_amdgcn_readlane(t_jr, i);
-    t.jt = jr >> 9;
-    t.rows = jr & 511;
+    t.g = __builtin_amdgcn_readfirstlane(e.x);
+    const int first_row = __builtin_amdgcn_readfirstlane(e.y), jr = __builtin_amdgcn_readfirstlane(e.z);
+    if constexpr (EPI == EPI_DW) {
+      t.from = first_row;
+      t.jt = jr >> 13;
+      t.row0 = (int64_t)(jr & 8191) * kTileRowsM;
+      t.rows = (int)min64(kTileRowsM, p.N - t.row0);
+      t.len = __builtin_amdgcn_readfirstlane(e.w);
+    } else {
+      t.from = t.len = 0;
+      t.row0 = first_row;
+      t.jt = jr >> 9;
+      t.rows = jr & 511;
+    }
     return t;
   };
 
-  // ---- loads: pieces of 8 rows, wave w has the pieces w and w + 8 of each half
+  // ---- loads: pieces of 1 KiB, wave w has the pieces w and w + 8 of each half: 8 rows by 128 bytes,
+  // of a turned operand 4 contraction rows by 256
   const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;  // place in the stage's 128 bytes
   const uint32_t voff = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)kb + (uint32_t)c16;
+  const int trow = 4 * wave + (lane >> 4), tc16 = Tn::slot(trow, lane & 15) * 16;  // rows 32 apart: the same slots
+  const uint32_t tva = (uint32_t)(trow * kb + tc16), tvb = (uint32_t)(trow * fb_ + tc16);
   __amdgpu_buffer_rsrc_t ra, rb0, rb1;
-  int load_tile = 0, load_stage = 0;  // what the next four phases ask for
-  auto rsrc = [&](const char *at, int64_t rows) {
-    const uint64_t v = (uint64_t)(uintptr_t)at;  // the same in every lane; made visibly so
-    const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-    const uint32_t h = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)(((uint64_t)h << 32) | l), (short)0,
-                                             (int)rows * kb, 0x00020000);
+  const char *ta = nullptr, *tb = nullptr;  // turned operands: the tile's first column of the stage's first row
+  int wide_a = 0, wide_b = 0;               // and bytes of columns
+  int load_tile = 0, load_stage = 0, load_nk = 2, load_len = 0;  // what the next four phases ask for
+  auto rsrc = [&](const char *at, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)gemm::uniform_ptr(at), (short)0, bytes, 0x00020000);
   };
   auto aim = [&]() {  // the streams of tile load_tile
     if (load_tile >= count) return;
+    asm volatile("" ::: "memory");  // the place is read here alone, not ahead of the test in every stage
     const TilePlace t = place(load_tile);
-    const char *wg = group_weights<IN, EPI>(p, t.g);
     const int64_t col0 = (int64_t)t.jt * kColsB, left = p.F - col0;
-    ra = rsrc(p.x + t.row0 * kb, GL_DEVICE_CHECKS ? max(t.rows, 1) : t.rows);
-    rb0 = rsrc(wg + col0 * kb, min64(kHalf, left));
+    load_nk = stages_of(t.len);
+    if constexpr (EPI == EPI_DW) {
+      load_len = t.len;
+      ta = p.x + (int64_t)t.from * kb + t.row0 * in_bytes(IN);
+      wide_a = t.rows * in_bytes(IN);
+      tb = p.w + (int64_t)t.from * fb_ + col0 * in_bytes(IN);
+      wide_b = (int)min64(2 * kHalf, left) * in_bytes(IN);
+      return;
+    }
+    const char *wg = group_weights<IN, EPI>(p, t.g);
+    ra = rsrc(p.x + t.row0 * kb, (GL_DEVICE_CHECKS ? max(t.rows, 1) : t.rows) * kb);
+    if constexpr (EPI == EPI_DX) {
+      load_len = (int)p.K;
+      tb = wg + col0 * in_bytes(IN);
+      wide_b = (int)min64(2 * kHalf, left) * in_bytes(IN);
+      return;
+    }
+    rb0 = rsrc(wg + col0 * kb, (int)min64(kHalf, left) * kb);
     if (EPI == EPI_PLAIN)
-      rb1 = left > kHalf ? rsrc(wg + (col0 + kHalf) * kb, min64(kHalf, left - kHalf)) : rsrc(wg + col0 * kb, 1);
+      rb1 = left > kHalf ? rsrc(wg + (col0 + kHalf) * kb, (int)min64(kHalf, left - kHalf) * kb) : rsrc(wg + col0 * kb, kb);
     else
-      rb1 = rsrc(wg + (p.F + col0) * kb, min64(kHalf, left));
+      rb1 = rsrc(wg + (p.F + col0) * kb, (int)min64(kHalf, left) * kb);
   };
   // half 0 A0, 1 A1, 2 B0, 3 B1 of stage load_stage into ring slot `ring`
-  auto issue = [&](int half, int ring) {
-    const int at = load_stage * kStageB;
-    const int lim = load_tile < count ? kb - at : 0;  // bytes of the row left
-    const __amdgpu_buffer_rsrc_t r = half < 2 ? ra : half == 2 ? rb0 : rb1;
+  auto issue = [&](auto half_tag, int ring) __attribute__((always_inline)) {
+    constexpr int half = decltype(half_tag)::value;
+    char *to = lds + ring * kRingBytes + half * kHalfBytes + wave * 1024;
+    if constexpr (half < 2 ? kTurnA : kTurnB) {
+      const int ld = half < 2 ? kb : fb_, wide = half < 2 ? wide_a : wide_b;
+      const int left = __builtin_amdgcn_readfirstlane(  // rows of the stage
+          load_tile < count ? min(kStageRows, load_len - load_stage * kStageRows) : 0);
+      const __amdgpu_buffer_rsrc_t r = rsrc(half < 2 ? ta : tb, max(left, 0) * ld);
+      constexpr int c = (half & 1) * (kHalf * in_bytes(IN));  // the half's first column
+      const uint32_t v = half < 2 ? tva : tvb;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t o = voff + (uint32_t)(((half == 1) * kHalf + q * 64) * kb);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (GL_LDS void *)(lds + ring * kRingBytes + half * kHalfBytes + (wave + 8 * q) * 1024), 16,
-          c16 < lim ? o : kOutside, lim > 0 ? at : 0, 0, 0);
+      for (int q = 0; q < 2; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GL_LDS void *)(to + q * 8192), 16,
+                                                 tc16 + c < wide ? v + (uint32_t)(32 * q * ld + c) : kOutside, 0, 0, 0);
+    } else {
+      const int at = load_stage * kStageB;
+      const int lim = load_tile < count ? kb - at : 0;  // bytes of the row left
+      const __amdgpu_buffer_rsrc_t r = half < 2 ? ra : half == 2 ? rb0 : rb1;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t o = voff + (uint32_t)(((half == 1) * kHalf + q * 64) * kb);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GL_LDS void *)(to + q * 8192), 16, c16 < lim ? o : kOutside,
+                                                 lim > 0 ? at : 0, 0, 0);
+      }
     }
   };
   auto next_stage = [&]() {
-    if (++load_stage == nk) {
+    if (kTurnA) ta += (int64_t)kStageRows * kb;
+    if (kTurnB) tb += (int64_t)kStageRows * fb_;
+    if (++load_stage == load_nk) {
       load_stage = 0;
       ++load_tile;
       aim();
     }
   };
 
-  // ---- fragments: 16 bytes of row l % 16 of a block, of the stage's half s
+  // ---- fragments: 16 bytes of row l % 16 of a block, of the stage's half s (turned: of column l % 16)
   const int fr = lane & 15, fq = lane >> 4;
-  auto frag = [&](int half, int row, int ring, int s) {
-    const int r = row + fr;
-    return *(const i32x4_t *)(lds + ring * kRingBytes + half * kHalfBytes + r * kStageB +
-                              (((4 * s + fq) ^ ((r >> 1) & 7)) << 4));
+  // places of the first block of A and of B in a half: the others and the other half of the stage are
+  // an offset or a bit away
+  const uint32_t at_a = kTurnA ? Tn::place(wm * 16, lane) : (wm * 16 + fr) * kStageB + ((fq ^ (fr >> 1)) & 7) * 16;
+  const uint32_t at_b = kTurnB ? Tn::place(wn * 64, lane) : (wn * 64 + fr) * kStageB + ((fq ^ (fr >> 1)) & 7) * 16;
+  auto opaque = [](uint32_t v) {
+    if (kTurnB) asm volatile("" : "+v"(v));  // found at each read (kept, they are the registers that spill)
+    return v;
   };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(GL_LDS char *)lds;
   i32x4_t fa[2][2], fb[2][4][2];  // [block][half of the stage]; two sets of B
   int blocks = 4;  // row blocks of the wave that hold rows: (A half, i) in turn are 64 rows apart
   auto read_a = [&](int half, int ring) {
+    const uint32_t o = opaque(at_a + ring * kRingBytes + half * kHalfBytes);
+    if constexpr (kTurnA) {
+      const uint32_t at[2] = {lds0 + o, lds0 + (o ^ 128)};
+      read_turned<256>(at, fa);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (!RAGGED || 2 * half + i < blocks)
+      for (int i = 0; i < 2; ++i)
+        if (!RAGGED || 2 * half + i < blocks)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) fa[i][s] = frag(half, i * 64 + wm * 16, ring, s);
+          for (int s = 0; s < 2; ++s) fa[i][s] = *(const i32x4_t *)(lds + (o ^ (64 * s)) + i * 64 * kStageB);
+    }
   };
   auto read_b = [&](int set, int half, int ring) {
+    const uint32_t o = opaque(at_b + ring * kRingBytes + half * kHalfBytes);
+    if constexpr (kTurnB) {
+      const uint32_t at[4] = {lds0 + o, lds0 + (o ^ 32), lds0 + (o ^ 64), lds0 + (o ^ 96)};
+      read_turned<256>(at, fb[set]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) fb[set][j][s] = frag(half, wn * 64 + j * 16, ring, s);
+        for (int s = 0; s < 2; ++s) fb[set][j][s] = *(const i32x4_t *)(lds + (o ^ (64 * s)) + j * 16 * kStageB);
+    }
   };
   acc_t acc[2][2][2][4];  // [A half][B half][row block][column block]
   auto zero = [&]() {
@@ -297,25 +389,24 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   // other set after it.
   auto stage = [&](auto set_tag, int ring) __attribute__((always_inline)) {
     constexpr int S = decltype(set_tag)::value;
-    read_a(0, ring);
-    issue(2, ring);
-    read_done();
+    // (a turned operand's reads wait for themselves: the phase's loads go out before them)
+    auto phase = [&](auto load_tag, bool last, auto read, bool turned) __attribute__((always_inline)) {
+      if (!turned) read();
+      issue(load_tag, ring);
+      if (last) next_stage();
+      if (turned) read();
+      read_done();
+    };
+    phase(std::integral_constant<int, 2>{}, false, [&] { read_a(0, ring); }, kTurnA);
     multiply(S, 0, acc[0][0]);
     barrier();
-    read_b(1 - S, 3, ring);
-    issue(0, ring);
-    read_done();
+    phase(std::integral_constant<int, 0>{}, false, [&] { read_b(1 - S, 3, ring); }, kTurnB);
     multiply(1 - S, 0, acc[0][1]);
     barrier();
-    read_a(1, ring);
-    issue(3, ring);
-    read_done();
+    phase(std::integral_constant<int, 3>{}, false, [&] { read_a(1, ring); }, kTurnA);
     multiply(1 - S, 1, acc[1][1]);
     barrier();
-    read_b(1 - S, 2, ring ^ 1);
-    issue(1, ring);
-    next_stage();
-    read_done();
+    phase(std::integral_constant<int, 1>{}, true, [&] { read_b(1 - S, 2, ring ^ 1); }, kTurnB);
     multiply(S, 1, acc[1][0]);
     barrier();
   };
@@ -324,10 +415,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   aim();
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    issue(2, s);
-    issue(0, s);
-    issue(3, s);
-    issue(1, s);
+    issue(std::integral_constant<int, 2>{}, s);
+    issue(std::integral_constant<int, 0>{}, s);
+    issue(std::integral_constant<int, 3>{}, s);
+    issue(std::integral_constant<int, 1>{}, s);
     next_stage();
   }
   fence();
@@ -339,6 +430,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     zero();
     const TilePlace t = place(n);
     blocks = (t.rows - wm * 16 + 63) / 64;
+    const int nk = stages_of(t.len);
     // B0 of the first stage (again: the last tile's last stage read it, but held through the
     // epilogue it would cost 32 registers), by all waves before the first loads may replace it
     read_b(0, 2, ring);
@@ -363,32 +455,53 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     const int er = le & 15, eq = le >> 4;
     const int64_t col0 = (int64_t)t.jt * kColsB;
     const int width = (int)min64(kHalf, p.F - col0);  // columns of the first set
-    const int width1 = EPI == EPI_PLAIN ? (int)min64(kHalf, p.F - col0 - kHalf) : width;
-    const int64_t second = EPI == EPI_PLAIN ? col0 + kHalf : p.F + col0;  // the second set's first column
+    const int width1 = kGated ? width : (int)min64(kHalf, p.F - col0 - kHalf);
+    const int64_t second = kGated ? p.F + col0 : col0 + kHalf;  // the second set's first column
     ColumnTerms<IN, EL> ct[2][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = wn * 64 + j * 16 + eq * 4;  // a lane past the last column takes the last four, and is not stored
-      ct[0][j] = column_terms<IN, EL, EPI>(p, t.g, col0 + min(c, width - 4));
-      ct[1][j] = column_terms<IN, EL, EPI>(p, t.g, width1 > 0 ? second + min(c, width1 - 4) : col0);
-    }
     float rs[2][2];
+    if constexpr (!kTurnB) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+      for (int j = 0; j < 4; ++j) {
+        const int c = wn * 64 + j * 16 + eq * 4;  // a lane past the last column takes the last four, and is not stored
+        ct[0][j] = column_terms<IN, EL, EPI>(p, t.g, col0 + min(c, width - 4));
+        ct[1][j] = column_terms<IN, EL, EPI>(p, t.g, width1 > 0 ? second + min(c, width1 - 4) : col0);
+      }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, t.rows - 1)] : 0.f;
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, t.rows - 1)] : 0.f;
+    }
+    // dW is the group's own matrix; with accumulate, a group without rows is not touched
+    void *const out = EPI == EPI_DW ? p.out ? (char *)p.out + (int64_t)t.g * p.N * p.F * elem_bytes(EL) : p.out_ptrs[t.g] : p.out;
+    const bool untouched = EPI == EPI_DW && p.accumulate && t.len == 0;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         typedef Quad<EL> Q;
         const TileStore<EL> st{lds + 2 * kRingBytes + wave * kStoreBytes, le, a * kHalf + i * 64 + wm * 16, t.rows, wn * 64};
-        if (2 * a + i >= blocks) continue;
+        if (2 * a + i >= blocks || untouched) continue;
         auto value = [&](int b, int j) { return finish<IN, EL>(acc[a][b][i][j], rs[a][i], ct[b][j]); };
         auto gate = [&](int j) { return Q::pack(value(0, j)); };
         auto other = [&](int j) { return Q::pack(value(1, j)); };
-        if constexpr (EPI == EPI_PLAIN) {
+        if constexpr (kTurnB) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (b == 1 && width1 <= 0) break;
+            typename Q::raw old[4];
+            if (EPI == EPI_DW && p.accumulate) st.get(out, t.row0, p.F, b ? second : col0, b ? width1 : width, old);
+            st.put(out, t.row0, p.F, b ? second : col0, b ? width1 : width, [&](int j) {
+              const acc_t v = acc[a][b][i][j];
+              float4 o = make_float4(v[0], v[1], v[2], v[3]);
+              if (EPI == EPI_DW && p.accumulate) {
+                const float4 m = Q::value(old[j]);
+                o = make_float4(o.x + m.x, o.y + m.y, o.z + m.z, o.w + m.w);
+              }
+              return Q::pack(o);
+            });
+          }
+        } else if constexpr (EPI == EPI_PLAIN) {
           st.put(p.out, t.row0, p.F, col0, width, gate);
           if (width1 > 0) st.put(p.out, t.row0, p.F, second, width1, other);
         } else if constexpr (EPI == EPI_GLU) {
@@ -425,10 +538,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
 template <int IN, int EL, int EPI, int ACT>
 inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, bool ragged, hipStream_t s) {
   const dim3 grid(gemm::persistent_grid(items)), block(kTileThreads);
-  if (ragged)
-    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, false>), grid, block, 0, s, p);
+  if constexpr (EPI != EPI_DW) {
+    if (ragged) {
+      hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, true>), grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

@@ -114,12 +114,14 @@ def test_every_split_of_the_rows_gives_the_same_rows():
         check(a, *glu_limits("silu", ref_h, e, BF), str(m))
 
 
-# products of the backward: (rows of the groups, K, F) by the tile of dx / of dW that they take
+# products of the backward: (rows of the groups, K, F) by the tiles that dx and dW take
 BACK = {
     "64": ([5, 0, 70, 20], 264, 72),
-    "128": ([130, 0, 400, 257, 300], 2056, 520),       # dx 192 tiles of 128, dW more
-    "dw256": ([3, 0, 129, 0, 66, 1], 2312, 2312),      # dW over 1024 tiles of 256
-    "dx256": ([300, 2, 513], 8200, 40),                # dx 165 tiles of 256
+    "128": ([130, 0, 400, 257, 300], 1032, 520),        # dx by 128 (144 tiles of 256 rows); dW by 256
+    "dw128": ([700], 1544, 1032),                      # dW by 128 (63 tiles of 256)
+    "dw256": ([3, 0, 129, 0, 66, 1], 2312, 2312),      # dW over 1000 tiles of 256
+    "dx256": ([300, 2, 513], 8200, 40),                # dx 231 tiles of 256, whole
+    "dx256_skip": ([3, 0, 20, 1] * 8, 1544, 72),       # and of few rows
 }
 
 
