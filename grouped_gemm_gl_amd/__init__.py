@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Union
 
@@ -741,48 +742,79 @@ def gl_moe_few_tokens(x: Tensor, ids: Tensor, weights: Tensor, w1: Grouped, w2: 
 
 
 # ------------------------------------------------- gated layer, 8-bit integers
+#
+# (These are called for single tokens too, where the checks below are most of a call: a stacked tensor
+# is looked at once, and nothing is sliced.)
 
 
-def _on_current_device(x: Tensor) -> None:
-    """The launch goes to the current device, so its tensors have to be there."""
-    if x.is_cuda and x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {x.device}, which is not the current device")
+def _here(t: Tensor) -> int:
+    """The GPU that ``t`` is on, which has to be the current one: the launch goes there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {t.device}, which is not the current device")
+    return dev
 
 
-def _grouped_on(x: Tensor, stream, **groups):
-    """Stacked address and pointer array of each stacked tensor or list, all on x's device,
-    contiguous, each 16-byte aligned (scales: 4), and what to keep alive until the call is made."""
-    at, keep = [], []
-    for what, g in groups.items():
-        if g is None:
-            at += [None, None]
-            continue
-        align = 4 if what.endswith("scale") else 16
-        each = _addresses(x, *((g,) if isinstance(g, Tensor) else g))[1:]
-        if any(a % align for a in each):
-            raise ValueError(f"{what} must be {align}-byte aligned (each group's)")
-        if isinstance(g, Tensor):
-            at += [each[0], None]
-        else:
-            ptrs = torch.tensor(each, dtype=torch.int64, device=x.device)
-            _record([ptrs], stream)
-            at += [None, ptrs.data_ptr()]
-            keep.append((ptrs, list(g)))
-    return at, keep
+def _at(dev: int, t: Optional[Tensor]) -> Optional[int]:
+    """Address of a contiguous tensor on GPU ``dev``, None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"tensors must be on one device (cuda:{dev} and {t.device})")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    return t.data_ptr()
 
 
-def _glu_sizes(x: Tensor, w: Grouped, gated: bool):
-    """(G, K, N, F) of x [T, K] and the weights, which all have one shape and x's type."""
-    _on_current_device(x)
-    w0 = _first(w)
-    if x.dim() != 2 or w0.dim() != 2 or (isinstance(w, Tensor) and w.dim() != 3):
+def _group_at(dev: int, g: Optional[Grouped], shape, dtype, what: str, stream, keep: list):
+    """(address, pointer array) of a stacked tensor of ``shape`` or a list of shape[0] tensors of
+    shape[1:], 16-byte aligned each (scales: 4); the pointer array goes into ``keep``."""
+    if g is None:
+        return None, None
+    if isinstance(g, Tensor):
+        if g.shape != shape or g.dtype != dtype:
+            raise ValueError(f"{what} must be {list(shape)} or {shape[0]} tensors {list(shape[1:])}, of {dtype}")
+        return _at(dev, g), None
+    if len(g) != shape[0] or any(t.shape != shape[1:] or t.dtype != dtype for t in g):
+        raise ValueError(f"{what} must be {list(shape)} or {shape[0]} tensors {list(shape[1:])}, of {dtype}")
+    each = [_at(dev, t) for t in g]
+    align = 4 if what == "w_scale" else 16
+    if any(a % align for a in each):  # the library sees only their array
+        raise ValueError(f"every group's {what} must be {align}-byte aligned")
+    ptrs = torch.tensor(each, dtype=torch.int64, device=f"cuda:{dev}")
+    _record([ptrs], stream)
+    keep.append((ptrs, list(g)))
+    return None, ptrs.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(num_groups: int) -> int:
+    return gl_workspace_size(num_groups)
+
+
+def _glu_sizes(x: Tensor, w: Grouped, workspace: Tensor, gated: bool):
+    """(T, G, K, N, F) of x [T, K] and w [G, N, K] or G tensors [N, K]."""
+    ws = w.shape if isinstance(w, Tensor) else (len(w), *(w[0].shape if len(w) else ()))
+    if x.dim() != 2 or len(ws) != 3:
         raise ValueError("x must be [T, K] and w [G, N, K] or G tensors [N, K]")
-    G = w.shape[0] if isinstance(w, Tensor) else len(w)
-    N, K = w0.shape[-2:]
-    if x.shape[1] != K or (gated and N % 2):
+    G, N, K = ws
+    T, k = x.shape
+    if k != K or (gated and N % 2):
         raise ValueError(f"x must be [T, {K}], and w have an even number of rows where they are gated")
-    _each_shape(w, G, (N, K), x.dtype, "w")
-    return G, K, N, N // 2 if gated else N
+    if workspace.numel() * workspace.element_size() < _workspace_bytes(G):
+        raise ValueError(f"workspace must hold {_workspace_bytes(G)} bytes")
+    return T, G, K, N, N // 2 if gated else N
+
+
+def _matrix(t: Optional[Tensor], rows: int, cols: int, dtype, what: str, more: bool = False) -> None:
+    """Checks a tensor [rows, cols] (``more``: or of more rows), None passes."""
+    if t is None:
+        return
+    s = t.shape
+    if len(s) != 2 or s[1] != cols or (s[0] < rows if more else s[0] != rows) or t.dtype != dtype:
+        raise ValueError(f"{what} must be [{'rows >= ' if more else ''}{rows}, {cols}] of {dtype}")
 
 
 def gl_glu_forward(x: Tensor, w: Grouped, a: Tensor, workspace: Tensor, *, bias: Optional[Grouped] = None,
@@ -792,18 +824,15 @@ def gl_glu_forward(x: Tensor, w: Grouped, a: Tensor, workspace: Tensor, *, bias:
     x: [T, K]; w: [G, 2F, K] or G tensors [2F, K], the gate's rows first; bias [G, 2F] or G
     tensors [2F]; a: [>= T, F], rows past T are left untouched; h: [T, 2F] to keep for
     ``gl_glu_backward``, or None.  One dtype (float32, bfloat16, float16)."""
-    G, K, N, F = _glu_sizes(x, w, True)
-    T = x.shape[0]
-    if a.dim() != 2 or a.shape[1] != F or a.dtype != x.dtype:
-        raise ValueError(f"a must be [rows >= {T}, {F}] of x's dtype")
-    if h is not None and (h.shape != (T, N) or h.dtype != x.dtype):
-        raise ValueError(f"h must be [{T}, {N}] of x's dtype")
-    _each_shape(bias, G, (N,), x.dtype, "bias")
-    px, ph, pa, ws = _addresses(x, h, a, workspace)
-    _enough(workspace, gl_workspace_size(G))
-    (pw, pww, pb, pbb), keep = _grouped_on(x, stream, w=w, bias=bias)
-    _check(load().gl_glu_forward(G, K, F, T, _dtype(x), int(act), px, pw, pww, pb, pbb, ph, pa, a.shape[0], ws,
-                                 _stream(stream)))
+    T, G, K, N, F = _glu_sizes(x, w, workspace, True)
+    dt = x.dtype
+    _matrix(a, T, F, dt, "a", more=True)
+    _matrix(h, T, N, dt, "h")
+    dev, keep = _here(x), []
+    pw, pww = _group_at(dev, w, (G, N, K), dt, "w", stream, keep)
+    pb, pbb = _group_at(dev, bias, (G, N), dt, "bias", stream, keep)
+    _check(load().gl_glu_forward(G, K, F, T, _dtype(x), int(act), _at(dev, x), pw, pww, pb, pbb, _at(dev, h), _at(dev, a),
+                                 a.shape[0], _at(dev, workspace), _stream(stream)))
     del keep
     return a
 
@@ -816,23 +845,24 @@ def gl_glu_backward(x: Tensor, w: Grouped, da: Tensor, dh: Tensor, dx: Optional[
     h, a caller's buffer; may be h), dx[:T] (or None), dw (of x's dtype or float32, added into
     with ``accumulate``) and db (of x's dtype).  ``h`` as the forward kept it, or None: computed
     again from x, w and ``bias``.  ``a`` [T, F] receives the forward's output again."""
-    G, K, N, F = _glu_sizes(x, w, True)
-    T = x.shape[0]
-    for t, shape, what in ((da, (T, F), "da"), (dh, (T, N), "dh"), (h, (T, N), "h"), (a, (T, F), "a")):
-        if t is not None and (t.shape != shape or t.dtype != x.dtype):
-            raise ValueError(f"{what} must be [{shape[0]}, {shape[1]}] of x's dtype")
-    if dx is not None and (dx.dim() != 2 or dx.shape[1] != K or dx.dtype != x.dtype):
-        raise ValueError(f"dx must be [rows >= {T}, {K}] of x's dtype")
-    wd = _first(dw).dtype
-    _each_shape(dw, G, (N, K), wd, "dw")
-    _each_shape(bias, G, (N,), x.dtype, "bias")
-    _each_shape(db, G, (N,), x.dtype, "db")
-    px, ph, pda, pdh, pa, pdx, ws = _addresses(x, h, da, dh, a, dx, workspace)
-    _enough(workspace, gl_workspace_size(G))
-    (pw, pww, pb, pbb, pdw, pdww, pdb, pdbb), keep = _grouped_on(x, stream, w=w, bias=bias, dw=dw, db=db)
-    _check(load().gl_glu_backward(G, K, F, T, _dtype(x), _dtype(_first(dw)), int(act), px, pw, pww, pb, pbb, ph, pda,
-                                  pdh, pa, pdx, 0 if dx is None else dx.shape[0], pdw, pdww, pdb, pdbb,
-                                  int(bool(accumulate)), ws, _stream(stream)))
+    T, G, K, N, F = _glu_sizes(x, w, workspace, True)
+    dt = x.dtype
+    _matrix(da, T, F, dt, "da")
+    _matrix(dh, T, N, dt, "dh")
+    _matrix(h, T, N, dt, "h")
+    _matrix(a, T, F, dt, "a")
+    _matrix(dx, T, K, dt, "dx", more=True)
+    wd = (dw if isinstance(dw, Tensor) else dw[0]).dtype
+    if wd not in _DT:
+        raise ValueError(f"unsupported dtype {wd}")
+    dev, keep = _here(x), []
+    pw, pww = _group_at(dev, w, (G, N, K), dt, "w", stream, keep)
+    pb, pbb = _group_at(dev, bias, (G, N), dt, "bias", stream, keep)
+    pdw, pdww = _group_at(dev, dw, (G, N, K), wd, "dw", stream, keep)
+    pdb, pdbb = _group_at(dev, db, (G, N), dt, "db", stream, keep)
+    _check(load().gl_glu_backward(G, K, F, T, _dtype(x), _DT[wd], int(act), _at(dev, x), pw, pww, pb, pbb, _at(dev, h),
+                                  _at(dev, da), _at(dev, dh), _at(dev, a), _at(dev, dx), 0 if dx is None else dx.shape[0],
+                                  pdw, pdww, pdb, pdbb, int(bool(accumulate)), _at(dev, workspace), _stream(stream)))
     del keep
     return dx
 
@@ -840,33 +870,30 @@ def gl_glu_backward(x: Tensor, w: Grouped, da: Tensor, dh: Tensor, dx: Optional[
 def gl_quantize_int8(src: Tensor, data: Tensor, scale: Tensor, stream=None):
     """Rows of src [..., cols] as int8 codes data (src's shape) and float32 scale [...]: a
     token's activations, or with weights [G, N, K] a channel's."""
-    _on_current_device(src)
-    if src.dim() < 1 or data.shape != src.shape or data.dtype != torch.int8:
+    s = src.shape
+    if len(s) < 1 or data.shape != s or data.dtype != torch.int8:
         raise ValueError("data must be int8 of src's shape")
-    if scale.shape != src.shape[:-1] or scale.dtype != torch.float32:
+    if scale.shape != s[:-1] or scale.dtype != torch.float32:
         raise ValueError("scale must be float32 with one value for each row of src")
-    cols = src.shape[-1]
-    at = _addresses(src, data, scale)
-    _check(load().gl_quantize_int8(src.numel() // cols if cols else 0, cols, _dtype(src), *at, _stream(stream)))
+    cols, dev = s[-1], _here(src)
+    _check(load().gl_quantize_int8(src.numel() // cols if cols else 0, cols, _dtype(src), _at(dev, src), _at(dev, data),
+                                   _at(dev, scale), _stream(stream)))
     return data, scale
 
 
 def _int8(name: str, gated: bool, x, x_scale, w, w_scale, y, workspace, bias, act, stream) -> Tensor:
-    G, K, N, F = _glu_sizes(x, w, gated)
-    T = x.shape[0]
+    T, G, K, N, F = _glu_sizes(x, w, workspace, gated)
     if x.dtype != torch.int8 or x_scale.shape != (T,) or x_scale.dtype != torch.float32:
         raise ValueError("x must be int8 [T, K] and x_scale float32 [T]")
-    if y.dim() != 2 or y.shape[1] != F:
-        raise ValueError(f"the output must be [rows >= {T}, {F}]")
     if isinstance(w, Tensor) != isinstance(w_scale, Tensor):
         raise ValueError("w and w_scale must both be stacked or both be lists")
-    _each_shape(w_scale, G, (N,), torch.float32, "w_scale")
-    _each_shape(bias, G, (N,), y.dtype, "bias")
-    px, ps, py, ws = _addresses(x, x_scale, y, workspace)
-    _enough(workspace, gl_workspace_size(G))
-    (pw, pww, pc, pcc, pb, pbb), keep = _grouped_on(x, stream, w=w, w_scale=w_scale, bias=bias)
-    _check(getattr(load(), name)(G, K, F, T, _dtype(y), *((int(act),) if gated else ()), px, ps, pw, pww, pc, pcc, pb,
-                                 pbb, py, y.shape[0], ws, _stream(stream)))
+    _matrix(y, T, F, y.dtype, "the output", more=True)
+    dev, keep = _here(x), []
+    pw, pww = _group_at(dev, w, (G, N, K), torch.int8, "w", stream, keep)
+    pc, pcc = _group_at(dev, w_scale, (G, N), torch.float32, "w_scale", stream, keep)
+    pb, pbb = _group_at(dev, bias, (G, N), y.dtype, "bias", stream, keep)
+    _check(getattr(load(), name)(G, K, F, T, _dtype(y), *((int(act),) if gated else ()), _at(dev, x), _at(dev, x_scale), pw,
+                                 pww, pc, pcc, pb, pbb, _at(dev, y), y.shape[0], _at(dev, workspace), _stream(stream)))
     del keep
     return y
 

@@ -13,6 +13,7 @@
 
 #include <type_traits>
 
+#include "gl_gemm_tile.hpp"
 #include "gl_vec.hpp"
 
 namespace gl {
@@ -129,6 +130,41 @@ struct BackParams {
   const void *ws;
   int G, accumulate;
   int64_t T, K, N;  // N = 2F
+};
+
+// The row tiles of a launch and their groups.  Below 64 groups the wave's lanes hold the whole tables
+// (lane i: group i), so that a workgroup's first loads wait for one round trip to memory where the
+// tables one after the other take four.
+struct RowTiles {
+  const int64_t *__restrict__ off;
+  const int32_t *__restrict__ pre;
+  int G, pre_l = 0;
+  int64_t off_l = 0;
+  bool held;
+  __device__ __forceinline__ RowTiles(const WsView &ws, int G, int rows)
+      : off(ws.off), pre(ws.pre[tile_rows_index(rows)]), G(G), held(G < 64) {
+    if (held) {
+      const int i = min((int)(threadIdx.x & 63), G);
+      pre_l = pre[i];
+      off_l = off[i];
+    }
+  }
+  // (read back as uniform: a buffer resource's length from them is otherwise taken as the lanes' own,
+  // and every load goes through a loop over its values)
+  __device__ __forceinline__ int tile(int g) const {
+    return held ? __builtin_amdgcn_readlane(pre_l, g) : __builtin_amdgcn_readfirstlane(pre[g]);
+  }
+  __device__ __forceinline__ int64_t row(int g) const {
+    if (!held) return (int64_t)(uintptr_t)gemm::uniform_ptr((const char *)(uintptr_t)off[g]);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)off_l, g);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)off_l >> 32), g);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+  }
+  // the group of row tile q (the last whose first tile is not after q)
+  __device__ __forceinline__ int group(int q) const {
+    if (!held) return __builtin_amdgcn_readfirstlane(find_group(pre, G, q));
+    return __popcll(__ballot((int)(threadIdx.x & 63) <= G && pre_l <= q)) - 1;
+  }
 };
 
 template <int IN, int EPI>

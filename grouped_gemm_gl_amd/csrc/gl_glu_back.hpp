@@ -28,11 +28,10 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
   __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
 
   const WsView ws = ws_view(p.ws, p.G);
+  const RowTiles tiles(ws, p.G, TILE);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
-  const int64_t *__restrict__ off = ws.off;
-  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(TILE)];
   const int tiles_i = (int)((p.N + TILE - 1) / TILE), tiles_j = (int)((p.K + TILE - 1) / TILE);
-  const int64_t total = WGRAD ? (int64_t)p.G * tiles_i * tiles_j : (int64_t)pre[p.G] * tiles_j;
+  const int64_t total = WGRAD ? (int64_t)p.G * tiles_i * tiles_j : (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -50,11 +49,11 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
     } else {
       const int qt = (int)(w / tiles_j);
       jt = (int)(w - (int64_t)qt * tiles_j);
-      g = find_group(pre, p.G, qt);
+      g = tiles.group(qt);
       if (!device_check(g >= 0 && g < p.G, p.ws)) continue;
-      it = qt - pre[g];
+      it = qt - tiles.tile(g);
     }
-    const int64_t g_off = off[g], g_rows = off[g + 1] - g_off;
+    const int64_t g_off = tiles.row(g), g_rows = tiles.row(g + 1) - g_off;
     if (WGRAD && p.accumulate && g_rows == 0) continue;  // not touched
     const int64_t i0 = (int64_t)it * TILE, j0 = (int64_t)jt * TILE;
     const int64_t contr = WGRAD ? g_rows : p.N;  // values of the contraction

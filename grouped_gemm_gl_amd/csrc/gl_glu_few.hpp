@@ -50,11 +50,10 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
   constexpr int kCols = EPI == EPI_PLAIN ? 32 : 16;
   __shared__ acc_t part[kFewWaves][2][64];
   const WsView ws = ws_view(p.ws, p.G);
+  const RowTiles tiles(ws, p.G, 32);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
-  const int64_t *__restrict__ off = ws.off;
-  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(32)];
   const int tiles_j = (int)((p.F + kCols - 1) / kCols);
-  const int64_t total = (int64_t)pre[p.G] * tiles_j;
+  const int64_t total = (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const uint32_t kb = (uint32_t)(p.K * in_bytes(IN));  // bytes of a row of either operand
@@ -62,11 +61,11 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int qt = (int)(w / tiles_j), jt = (int)(w - (int64_t)qt * tiles_j);
-    const int g = find_group(pre, p.G, qt);
+    const int g = tiles.group(qt);
     if (!device_check(g >= 0 && g < p.G, p.ws)) continue;
-    const int64_t row0 = off[g];
-    const int rows = (int)min64(16, off[g + 1] - row0);
-    if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T && qt == pre[g], p.ws)) continue;
+    const int64_t row0 = tiles.row(g);
+    const int rows = (int)min64(16, tiles.row(g + 1) - row0);
+    if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T && qt == tiles.tile(g), p.ws)) continue;
     const int64_t col0 = (int64_t)jt * kCols;
     // weight rows of the first 16 columns and of the second: the other half, or the next 16
     const char *wg = group_weights<IN, EPI>(p, g);

@@ -114,11 +114,10 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
   __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
 
   const WsView ws = ws_view(p.ws, p.G);
+  const RowTiles tiles(ws, p.G, ROWS);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
-  const int64_t *__restrict__ off = ws.off;
-  const int32_t *__restrict__ pre = ws.pre[tile_rows_index(ROWS)];
   const int tiles_j = (int)((p.F + kCols - 1) / kCols);
-  const int64_t total = (int64_t)pre[p.G] * tiles_j;
+  const int64_t total = (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -131,10 +130,10 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int qt = (int)(w / tiles_j), jt = (int)(w - (int64_t)qt * tiles_j);
-    const int g = find_group(pre, p.G, qt);
+    const int g = tiles.group(qt);
     if (!device_check(g >= 0 && g < p.G, p.ws)) continue;
-    const int64_t row0 = off[g] + (int64_t)(qt - pre[g]) * ROWS;
-    const int rows = (int)min64(ROWS, off[g + 1] - row0);
+    const int64_t row0 = tiles.row(g) + (int64_t)(qt - tiles.tile(g)) * ROWS;
+    const int rows = (int)min64(ROWS, tiles.row(g + 1) - row0);
     if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T, p.ws)) continue;
     const int64_t col0 = (int64_t)jt * kCols, left = p.F - col0;
     const int64_t second = EPI == EPI_PLAIN ? col0 + M::kColsHalf : p.F + col0;

@@ -117,7 +117,7 @@ __device__ __forceinline__ void offsets_block(const int64_t *__restrict__ m_spli
 // totals broadcast from lane 63): for the fused offsets + quantize launch, whose
 // other workgroups then need no LDS either.  Called by the 64 lanes of one wave.
 __device__ __forceinline__ void offsets_wave(const int64_t *__restrict__ m_splits, int G, int64_t total_rows,
-                                             void *ws) {
+                                             void *ws, int split_slots = kSplitSlots) {
   WsView v = ws_view(ws, G);
   int64_t *off = const_cast<int64_t *>(v.off);
   int32_t *pre[kNumTileRows];
@@ -159,7 +159,7 @@ __device__ __forceinline__ void offsets_wave(const int64_t *__restrict__ m_split
     h->num_groups = G;
     h->total_rows = total_rows;
     h->magic = kWsMagic;
-    h->split_slots = kSplitSlots;
+    h->split_slots = split_slots;
     h->status = (any_bad ? 1 : 0) | (carry != total_rows ? 2 : 0);
   }
 }
