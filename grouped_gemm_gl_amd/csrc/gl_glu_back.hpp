@@ -203,7 +203,7 @@ inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32,
     if (!wgrad) {
       if (tiles(256) >= 160 && (rows <= 24 || rows > 96)) {
         q.w = p.b; q.w_ptrs = p.b_ptrs; q.K = p.N;
-        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256), rows <= 256, s);
+        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256), rows <= 256 ? kRaggedTiles : kFullTiles, s);
       }
       if (tiles(128) >= 192) return launch_glu_back_tile<IN, EL, false, 128>(p, s);
       return launch_glu_back_tile<IN, EL, false, 64>(p, s);
@@ -211,8 +211,8 @@ inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32,
     if (tiles(256) >= 128) {
       q.w = p.x; q.N = p.N; q.accumulate = p.accumulate;
       const int64_t items = (int64_t)p.G * ((p.N + 255) / 256) * ((p.K + 255) / 256);
-      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, false, s)
-                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, false, s);
+      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, kFullTiles, s)
+                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, kFullTiles, s);
     }
     if (tiles(128) >= 192)
       return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 128>(p, s) : launch_glu_back_tile<IN, EL, true, 128>(p, s);

@@ -105,7 +105,8 @@ struct MidTile {
   static_assert(kPieces == 4 && kColsHalf == 16 * (kWaves / 2), "waves cover the tile");
 };
 
-template <int IN, int EL, int EPI, int ROWS>
+// ONCE: the weights are loaded as data that is read once (see launch_glu).
+template <int IN, int EL, int EPI, int ROWS, bool ONCE>
 __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
@@ -157,8 +158,8 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
       // a half of weight rows is kWaves pieces, the rows 2 kWaves
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + wave * 1024), 16, o0, soff, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + (wave + M::kWaves) * 1024), 16, o1, soff, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (GL_LDS void *)(st + (wave + 2 * M::kWaves) * 1024), 16, o0, soff, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, (GL_LDS void *)(st + (wave + 3 * M::kWaves) * 1024), 16, o0, soff, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (GL_LDS void *)(st + (wave + 2 * M::kWaves) * 1024), 16, o0, soff, 0, ONCE ? 2 : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, (GL_LDS void *)(st + (wave + 3 * M::kWaves) * 1024), 16, o0, soff, 0, ONCE ? 2 : 0);
     };
     const int blocks = (rows - wm * 16 + 31) / 32;  // of the wave that hold rows
     acc_t acc[2][M::kBlocks];
@@ -226,13 +227,16 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
 }
 
 template <int IN, int EL, int EPI, int ROWS>
-inline hipError_t launch_glu_mid(const GluParams &p, hipStream_t s) {
+inline hipError_t launch_glu_mid(const GluParams &p, bool once, hipStream_t s) {
   using M = MidTile<ROWS>;
   constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
   const int64_t groups = p.T < p.G ? p.T : p.G;
   const int64_t items = ((p.T + ROWS - 1) / ROWS + groups) * ((p.F + kCols - 1) / kCols);
-  hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS>), dim3((unsigned)(items < 8192 ? items : 8192)),
-                     dim3(M::kThreads), 0, s, p);
+  const dim3 grid((unsigned)(items < 8192 ? items : 8192)), block(M::kThreads);
+  if (once)
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

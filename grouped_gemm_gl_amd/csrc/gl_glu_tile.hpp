@@ -131,8 +131,10 @@ struct TilePlace {
 // ACT: a run-time activation would be three copies of the epilogue, whose common values the
 // compiler computes ahead of them all and spills.
 // RAGGED: row blocks past a tile's rows are neither read from LDS nor multiplied, which costs full
-// tiles a tenth of their speed in branches.
-template <int IN, int EL, int EPI, int ACT, bool RAGGED>
+// tiles a tenth of their speed in branches.  kRaggedOnce: and the weights are loaded as data that is
+// read once.
+enum { kFullTiles = 0, kRaggedTiles = 1, kRaggedOnce = 2 };
+template <int IN, int EL, int EPI, int ACT, int RAGGED>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
       for (int q = 0; q < 2; ++q) {
         const uint32_t o = voff + (uint32_t)(((half == 1) * kHalf + q * 64) * kb);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GL_LDS void *)(to + q * 8192), 16, c16 < lim ? o : kOutside,
-                                                 lim > 0 ? at : 0, 0, 0);
+                                                 lim > 0 ? at : 0, 0, RAGGED == kRaggedOnce && half >= 2 ? 2 : 0);
       }
     }
   };
@@ -536,15 +538,21 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
 }
 
 template <int IN, int EL, int EPI, int ACT>
-inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, bool ragged, hipStream_t s) {
+inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged, hipStream_t s) {
   const dim3 grid(gemm::persistent_grid(items)), block(kTileThreads);
-  if constexpr (EPI != EPI_DW) {
-    if (ragged) {
-      hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, true>), grid, block, 0, s, p);
+  if constexpr (IN == IN_I8) {
+    if (ragged == kRaggedOnce) {
+      hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kRaggedOnce>), grid, block, 0, s, p);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, false>), grid, block, 0, s, p);
+  if constexpr (EPI != EPI_DW) {
+    if (ragged) {
+      hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kRaggedTiles>), grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kFullTiles>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -559,7 +567,13 @@ inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, bool ragged
 //   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
 //     4 groups, 333 rows, K 1024 F 2048 37 / 69 / 216;  8 groups, 16384 rows, K 4096 F 7168
 //     (4032 tiles of 256) 16504 / 14747 / 14029
-// and at most 16 rows with few columns: 4 of 4 groups, K 1024 F 512, fp32, 9.5 by splitting the
+// Weights of more than the 256 MB of the last-level cache that about one row tile of each group reads
+// are loaded as data that is read once: 64 groups, 4099 rows, K 2048 F 1400, fp16 (734 MB of weights),
+// tiles of 128 180 -> 172; with it 8-bit integers of F 1408 take 84 on tiles of 256, 95 on those of 128.
+// Smaller ones lose what the cache holds from call to call (8 of 64 groups of 6 MB: 14.3 -> 16.5), and
+// weights that more row tiles read lose it within the call (8 groups, 2048 rows, K 4096 F 7168 int8
+// 89 -> 103).
+// And at most 16 rows with few columns: 4 of 4 groups, K 1024 F 512, fp32, 9.5 by splitting the
 // contraction and 16 by 64 rows (64 workgroups); 8 of 64 groups, K 2048 F 768 16.1 and 11.8 (192).
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
@@ -567,13 +581,16 @@ inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
   constexpr int64_t kWide = EPI == EPI_PLAIN ? 1 : 2;  // weight rows a column
   auto tiles = [&](int64_t r) { return ((p.T + r - 1) / r + groups) * ((kWide * p.F + r - 1) / r); };
   if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= 128) return launch_glu_few<IN, EL, EPI>(p, s);
-  const bool large = IN == IN_F32 ? tiles(256) >= 2048 : rows > 96 && tiles(256) >= 160;
+  const bool once = rows <= 96 && groups * kWide * p.F * p.K * in_bytes(IN) > (int64_t)256 << 20;
+  const bool large = IN == IN_F32  ? tiles(256) >= 2048
+                     : IN == IN_I8 ? tiles(256) >= 160 && (rows > 96 || (rows > 24 && once))
+                                   : tiles(256) >= 160 && rows > 96;
   if (!large) {
     if constexpr (IN != IN_F32)
-      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128>(p, s);
-    return launch_glu_mid<IN, EL, EPI, 64>(p, s);
+      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128>(p, once, s);
+    return launch_glu_mid<IN, EL, EPI, 64>(p, once, s);
   }
-  const bool ragged = rows <= 256;  // 8 groups of 256 rows: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
+  const int ragged = once ? kRaggedOnce : rows <= 256 ? kRaggedTiles : kFullTiles;  // 8 groups of 256 rows: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
   if constexpr (EPI != EPI_PLAIN) {
     if (p.act == ACT_GELU) return launch_glu_tile<IN, EL, EPI, ACT_GELU>(p, tiles(256), ragged, s);
     if (p.act == ACT_GELU_TANH) return launch_glu_tile<IN, EL, EPI, ACT_GELU_TANH>(p, tiles(256), ragged, s);
