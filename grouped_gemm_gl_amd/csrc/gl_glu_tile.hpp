@@ -472,7 +472,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, t.rows - 1)] : 0.f;
+          rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, max(t.rows, 1) - 1)] : 0.f;
     }
     // dW is the group's own matrix; with accumulate, a group without rows is not touched
     void *const out = EPI == EPI_DW ? p.out ? (char *)p.out + (int64_t)t.g * p.N * p.F * elem_bytes(EL) : p.out_ptrs[t.g] : p.out;

@@ -440,7 +440,8 @@ int gl_glu_forward(int num_groups, int64_t in_features, int64_t ffn_features, in
  *   dx           [dx_rows, K], dx_rows >= T, rows >= T never written; NULL: not computed
  *   dw / dw_ptrs, wgrad_dtype and accumulate as in gl_wgrad; db / db_ptrs of dtype as in
  *                gl_wgrad_bgrad, or none
- * Every step is checked before any is launched.  T = 0 writes the empty groups' gradients.
+ * No other two buffers overlap.  Every step is checked before any is launched.  T = 0 writes the
+ * empty groups' gradients.
  */
 int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, int64_t total_rows, gl_dtype dtype,
                     gl_dtype wgrad_dtype, int act, const void *x, const void *w, const void *const *w_ptrs,
