@@ -3,9 +3,10 @@
 // few to fill the chip.
 //
 // Both are out[i][j] = sum_p A(i, p) B(p, j) with j contiguous in B and out; A is dh, contiguous in
-// p for dx and in i for dW.  Tiles of TILE x TILE outputs, TILE 64 (4 waves, two workgroups a CU)
-// or 128 (8 waves); stages of the contraction (64 values of 16 bits, 32 of 32) go straight to a
-// ring of four in LDS, three ahead, one barrier a stage (as in glu_mid_kernel).  An operand whose tile
+// p for dx and in i for dW.  Tiles of TI x TJ outputs: 64 x 64 (4 waves, two workgroups a CU), dx also
+// 32 x 64 (4 waves, three), or 128 x 128 (8 waves); stages of the contraction (64 values of 16 bits, 32 of
+// 32) go straight to a ring of STAGES in LDS, STAGES - 1 ahead, one barrier a stage (as in
+// glu_mid_kernel).  An operand whose tile
 // index is contiguous is staged as it lies, contraction row after contraction row, and turned on
 // the way out of LDS: 16-bit values by the transposing read, which hands a lane 4 contraction values
 // of one column, 32-bit ones by single-word reads.  16-byte slots are permuted by the row so that
@@ -19,18 +20,20 @@
 
 namespace gl {
 
-template <int IN, int EL, bool WGRAD, int TILE>
-__global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(BackParams p) {
+// ONCE: dx's weights are loaded as data that is read once.
+template <int IN, int EL, bool WGRAD, int TI, int TJ, int STAGES, bool ONCE>
+__global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kernel(BackParams p) {
   using Op = Operand<IN>;
-  using M = MidTile<TILE>;
-  using Tn = Turned<IN, TILE>;
+  using M = MidTile<TI, TJ, STAGES>;
+  using Tn = Turned<IN, TJ>;  // dW: of A too, TI is TJ
+  static_assert(!WGRAD || TI == TJ, "square tiles");
   constexpr int E = in_bytes(IN);
   __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
 
   const WsView ws = ws_view(p.ws, p.G);
-  const RowTiles tiles(ws, p.G, TILE);
+  const RowTiles tiles(ws, p.G, TI);
   if (!ws_usable(ws.hdr, p.G, p.T)) return;
-  const int tiles_i = (int)((p.N + TILE - 1) / TILE), tiles_j = (int)((p.K + TILE - 1) / TILE);
+  const int tiles_i = (int)((p.N + TI - 1) / TI), tiles_j = (int)((p.K + TJ - 1) / TJ);
   const int64_t total = WGRAD ? (int64_t)p.G * tiles_i * tiles_j : (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -55,9 +58,9 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
     }
     const int64_t g_off = tiles.row(g), g_rows = tiles.row(g + 1) - g_off;
     if (WGRAD && p.accumulate && g_rows == 0) continue;  // not touched
-    const int64_t i0 = (int64_t)it * TILE, j0 = (int64_t)jt * TILE;
+    const int64_t i0 = (int64_t)it * TI, j0 = (int64_t)jt * TJ;
     const int64_t contr = WGRAD ? g_rows : p.N;  // values of the contraction
-    const int rows = (int)min64(TILE, (WGRAD ? p.N : g_rows) - i0), cols = (int)min64(TILE, p.K - j0);
+    const int rows = (int)min64(TI, (WGRAD ? p.N : g_rows) - i0), cols = (int)min64(TJ, p.K - j0);
     if (!device_check(rows > 0 && cols > 0 && g_off >= 0 && g_off + g_rows <= p.T, p.ws)) continue;
     const char *a = WGRAD ? p.a + g_off * nbytes + i0 * E : p.a + (g_off + i0) * nbytes;
     const char *b = WGRAD ? p.x + g_off * kbytes
@@ -80,7 +83,7 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
           const int c = Tn::slot(row, lane % Tn::kSlots) * 16;  // its own inverse
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               r, (GL_LDS void *)(to + u * 1024), 16,
-              row < left && c < width * E ? (uint32_t)(row * (int)ld + c) : kPastEnd, 0, 0, 0);
+              row < left && c < width * E ? (uint32_t)(row * (int)ld + c) : kPastEnd, 0, 0, ONCE ? 2 : 0);
         }
       };
       if constexpr (WGRAD) {
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)gemm::uniform_ptr(a), (short)0,
                                                                            (int)(rows * nbytes), 0x00020000);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < M::kRowPieces; ++q) {
           const int u = wave + q * M::kWaves;
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               r, (GL_LDS void *)(st + u * 1024), 16,
@@ -97,7 +100,7 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
               left > 0 ? (int)(first * E) : 0, 0, 0);
         }
       }
-      turned(b, kbytes, cols, st + TILE * 128);
+      turned(b, kbytes, cols, st + TI * 128);
     };
     const int blocks = (rows - wm * 16 + 31) / 32;
     f32x4_t acc[2][M::kBlocks];
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
       // read_turned waits for its reads, so what is multiplied next is read before
       i32x4_t fb[2][2], fa[M::kBlocks][2];
       if constexpr (IN != IN_F32) {
-        const uint32_t at[2] = {Tn::address(st + TILE * 128, wn * 32, lane), Tn::address(st + TILE * 128, wn * 32 + 16, lane)};
+        const uint32_t at[2] = {Tn::address(st + TI * 128, wn * 32, lane), Tn::address(st + TI * 128, wn * 32 + 16, lane)};
         if constexpr (WGRAD) {
           uint32_t ata[M::kBlocks];
 #pragma unroll
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) fb[h][c] = Tn::frag(st + TILE * 128, wn * 32 + h * 16, c, lane);
+          for (int c = 0; c < 2; ++c) fb[h][c] = Tn::frag(st + TI * 128, wn * 32 + h * 16, c, lane);
       }
 #pragma unroll
       for (int i = 0; i < M::kBlocks; ++i) {
@@ -171,48 +174,66 @@ __global__ __launch_bounds__(MidTile<TILE>::kThreads, 2) void glu_back_kernel(Ba
   }
 }
 
-template <int IN, int EL, bool WGRAD, int TILE>
+template <int IN, int EL, bool WGRAD, int TI, int TJ = TI, int STAGES = 4, bool ONCE = false>
 inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
-  const int64_t tiles_j = (p.K + TILE - 1) / TILE, groups = p.T < p.G ? p.T : p.G;
-  const int64_t items = WGRAD ? p.G * ((p.N + TILE - 1) / TILE) * tiles_j : ((p.T + TILE - 1) / TILE + groups) * tiles_j;
-  hipLaunchKernelGGL((glu_back_kernel<IN, EL, WGRAD, TILE>), dim3((unsigned)(items < 8192 ? items : 8192)),
-                     dim3(MidTile<TILE>::kThreads), 0, s, p);
+  const int64_t tiles_j = (p.K + TJ - 1) / TJ, groups = p.T < p.G ? p.T : p.G;
+  const int64_t items = WGRAD ? p.G * ((p.N + TI - 1) / TI) * tiles_j : ((p.T + TI - 1) / TI + groups) * tiles_j;
+  hipLaunchKernelGGL((glu_back_kernel<IN, EL, WGRAD, TI, TJ, STAGES, ONCE>), dim3((unsigned)(items < 8192 ? items : 8192)),
+                     dim3(MidTile<TI, TJ>::kThreads), 0, s, p);
   return hipGetLastError();
 }
 
-// Which tiles.  fp32 always takes those of 64 (of 128 up to twice as slow, at most a tenth faster; the
-// grouped calls' fp32 kernel works on the vector units: 4 groups, 333 rows, K 1024 F 1024, both
-// products 386 us, here 82).  Measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
+// Which tiles.  fp32: dW those of 64 (of 128 up to twice as slow, at most a tenth faster) with a ring of
+// three, three workgroups a CU, because a group's rows are few stages (4 groups, 333 rows, K 1024 F 1024
+// 34.4 us with a ring of four, 30.3 of three; one of 4096 rows 167 and 169); dx 32 x 64 up to 896 of them, for
+// which 768 are under way at once (47 us on tiles of 64, 32 on these; one of 4096 rows, 2064 of them, 153 and
+// 165).  (The grouped calls' fp32 kernel works on the vector units: both products 386 us, here 62.)
+// 16 bits, dx: up to 256 tiles of 32 x 64 those (144: one group, 256 rows, K 1024 F 1024 13.3 us on tiles of
+// 64, 11.6; 544: 2 of 1024 rows 35.8 and 37.8 with dW), and else as measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
 //   dx by tiles of 256:  16 (1, 256, 2048, 2048) 25 / 41 / 88     64 (4, 1024, 2048, 2048) 50 / 41 / 87
 //                       144 (2, 4096, 2048, 2048) 116 / 89 / 89  272 (1, 4096, 4096, 4096) 439 / 318 / 220
 //      and rows a group: 16 (64, 1024, 1024, 512) 36 / 34 / 27    64 (64, 4096, 2048, 768) 119 / 103 / 130
 //      by tiles of 128: 144 (16, 256, 1024, 512) 9.9 / 11.9      192 (4, 1024, 2048, 2048) 50 / 41
 //   dW by tiles of 256:  32 (1, 8192, 1024, 1024) 81 / 92 / 196  128 (1, 2048, 2048, 2048) 75 / 59 / 63
 //                       256 (16, 256, 1024, 512) 32 / 25 / 17   1024 (16, 1024, 2048, 1024) 107 / 87 / 44
+// What passes the last-level cache's 256 MB does not stay there: weights that one or two row tiles a group read
+// and weight gradients then go past it (64 groups, 4099 rows, K 2048 F 1400 fp16, 734 MB each: dx 211 -> 172,
+// dW 213 -> 185; 8 of 1024, K 4096 F 7168 dx 331 -> 282, dW 280 -> 262).  Smaller weight gradients are left
+// where their next reader finds them, though they too are written faster (1 of 512, K 2048 F 2048, 17 MB,
+// 27.4 -> 25.8).
 template <int IN, int EL>
 inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s) {
+  const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
+  const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((p.K + 63) / 64);
   if constexpr (IN == IN_F32) {
-    return wgrad ? launch_glu_back_tile<IN, EL, true, 64>(p, s) : launch_glu_back_tile<IN, EL, false, 64>(p, s);
+    if (wgrad) return launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
+    if (rows <= 32 || tiles32 <= 896) return launch_glu_back_tile<IN, EL, false, 32, 64>(p, s);
+    return launch_glu_back_tile<IN, EL, false, 64>(p, s);
   } else {
-    const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
     auto tiles = [&](int64_t r) {
       return (wgrad ? groups * ((p.N + r - 1) / r) : (p.T + r - 1) / r + groups) * ((p.K + r - 1) / r);
     };
     GluParams q{};
     q.x = p.a; q.ws = p.ws; q.G = p.G; q.T = p.T; q.F = p.K; q.out = p.out; q.out_ptrs = p.out_ptrs;
     if (!wgrad) {
+      const bool large = groups * p.K * p.N * in_bytes(IN) > kLastLevelCache;  // weights
       if (tiles(256) >= 160 && (rows <= 24 || rows > 96)) {
         q.w = p.b; q.w_ptrs = p.b_ptrs; q.K = p.N;
-        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256), rows <= 256 ? kRaggedTiles : kFullTiles, s);
+        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256),
+                                                         rows > 256 ? kFullTiles : large ? kRaggedOnce : kRaggedTiles, s);
       }
-      if (tiles(128) >= 192) return launch_glu_back_tile<IN, EL, false, 128>(p, s);
-      return launch_glu_back_tile<IN, EL, false, 64>(p, s);
+      if (tiles(128) >= 192)
+        return large && rows <= 96 ? launch_glu_back_tile<IN, EL, false, 128, 128, 4, true>(p, s)
+                                   : launch_glu_back_tile<IN, EL, false, 128>(p, s);
+      return tiles32 <= 256 ? launch_glu_back_tile<IN, EL, false, 32, 64>(p, s)
+                            : launch_glu_back_tile<IN, EL, false, 64>(p, s);
     }
     if (tiles(256) >= 128) {
       q.w = p.x; q.N = p.N; q.accumulate = p.accumulate;
       const int64_t items = (int64_t)p.G * ((p.N + 255) / 256) * ((p.K + 255) / 256);
-      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, kFullTiles, s)
-                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, kFullTiles, s);
+      const int stores = p.G * p.N * p.K * (out_f32 ? 4 : in_bytes(IN)) > kLastLevelCache ? kWrittenOnce : kFullTiles;
+      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, stores, s)
+                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, stores, s);
     }
     if (tiles(128) >= 192)
       return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 128>(p, s) : launch_glu_back_tile<IN, EL, true, 128>(p, s);

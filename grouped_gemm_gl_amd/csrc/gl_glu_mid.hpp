@@ -1,6 +1,6 @@
 // Grouped products with a gated or scaled epilogue on small tiles, where 256-row tiles would be
-// too few to fill the chip: 64 rows by 64 weight rows (4 waves, two workgroups a CU) or 128 by
-// 128 (8 waves), half of the weight rows the gate's and half the other's of the same columns
+// too few to fill the chip: 32 rows by 32 weight rows (2 waves, five workgroups a CU) or by 64 (4
+// waves, three), 64 by 64 (4 waves, two) or 128 by 128 (8 waves, one), half of the weight rows the gate's and half the other's of the same columns
 // (plain: neighbouring columns).
 //
 // Stages of 128 bytes of every row go straight to a ring of kStages in LDS, kStages - 1 ahead, and
@@ -94,23 +94,23 @@ __device__ __forceinline__ void read_turned(const uint32_t (&at)[B], i32x4_t (&o
       o[b][c] = i32x4_t{v[b][2 * c][0], v[b][2 * c][1], v[b][2 * c + 1][0], v[b][2 * c + 1][1]};
 }
 
-template <int ROWS>
+template <int ROWS, int WEIGHT_ROWS = ROWS, int STAGES = 4>
 struct MidTile {
-  static constexpr int kWaves = ROWS / 16, kThreads = 64 * kWaves;
-  static constexpr int kStages = 4;
-  static constexpr int kStageBytes = 2 * ROWS * 128;  // rows, then weight rows
-  static constexpr int kPieces = kStageBytes / 1024 / kWaves;
+  static constexpr int kWaves = WEIGHT_ROWS / 16, kThreads = 64 * kWaves;
+  static constexpr int kStages = STAGES;
+  static constexpr int kStageBytes = (ROWS + WEIGHT_ROWS) * 128;  // rows, then weight rows
+  static constexpr int kRowPieces = ROWS / 8 / kWaves, kPieces = kRowPieces + 2;  // of 1 KiB, of a wave
   static constexpr int kBlocks = ROWS / 32;  // of 16 rows, of a wave
-  static constexpr int kColsHalf = ROWS / 2;  // weight rows of a half
-  static_assert(kPieces == 4 && kColsHalf == 16 * (kWaves / 2), "waves cover the tile");
+  static constexpr int kColsHalf = WEIGHT_ROWS / 2;  // weight rows of a half
+  static_assert(kPieces * kWaves * 1024 == kStageBytes && kColsHalf == 16 * (kWaves / 2), "waves cover the tile");
 };
 
 // ONCE: the weights are loaded as data that is read once (see launch_glu).
-template <int IN, int EL, int EPI, int ROWS, bool ONCE>
-__global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(GluParams p) {
+template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS, bool ONCE>
+__global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu_mid_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
-  using M = MidTile<ROWS>;
+  using M = MidTile<ROWS, WEIGHT_ROWS>;
   constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
   __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
 
@@ -125,7 +125,8 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
   const int fr = lane & 15, fq = lane >> 4;
   const int kb = (int)(p.K * in_bytes(IN));
   const int nk = (kb + 127) / 128;
-  // pieces of 8 rows: wave w has the pieces w, w + kWaves (of the rows), and so of the weight rows
+  // pieces of 8 rows: wave w has the pieces w and (not in 32 rows by 64) w + kWaves of the rows, and
+  // piece w of each half of the weight rows
   const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;
   const uint32_t voff = (uint32_t)(8 * wave + (lane >> 3)) * (uint32_t)kb + (uint32_t)c16;
 
@@ -155,11 +156,12 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
       const uint32_t far = (uint32_t)(8 * M::kWaves) * (uint32_t)kb;  // from a wave's piece of a half to its next
       const uint32_t o0 = c16 < lim ? voff : kPastEnd, o1 = c16 < lim ? voff + far : kPastEnd;
       const int soff = lim > 0 ? at : 0;
-      // a half of weight rows is kWaves pieces, the rows 2 kWaves
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + wave * 1024), 16, o0, soff, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + (wave + M::kWaves) * 1024), 16, o1, soff, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (GL_LDS void *)(st + (wave + 2 * M::kWaves) * 1024), 16, o0, soff, 0, ONCE ? 2 : 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, (GL_LDS void *)(st + (wave + 3 * M::kWaves) * 1024), 16, o0, soff, 0, ONCE ? 2 : 0);
+      if constexpr (M::kRowPieces == 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GL_LDS void *)(st + (wave + M::kWaves) * 1024), 16, o1, soff, 0, 0);
+      char *wt = st + ROWS * 128 + wave * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (GL_LDS void *)wt, 16, o0, soff, 0, ONCE ? 2 : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, (GL_LDS void *)(wt + M::kWaves * 1024), 16, o0, soff, 0, ONCE ? 2 : 0);
     };
     const int blocks = (rows - wm * 16 + 31) / 32;  // of the wave that hold rows
     acc_t acc[2][M::kBlocks];
@@ -226,17 +228,17 @@ __global__ __launch_bounds__(MidTile<ROWS>::kThreads, 2) void glu_mid_kernel(Glu
   }
 }
 
-template <int IN, int EL, int EPI, int ROWS>
+template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS>
 inline hipError_t launch_glu_mid(const GluParams &p, bool once, hipStream_t s) {
-  using M = MidTile<ROWS>;
+  using M = MidTile<ROWS, WEIGHT_ROWS>;
   constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
   const int64_t groups = p.T < p.G ? p.T : p.G;
   const int64_t items = ((p.T + ROWS - 1) / ROWS + groups) * ((p.F + kCols - 1) / kCols);
   const dim3 grid((unsigned)(items < 8192 ? items : 8192)), block(M::kThreads);
   if (once)
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, true>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

@@ -85,7 +85,7 @@ struct TileStore {
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t block(const void *base, int64_t row0, int64_t ld, int64_t col0) const {
     return gemm::rsrc_at(gemm::uniform_ptr((const char *)base + (row0 * ld + col0) * E));
   }
-  template <class F>
+  template <bool ONCE = false, class F>
   __device__ __forceinline__ void put(void *base, int64_t row0, int64_t ld, int64_t col0, int width, F value) const {
     const __amdgpu_buffer_rsrc_t rs = block(base, row0, ld, col0);
 #pragma unroll
@@ -97,8 +97,8 @@ struct TileStore {
       }
       order();
       const u32x4_t v0 = *moved(0), v1 = *moved(1);
-      __builtin_amdgcn_raw_buffer_store_b128(v0, rs, place(s, 0, ld, width), 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(v1, rs, place(s, 1, ld, width), 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v0, rs, place(s, 0, ld, width), 0, ONCE ? 2 : 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v1, rs, place(s, 1, ld, width), 0, ONCE ? 2 : 0);
       order();
     }
   }
@@ -132,8 +132,9 @@ struct TilePlace {
 // compiler computes ahead of them all and spills.
 // RAGGED: row blocks past a tile's rows are neither read from LDS nor multiplied, which costs full
 // tiles a tenth of their speed in branches.  kRaggedOnce: and the weights are loaded as data that is
-// read once.
-enum { kFullTiles = 0, kRaggedTiles = 1, kRaggedOnce = 2 };
+// read once.  kWrittenOnce: full tiles whose outputs are stored as data that is not read soon.
+enum { kFullTiles = 0, kRaggedTiles = 1, kRaggedOnce = 2, kWrittenOnce = 3 };
+constexpr int64_t kLastLevelCache = (int64_t)256 << 20;
 template <int IN, int EL, int EPI, int ACT, int RAGGED>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
@@ -143,6 +144,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   constexpr int kColsB = kGated ? kHalf : 2 * kHalf;  // output columns of a tile
   constexpr int kStageRows = kStageB / in_bytes(IN);  // contraction values of a stage
   using Tn = Turned<IN, kHalf>;
+  constexpr bool kSkip = RAGGED == kRaggedTiles || RAGGED == kRaggedOnce;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kRingBytes + kTileWaves * (kStoreBytes + kPlacesBytes)];
 
   const WsView ws = ws_view(p.ws, p.G);
@@ -295,7 +297,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (GL_LDS void *)(to + q * 8192), 16,
-                                                 tc16 + c < wide ? v + (uint32_t)(32 * q * ld + c) : kOutside, 0, 0, 0);
+                                                 tc16 + c < wide ? v + (uint32_t)(32 * q * ld + c) : kOutside, 0, 0,
+                                                 RAGGED == kRaggedOnce && half >= 2 ? 2 : 0);
     } else {
       const int at = load_stage * kStageB;
       const int lim = load_tile < count ? kb - at : 0;  // bytes of the row left
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (!RAGGED || 2 * half + i < blocks)
+        if (!kSkip || 2 * half + i < blocks)
 #pragma unroll
           for (int s = 0; s < 2; ++s) fa[i][s] = *(const i32x4_t *)(lds + (o ^ (64 * s)) + i * 64 * kStageB);
     }
@@ -370,7 +373,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
   auto multiply = [&](int set, int half, acc_t(&c)[2][4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (!RAGGED || 2 * half + i < blocks)
+      if (!kSkip || 2 * half + i < blocks)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -493,7 +496,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
             if (b == 1 && width1 <= 0) break;
             typename Q::raw old[4];
             if (EPI == EPI_DW && p.accumulate) st.get(out, t.row0, p.F, b ? second : col0, b ? width1 : width, old);
-            st.put(out, t.row0, p.F, b ? second : col0, b ? width1 : width, [&](int j) {
+            st.template put<RAGGED == kWrittenOnce>(out, t.row0, p.F, b ? second : col0, b ? width1 : width, [&](int j) {
               const acc_t v = acc[a][b][i][j];
               float4 o = make_float4(v[0], v[1], v[2], v[3]);
               if (EPI == EPI_DW && p.accumulate) {
@@ -540,13 +543,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
 template <int IN, int EL, int EPI, int ACT>
 inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged, hipStream_t s) {
   const dim3 grid(gemm::persistent_grid(items)), block(kTileThreads);
-  if constexpr (IN == IN_I8) {
+  if constexpr (IN == IN_I8 || EPI == EPI_DX) {
     if (ragged == kRaggedOnce) {
       hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kRaggedOnce>), grid, block, 0, s, p);
       return hipGetLastError();
     }
   }
-  if constexpr (EPI != EPI_DW) {
+  if constexpr (EPI == EPI_DW) {
+    if (ragged == kWrittenOnce) {
+      hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kWrittenOnce>), grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  } else {
     if (ragged) {
       hipLaunchKernelGGL((glu_tile_kernel<IN, EL, EPI, ACT, kRaggedTiles>), grid, block, 0, s, p);
       return hipGetLastError();
@@ -567,28 +575,49 @@ inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged,
 //   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
 //     4 groups, 333 rows, K 1024 F 2048 37 / 69 / 216;  8 groups, 16384 rows, K 4096 F 7168
 //     (4032 tiles of 256) 16504 / 14747 / 14029
+// Among the small tiles (rows by weight rows; us):
+//   16 bits, 64 x 64 / 32 x 32: at most 256 tiles of 64: 2 groups, 64 rows, K 4096 F 2048 23.6 / 15.8, one of
+//     300, K 1024 F 1024 8.3 / 7.6 (at 1 of 128, K 4096 F 4096, 384 tiles, 23.2 / 25.8).  At most 8 rows
+//     a group: 64 of 256, K 4096 F 768 170 / 134, 8 of 16, K 4096 F 7168 156 / 136, but K 2048 72 / 76 and 81 / 84
+//     (64 of 1024, K 2048 F 768 76 / 86).
+//   8-bit integers, 64 x 64 / 32 x 64: 64 of 32 rows, K 1408 N 2048 16.1 / 13.5; 64 of 1024 37.8 / 34.4; one of
+//     512, K 2048 N 1024 8.6 / 7.7; one of 32, K 4096 N 4096 10.8 / 11.2.
+//   fp32, 64 x 64 / 32 x 64: up to 896 tiles of 32, for which 768 are under way at once: 8 of 600, K 2048 F 1024
+//     (864) 71 / 60, but 4 of 333, K 1024 F 2048 (960) 37 / 41.  64 of 64, K 1024 F 512 39 / 34; one of 256,
+//     K 4096 F 4096 (1152) 137 / 165.
 // Weights of more than the 256 MB of the last-level cache that about one row tile of each group reads
 // are loaded as data that is read once: 64 groups, 4099 rows, K 2048 F 1400, fp16 (734 MB of weights),
 // tiles of 128 180 -> 172; with it 8-bit integers of F 1408 take 84 on tiles of 256, 95 on those of 128.
 // Smaller ones lose what the cache holds from call to call (8 of 64 groups of 6 MB: 14.3 -> 16.5), and
 // weights that more row tiles read lose it within the call (8 groups, 2048 rows, K 4096 F 7168 int8
 // 89 -> 103).
-// And at most 16 rows with few columns: 4 of 4 groups, K 1024 F 512, fp32, 9.5 by splitting the
-// contraction and 16 by 64 rows (64 workgroups); 8 of 64 groups, K 2048 F 768 16.1 and 11.8 (192).
+// And at most 16 rows with few columns, by tiles of 64 weight rows (us; the contraction split / tiles of 32 rows):
+//   16 bits: 64 (4 groups of 8 rows, K 1024 F 512) 6.4 / 6.5, 256 (one of 16, K 4096 F 4096, 128) 14.8 / 15.4,
+//     192 (8 of 64, 8 rows, K 2048 F 768) 13.6 / 11.3;  8 bits: 128 (one of 16, K 4096 N 8192) 9.6 / 11.3,
+//     256 (4 of 16, K 2048 N 4096) 9.0 / 7.8.
+//   fp32: 192 (8 of 8, K 2048 F 768) 15.5 / 29, 256 (16 of 64, K 1024 F 512) 14.4 / 17.8, 512 (8 of 8, K 2048
+//     F 2048) 36.6 / 30.6.
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
   const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
   constexpr int64_t kWide = EPI == EPI_PLAIN ? 1 : 2;  // weight rows a column
   auto tiles = [&](int64_t r) { return ((p.T + r - 1) / r + groups) * ((kWide * p.F + r - 1) / r); };
-  if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= 128) return launch_glu_few<IN, EL, EPI>(p, s);
-  const bool once = rows <= 96 && groups * kWide * p.F * p.K * in_bytes(IN) > (int64_t)256 << 20;
+  if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= (IN == IN_F32 ? 256 : 128)) return launch_glu_few<IN, EL, EPI>(p, s);
+  const bool once = rows <= 96 && groups * kWide * p.F * p.K * in_bytes(IN) > kLastLevelCache;
   const bool large = IN == IN_F32  ? tiles(256) >= 2048
                      : IN == IN_I8 ? tiles(256) >= 160 && (rows > 96 || (rows > 24 && once))
                                    : tiles(256) >= 160 && rows > 96;
   if (!large) {
-    if constexpr (IN != IN_F32)
-      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128>(p, once, s);
-    return launch_glu_mid<IN, EL, EPI, 64>(p, once, s);
+    if constexpr (IN == IN_F32) {
+      const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((kWide * p.F + 63) / 64);
+      if (rows <= 32 || tiles32 <= 896) return launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
+      return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
+    } else {
+      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128, 128>(p, once, s);
+      if constexpr (IN == IN_I8) return launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
+      else if (rows <= 8 || tiles(64) <= 256) return launch_glu_mid<IN, EL, EPI, 32, 32>(p, once, s);
+      else return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
+    }
   }
   const int ragged = once ? kRaggedOnce : rows <= 256 ? kRaggedTiles : kFullTiles;  // 8 groups of 256 rows: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
   if constexpr (EPI != EPI_PLAIN) {
