@@ -20,7 +20,8 @@
 
 namespace gl {
 
-// ONCE: dx's weights are loaded as data that is read once.
+// ONCE: dx's weights are loaded as data that is read once, fp32 weight gradients stored as data that is
+// not read soon.
 template <int IN, int EL, bool WGRAD, int TI, int TJ, int STAGES, bool ONCE>
 __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kernel(BackParams p) {
   using Op = Operand<IN>;
@@ -83,7 +84,7 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
           const int c = Tn::slot(row, lane % Tn::kSlots) * 16;  // its own inverse
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               r, (GL_LDS void *)(to + u * 1024), 16,
-              row < left && c < width * E ? (uint32_t)(row * (int)ld + c) : kPastEnd, 0, 0, ONCE ? 2 : 0);
+              row < left && c < width * E ? (uint32_t)(row * (int)ld + c) : kPastEnd, 0, 0, ONCE && !WGRAD ? 2 : 0);
         }
       };
       if constexpr (WGRAD) {
@@ -166,7 +167,12 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
           const float4 o = load4<EL>(out, at);
           v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
         }
-        put4<EL>(out, at, v);
+        if constexpr (WGRAD && ONCE) {
+          static_assert(EL == EL_F32, "fp32 gradients");
+          __builtin_nontemporal_store(f32x4_t{v.x, v.y, v.z, v.w}, (f32x4_t *)((float *)out + at));
+        } else {
+          put4<EL>(out, at, v);
+        }
       }
     }
     gemm::wait_vm0();
@@ -198,7 +204,8 @@ inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
 //                       256 (16, 256, 1024, 512) 32 / 25 / 17   1024 (16, 1024, 2048, 1024) 107 / 87 / 44
 // What passes the last-level cache's 256 MB does not stay there: weights that one or two row tiles a group read
 // and weight gradients then go past it (64 groups, 4099 rows, K 2048 F 1400 fp16, 734 MB each: dx 211 -> 172,
-// dW 213 -> 185; 8 of 1024, K 4096 F 7168 dx 331 -> 282, dW 280 -> 262).  Smaller weight gradients are left
+// dW 213 -> 185; 8 of 1024, K 4096 F 7168 dx 331 -> 282, dW 280 -> 262;
+// fp32, 8 of 16, K 4096 F 4096 dx 223 -> 156, dW 333 -> 298).  Smaller weight gradients are left
 // where their next reader finds them, though they too are written faster (1 of 512, K 2048 F 2048, 17 MB,
 // 27.4 -> 25.8).
 template <int IN, int EL>
@@ -206,9 +213,15 @@ inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32,
   const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
   const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((p.K + 63) / 64);
   if constexpr (IN == IN_F32) {
-    if (wgrad) return launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
-    if (rows <= 32 || tiles32 <= 896) return launch_glu_back_tile<IN, EL, false, 32, 64>(p, s);
-    return launch_glu_back_tile<IN, EL, false, 64>(p, s);
+    if (wgrad)
+      return p.G * p.N * p.K * 4 > kLastLevelCache ? launch_glu_back_tile<IN, EL, true, 64, 64, 3, true>(p, s)
+                                                   : launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
+    const bool once = rows <= 96 && groups * p.K * p.N * 4 > kLastLevelCache;
+    if (rows <= 32 || tiles32 <= 896)
+      return once ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, true>(p, s)
+                  : launch_glu_back_tile<IN, EL, false, 32, 64>(p, s);
+    return once ? launch_glu_back_tile<IN, EL, false, 64, 64, 4, true>(p, s)
+                : launch_glu_back_tile<IN, EL, false, 64>(p, s);
   } else {
     auto tiles = [&](int64_t r) {
       return (wgrad ? groups * ((p.N + r - 1) / r) : (p.T + r - 1) / r + groups) * ((p.K + r - 1) / r);

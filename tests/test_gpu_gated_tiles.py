@@ -67,6 +67,8 @@ BACKWARD = {
     "dx 32x64 f32": (F32, [33, 0, 1, 70], 260, 36),
     "dx 64 f32": (F32, [300, 2, 513], 2052, 68),               # 957 tiles of 32
     "dx 256, dW stored once": (BF, [100, 0, 140, 500, 1, 59, 0, 8], 4104, 2056),  # 270 MB of weights
+    "dx 32x64, once f32": (F32, [2, 0, 7, 33, 1, 9, 0, 8], 3076, 1420),            # 280 MB
+    "dx 64, once f32": (F32, [40, 0, 70, 133, 1, 9, 0, 58], 3076, 1420),          # 38 rows a group
     "dx 128, weights once": (F16, [30, 0, 41, 200, 1, 9, 0, 8], 4104, 2056),
 }
 
