@@ -34,6 +34,14 @@
 // last valid row, so rows past the group's or the matrix's end load zeros without a test; a lane's
 // offset from there is the same for every stream, because the rows of both operands have the same
 // length; past the row's end (the last stage) lanes take an offset out of range, and get zeros.
+//
+// The products of the backward whose operands lie with the other index contiguous (dx's weights, both of
+// dW's) stage them as they lie, contraction row after contraction row, and turn them on the way out of LDS
+// (read_turned, which waits for itself: there a phase's loads go out before its reads).
+//
+// Bound by the matrix cores: 8 groups, 16384 rows, K 4096 F 7168 bf16 1425 us, 1350 TFLOP/s (with h 1475), int8
+// 782 us, 2460 TOP/s; a library product of that size reaches 1438 and 2313.  dx and dW 1640 and 1660 us, 1170
+// and 1160 TFLOP/s, by the reads of the turned operands.  Without the lag of the second wave group 1651.
 #pragma once
 
 #include "gl_gemm_tile.hpp"
