@@ -4,7 +4,7 @@
 //
 // Both are out[i][j] = sum_p A(i, p) B(p, j) with j contiguous in B and out; A is dh, contiguous in
 // p for dx and in i for dW.  Tiles of TI x TJ outputs: 64 x 64 (4 waves, two workgroups a CU), dx also
-// 32 x 64 (4 waves, three), or 128 x 128 (8 waves); stages of the contraction (64 values of 16 bits, 32 of
+// 32 x 64 (4 waves, three; or with the contraction in two parts 8, one), or 128 x 128 (8 waves); stages of the contraction (64 values of 16 bits, 32 of
 // 32) go straight to a ring of STAGES in LDS, STAGES - 1 ahead, one barrier a stage (as in
 // glu_mid_kernel).  An operand whose tile
 // index is contiguous is staged as it lies, contraction row after contraction row, and turned on
@@ -22,14 +22,16 @@ namespace gl {
 
 // ONCE: dx's weights are loaded as data that is read once, fp32 weight gradients stored as data that is
 // not read soon.
-template <int IN, int EL, bool WGRAD, int TI, int TJ, int STAGES, bool ONCE>
-__global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kernel(BackParams p) {
+// PARTS of dx's contraction, as in glu_mid_kernel.
+template <int IN, int EL, bool WGRAD, int TI, int TJ, int STAGES, bool ONCE, int PARTS>
+__global__ __launch_bounds__((PARTS * MidTile<TI, TJ>::kThreads), 2) void glu_back_kernel(BackParams p) {
   using Op = Operand<IN>;
   using M = MidTile<TI, TJ, STAGES>;
   using Tn = Turned<IN, TJ>;  // dW: of A too, TI is TJ
   static_assert(!WGRAD || TI == TJ, "square tiles");
   constexpr int E = in_bytes(IN);
-  __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
+  constexpr int kRing = M::kStages * M::kStageBytes;
+  __shared__ __attribute__((aligned(1024))) char lds[PARTS * kRing];
 
   const WsView ws = ws_view(p.ws, p.G);
   const RowTiles tiles(ws, p.G, TI);
@@ -37,7 +39,9 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
   const int tiles_i = (int)((p.N + TI - 1) / TI), tiles_j = (int)((p.K + TJ - 1) / TJ);
   const int64_t total = WGRAD ? (int64_t)p.G * tiles_i * tiles_j : (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int index = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = PARTS == 1 ? 0 : index / M::kWaves, wave = PARTS == 1 ? index : index % M::kWaves;
+  char *const ring = lds + part * kRing;
   const int wm = wave & 1, wn = wave >> 1;
   const int fr = lane & 15, fq = lane >> 4;
   const int64_t kbytes = p.K * E, nbytes = p.N * E;
@@ -67,14 +71,15 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
     const char *b = WGRAD ? p.x + g_off * kbytes
                           : p.b ? p.b + (int64_t)g * p.N * kbytes : p.b_ptrs[g];
     b += j0 * E;
-    const int nk = (int)((contr + Tn::kRows - 1) / Tn::kRows);
+    const int stages = (int)((contr + Tn::kRows - 1) / Tn::kRows), nk = (stages + PARTS - 1) / PARTS;  // nk of each part
+    const int64_t part0 = (int64_t)part * nk * Tn::kRows;
 
     // K-major A: pieces of 8 rows, 128 bytes of each; turned operands: pieces of kPieceRows rows
     const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;
     auto issue = [&](int s) {
-      char *st = lds + (s % M::kStages) * M::kStageBytes;
-      const int64_t first = (int64_t)s * Tn::kRows;
-      const int left = s < nk ? (int)min64(Tn::kRows, contr - first) : 0;  // contraction values of the stage
+      char *st = ring + (s % M::kStages) * M::kStageBytes;
+      const int64_t first = part0 + (int64_t)s * Tn::kRows;
+      const int left = s < nk && (PARTS == 1 || first < contr) ? (int)min64(Tn::kRows, contr - first) : 0;  // contraction values of the stage
       auto turned = [&](const char *base, int64_t ld, int width, char *to) {
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
             (void *)gemm::uniform_ptr(base + (left > 0 ? first * ld : 0)), (short)0, (int)(max(left, 1) * ld), 0x00020000);
@@ -117,7 +122,7 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       issue(s + M::kStages - 1);
-      const char *st = lds + (s % M::kStages) * M::kStageBytes;
+      const char *st = ring + (s % M::kStages) * M::kStageBytes;
       // read_turned waits for its reads, so what is multiplied next is read before
       i32x4_t fb[2][2], fa[M::kBlocks][2];
       if constexpr (IN != IN_F32) {
@@ -151,12 +156,13 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
         }
       }
     }
+    if constexpr (PARTS == 2) add_parts<2 * M::kBlocks>(lds, part, wave, lane, &acc[0][0]);
     void *out = WGRAD && !p.out ? p.out_ptrs[g] : p.out;
     const int64_t out0 = WGRAD ? (p.out ? (int64_t)g * p.N * p.K : 0) + i0 * p.K : (g_off + i0) * p.K;
 #pragma unroll
     for (int i = 0; i < M::kBlocks; ++i) {
       const int rl = i * 32 + wm * 16 + fr;
-      if (rl >= rows) break;
+      if (rl >= rows || part != 0) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int c = wn * 32 + h * 16 + fq * 4;
@@ -180,12 +186,12 @@ __global__ __launch_bounds__((MidTile<TI, TJ>::kThreads), 2) void glu_back_kerne
   }
 }
 
-template <int IN, int EL, bool WGRAD, int TI, int TJ = TI, int STAGES = 4, bool ONCE = false>
+template <int IN, int EL, bool WGRAD, int TI, int TJ = TI, int STAGES = 4, bool ONCE = false, int PARTS = 1>
 inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
   const int64_t tiles_j = (p.K + TJ - 1) / TJ, groups = p.T < p.G ? p.T : p.G;
   const int64_t items = WGRAD ? p.G * ((p.N + TI - 1) / TI) * tiles_j : ((p.T + TI - 1) / TI + groups) * tiles_j;
-  hipLaunchKernelGGL((glu_back_kernel<IN, EL, WGRAD, TI, TJ, STAGES, ONCE>), dim3((unsigned)(items < 8192 ? items : 8192)),
-                     dim3(MidTile<TI, TJ>::kThreads), 0, s, p);
+  hipLaunchKernelGGL((glu_back_kernel<IN, EL, WGRAD, TI, TJ, STAGES, ONCE, PARTS>), dim3((unsigned)(items < 8192 ? items : 8192)),
+                     dim3(PARTS * MidTile<TI, TJ>::kThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -193,9 +199,10 @@ inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
 // three, three workgroups a CU, because a group's rows are few stages (4 groups, 333 rows, K 1024 F 1024
 // 34.4 us with a ring of four, 30.3 of three; one of 4096 rows 167 and 169); dx 32 x 64 up to 896 of them, for
 // which 768 are under way at once (47 us on tiles of 64, 32 on these; one of 4096 rows, 2064 of them, 153 and
-// 165).  (The grouped calls' fp32 kernel works on the vector units: both products 386 us, here 62.)
-// 16 bits, dx: up to 256 tiles of 32 x 64 those (144: one group, 256 rows, K 1024 F 1024 13.3 us on tiles of
-// 64, 11.6; 544: 2 of 1024 rows 35.8 and 37.8 with dW), and else as measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
+// 165), up to 384 with the contraction in two parts (240: those 32 -> 27; 864: 66 -> 84).  (The grouped calls' fp32 kernel works on the vector units: both products 386 us, here 57.)
+// 16 bits, dx: up to 256 tiles of 32 x 64 those, in two parts (144: one group, 256 rows, K 1024 F 1024 13.3 us
+// on tiles of 64, 11.8 in one part, 9.7 in two; 544: 2 of 1024 rows 35.8 and 37.8 with dW), and else as
+// measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
 //   dx by tiles of 256:  16 (1, 256, 2048, 2048) 25 / 41 / 88     64 (4, 1024, 2048, 2048) 50 / 41 / 87
 //                       144 (2, 4096, 2048, 2048) 116 / 89 / 89  272 (1, 4096, 4096, 4096) 439 / 318 / 220
 //      and rows a group: 16 (64, 1024, 1024, 512) 36 / 34 / 27    64 (64, 4096, 2048, 768) 119 / 103 / 130
@@ -216,6 +223,7 @@ inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32,
     if (wgrad)
       return p.G * p.N * p.K * 4 > kLastLevelCache ? launch_glu_back_tile<IN, EL, true, 64, 64, 3, true>(p, s)
                                                    : launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
+    if (tiles32 <= 384) return launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s);
     const bool once = rows <= 96 && groups * p.K * p.N * 4 > kLastLevelCache;
     if (rows <= 32 || tiles32 <= 896)
       return once ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, true>(p, s)
@@ -238,7 +246,7 @@ inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32,
       if (tiles(128) >= 192)
         return large && rows <= 96 ? launch_glu_back_tile<IN, EL, false, 128, 128, 4, true>(p, s)
                                    : launch_glu_back_tile<IN, EL, false, 128>(p, s);
-      return tiles32 <= 256 ? launch_glu_back_tile<IN, EL, false, 32, 64>(p, s)
+      return tiles32 <= 256 ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s)
                             : launch_glu_back_tile<IN, EL, false, 64>(p, s);
     }
     if (tiles(256) >= 128) {

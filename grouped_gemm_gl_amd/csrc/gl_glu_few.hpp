@@ -1,16 +1,18 @@
-// Grouped products with a gated or scaled epilogue for at most 16 rows in all and few columns:
-// one row tile a group, and not enough of it to fill the chip, so the contraction is split too.
+// The fp32 gated products for at most 16 rows in all and few columns: one row tile a group, and not
+// enough of it to fill the chip, so the contraction is split too.
 //
 // A workgroup of four waves takes 16 columns of the gate and the 16 of the other half that
-// belong to them (plain: 32 columns) of one group.  Its waves split the contraction: wave v takes
+// belong to them of one group.  Its waves split the contraction: wave v takes
 // units v, v + 4, .., a unit being 128 bytes of every row, straight from memory to registers as
 // whole 128-byte lines (8 rows a load, and a rotation of 8 lanes gives the matrix instruction its
 // layout).  The weights are the instruction's first operand and the rows its second, so a lane
 // ends with four neighbouring columns of a row.  The four waves' sums meet in LDS and are added in
 // a fixed order.
 //
-// Bound by the latency of a few loads one after the other: one row, K 1024 F 2048, bf16 6 us a call, 8 rows
-// on 4 groups, K 1024 F 512, fp32 9.2 (16.2 on tiles, which go through the contraction in one piece).
+// Bound by the latency of a few loads one after the other: 8 rows on 4 groups, K 1024 F 512, 9.1 us a call,
+// 13.6 on tiles of 32 by 64 with the contraction in two parts.  (16 bits and 8-bit integers, whose stages
+// hold two and four times the values, go by those tiles: 6.3 us both, 2 groups of 16, K 2048 F 2048 bf16 8.9
+// here and 7.9 there, but one of 16, K 4096 F 4096 14.8 and 15.4.)
 #pragma once
 
 #include "gl_glu.hpp"
@@ -46,11 +48,11 @@ struct RowBlock {
   }
 };
 
-template <int IN, int EL, int EPI>
+template <int EPI>
 __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
+  constexpr int IN = IN_F32, EL = EL_F32, kCols = 16;
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
-  constexpr int kCols = EPI == EPI_PLAIN ? 32 : 16;
   __shared__ acc_t part[kFewWaves][2][64];
   const WsView ws = ws_view(p.ws, p.G);
   const RowTiles tiles(ws, p.G, 32);
@@ -70,16 +72,13 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
     const int rows = (int)min64(16, tiles.row(g + 1) - row0);
     if (!device_check(rows > 0 && row0 >= 0 && row0 + rows <= p.T && qt == tiles.tile(g), p.ws)) continue;
     const int64_t col0 = (int64_t)jt * kCols;
-    // weight rows of the first 16 columns and of the second: the other half, or the next 16
     const char *wg = group_weights<IN, EPI>(p, g);
-    const int64_t second = EPI == EPI_PLAIN ? col0 + 16 : p.F + col0;
-    const int cols0 = (int)min64(16, p.F - col0);
-    const int cols1 = EPI == EPI_PLAIN ? (int)max((int64_t)0, min64(16, p.F - second)) : cols0;
+    const int64_t second = p.F + col0;
+    const int cols = (int)min64(16, p.F - col0);
     const __amdgpu_buffer_rsrc_t w0 = few_rsrc(wg + col0 * kb);
-    const __amdgpu_buffer_rsrc_t w1 = few_rsrc(wg + (cols1 > 0 ? second : col0) * kb);
+    const __amdgpu_buffer_rsrc_t w1 = few_rsrc(wg + second * kb);
     const uint32_t low = (r & 7) * kb + chunk, high = low + 8 * kb;
-    const bool low0 = (r & 7) < cols0, high0 = (r & 7) + 8 < cols0;
-    const bool low1 = (r & 7) < cols1, high1 = (r & 7) + 8 < cols1;
+    const bool loww = (r & 7) < cols, highw = (r & 7) + 8 < cols;
 
     const __amdgpu_buffer_rsrc_t xr = few_rsrc(p.x + row0 * kb);
     const bool lowx = (r & 7) < rows, highx = (r & 7) + 8 < rows;
@@ -89,8 +88,8 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
     };
     auto load = [&](Unit &n, uint32_t at) {
       const bool in = at + chunk < kb;
-      n.g.load(w0, in && low0 ? low + at : kPastEnd, in && high0 ? high + at : kPastEnd);
-      n.u.load(w1, in && low1 ? low + at : kPastEnd, in && high1 ? high + at : kPastEnd);
+      n.g.load(w0, in && loww ? low + at : kPastEnd, in && highw ? high + at : kPastEnd);
+      n.u.load(w1, in && loww ? low + at : kPastEnd, in && highw ? high + at : kPastEnd);
       n.x.load(xr, in && lowx ? low + at : kPastEnd, in && highx ? high + at : kPastEnd);
     };
     auto multiply = [&](const Unit &n) {
@@ -123,16 +122,10 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
 #pragma unroll
         for (int v = 1; v < kFewWaves; ++v) acc[h] += part[v][h][lane];
       const int64_t row = row0 + r;
-      const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
       const int c = 4 * q;
-      if constexpr (EPI == EPI_PLAIN) {
-        if (c < cols0)
-          put4<EL>(p.out, row * p.F + col0 + c, finish<IN, EL>(acc[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c)));
-        if (c < cols1)
-          put4<EL>(p.out, row * p.F + second + c, finish<IN, EL>(acc[1], rs, column_terms<IN, EL, EPI>(p, g, second + c)));
-      } else if (c < cols0) {
-        const float4 v0 = finish<IN, EL>(acc[0], rs, column_terms<IN, EL, EPI>(p, g, col0 + c));
-        const float4 v1 = finish<IN, EL>(acc[1], rs, column_terms<IN, EL, EPI>(p, g, second + c));
+      if (c < cols) {
+        const float4 v0 = finish<IN, EL>(acc[0], 0.f, column_terms<IN, EL, EPI>(p, g, col0 + c));
+        const float4 v1 = finish<IN, EL>(acc[1], 0.f, column_terms<IN, EL, EPI>(p, g, second + c));
         with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
       }
     }
@@ -140,11 +133,10 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
   }
 }
 
-template <int IN, int EL, int EPI>
+template <int EPI>
 inline hipError_t launch_glu_few(const GluParams &p, hipStream_t s) {
-  constexpr int kCols = EPI == EPI_PLAIN ? 32 : 16;
-  const int64_t items = (p.T < p.G ? p.T : p.G) * ((p.F + kCols - 1) / kCols);
-  hipLaunchKernelGGL((glu_few_kernel<IN, EL, EPI>), dim3((unsigned)(items < 4096 ? items : 4096)), dim3(kFewThreads), 0,
+  const int64_t items = (p.T < p.G ? p.T : p.G) * ((p.F + 15) / 16);
+  hipLaunchKernelGGL((glu_few_kernel<EPI>), dim3((unsigned)(items < 4096 ? items : 4096)), dim3(kFewThreads), 0,
                      s, p);
   return hipGetLastError();
 }

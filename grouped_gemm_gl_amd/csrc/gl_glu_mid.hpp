@@ -1,6 +1,6 @@
 // Grouped products with a gated or scaled epilogue on small tiles, where 256-row tiles would be
 // too few to fill the chip: 32 rows by 32 weight rows (2 waves, five workgroups a CU) or by 64 (4
-// waves, three), 64 by 64 (4 waves, two) or 128 by 128 (8 waves, one), half of the weight rows the gate's and half the other's of the same columns
+// waves, three), either also with the contraction in two parts (twice the waves and LDS), 64 by 64 (4 waves, two) or 128 by 128 (8 waves, one), half of the weight rows the gate's and half the other's of the same columns
 // (plain: neighbouring columns).
 //
 // Stages of 128 bytes of every row go straight to a ring of kStages in LDS, kStages - 1 ahead, and
@@ -110,14 +110,34 @@ struct MidTile {
   static_assert(kPieces * kWaves * 1024 == kStageBytes && kColsHalf == 16 * (kWaves / 2), "waves cover the tile");
 };
 
-// ONCE: the weights are loaded as data that is read once (see launch_glu).
-template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS, bool ONCE>
-__global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu_mid_kernel(GluParams p) {
+// The contraction in two parts: twice the waves, the second half of which goes through the second half
+// of the stages in a ring of its own; its sums are added to the first's, in LDS, in a fixed order.
+// add_parts is called by every wave, after which those of part 0 have the sums.
+template <int N, class acc_t>
+__device__ __forceinline__ void add_parts(char *lds, int part, int wave, int lane, acc_t *acc) {
+  gemm::wait_vm0();
+  __syncthreads();  // the ring is not in use any more
+  acc_t *sums = (acc_t *)lds + wave * N * 64 + lane;
+  if (part == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i * 64] = acc[i];
+  }
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] += sums[i * 64];
+  }
+}
+
+// ONCE: the weights are loaded as data that is read once; PARTS of the contraction (see launch_glu).
+template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS, bool ONCE, int PARTS>
+__global__ __launch_bounds__((PARTS * MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu_mid_kernel(GluParams p) {
   using Op = Operand<IN>;
   using acc_t = typename Op::acc_t;
   using M = MidTile<ROWS, WEIGHT_ROWS>;
   constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
-  __shared__ __attribute__((aligned(1024))) char lds[M::kStages * M::kStageBytes];
+  constexpr int kRing = M::kStages * M::kStageBytes;
+  __shared__ __attribute__((aligned(1024))) char lds[PARTS * kRing];
 
   const WsView ws = ws_view(p.ws, p.G);
   const RowTiles tiles(ws, p.G, ROWS);
@@ -125,11 +145,13 @@ __global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu
   const int tiles_j = (int)((p.F + kCols - 1) / kCols);
   const int64_t total = (int64_t)tiles.tile(p.G) * tiles_j;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int index = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = PARTS == 1 ? 0 : index / M::kWaves, wave = PARTS == 1 ? index : index % M::kWaves;
   const int wm = wave & 1, wn = wave >> 1;
   const int fr = lane & 15, fq = lane >> 4;
   const int kb = (int)(p.K * in_bytes(IN));
-  const int nk = (kb + 127) / 128;
+  const int stages = (kb + 127) / 128, nk = (stages + PARTS - 1) / PARTS, part0 = part * nk * 128;  // nk of each part
+  char *const ring = lds + part * kRing;
   // pieces of 8 rows: wave w has the pieces w and (not in 32 rows by 64) w + kWaves of the rows, and
   // piece w of each half of the weight rows
   const int c16 = ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)) * 16;
@@ -156,8 +178,8 @@ __global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu
         has1 ? rsrc(wg + second * kb, min64(M::kColsHalf, EPI == EPI_PLAIN ? left - M::kColsHalf : left))
              : rsrc(wg + col0 * kb, 1);
     auto issue = [&](int s) {
-      char *st = lds + (s % M::kStages) * M::kStageBytes;
-      const int at = s * 128, lim = s < nk ? kb - at : 0;
+      char *st = ring + (s % M::kStages) * M::kStageBytes;
+      const int at = part0 + s * 128, lim = s < nk ? kb - at : 0;
       const uint32_t far = (uint32_t)(8 * M::kWaves) * (uint32_t)kb;  // from a wave's piece of a half to its next
       const uint32_t o0 = c16 < lim ? voff : kPastEnd, o1 = c16 < lim ? voff + far : kPastEnd;
       const int soff = lim > 0 ? at : 0;
@@ -182,7 +204,7 @@ __global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       issue(s + M::kStages - 1);
-      const char *st = lds + (s % M::kStages) * M::kStageBytes;
+      const char *st = ring + (s % M::kStages) * M::kStageBytes;
       auto frag = [&](int row, int c) {
         const int r = row + fr;
         return *(const i32x4_t *)(st + r * 128 + (((4 * c + fq) ^ ((r >> 1) & 7)) << 4));
@@ -202,8 +224,9 @@ __global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu
         acc[1][i] = Op::mma(b[1][1], a1, acc[1][i]);
       }
     }
+    if constexpr (PARTS == 2) add_parts<2 * M::kBlocks>(lds, part, wave, lane, &acc[0][0]);
     const int c = wn * 16 + fq * 4;
-    const bool in0 = c < left, in1 = EPI == EPI_PLAIN ? c + M::kColsHalf < left : in0;
+    const bool in0 = c < left && part == 0, in1 = EPI == EPI_PLAIN ? c + M::kColsHalf < left : in0;
     if (in0) {
       const ColumnTerms<IN, EL> t0 = column_terms<IN, EL, EPI>(p, g, col0 + c);
       const ColumnTerms<IN, EL> t1 = column_terms<IN, EL, EPI>(p, g, in1 ? second + c : col0 + c);
@@ -233,17 +256,17 @@ __global__ __launch_bounds__((MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu
   }
 }
 
-template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS>
+template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS, int PARTS = 1>
 inline hipError_t launch_glu_mid(const GluParams &p, bool once, hipStream_t s) {
   using M = MidTile<ROWS, WEIGHT_ROWS>;
   constexpr int kCols = EPI == EPI_PLAIN ? 2 * M::kColsHalf : M::kColsHalf;
   const int64_t groups = p.T < p.G ? p.T : p.G;
   const int64_t items = ((p.T + ROWS - 1) / ROWS + groups) * ((p.F + kCols - 1) / kCols);
-  const dim3 grid((unsigned)(items < 8192 ? items : 8192)), block(M::kThreads);
+  const dim3 grid((unsigned)(items < 8192 ? items : 8192)), block(PARTS * M::kThreads);
   if (once)
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, true, PARTS>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, false, PARTS>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

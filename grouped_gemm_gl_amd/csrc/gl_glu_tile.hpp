@@ -593,36 +593,43 @@ inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged,
 //   fp32, 64 x 64 / 32 x 64: up to 896 tiles of 32, for which 768 are under way at once: 8 of 600, K 2048 F 1024
 //     (864) 71 / 60, but 4 of 333, K 1024 F 2048 (960) 37 / 41.  64 of 64, K 1024 F 512 39 / 34; one of 256,
 //     K 4096 F 4096 (1152) 137 / 165.
+//   The contraction in one / two parts, by tiles of 32 x 64: 16 bits (on 32 x 32) 216 (8 of 64 groups, 8 rows, K 2048
+//     F 768) 11.2 / 10.4, 96 (one of 64, K 2048 F 1024) 9.1 / 7.7, 256 (2 of 64, K 4096 F 2048) 16.0 / 17.5;  8-bit
+//     integers 128 (one of 32, K 4096 N 4096) 11.1 / 8.6, 320 (8 of 64, K 2048 N 2048) 7.9 / 7.1, 1056 (64 of 32, K 1408
+//     N 2048) 13.5 / 19.3;  fp32 320 (8 of 40, K 2048 F 1024) 35 / 26, 544 (one of 512, K 1024 F 1024) 24.6 / 28.0.
+//     Weights of so few tiles are past the cache only where K is very long: they are not marked as read once.
 // Weights of more than the 256 MB of the last-level cache that about one row tile of each group reads
 // are loaded as data that is read once: 64 groups, 4099 rows, K 2048 F 1400, fp16 (734 MB of weights),
 // tiles of 128 180 -> 172; with it 8-bit integers of F 1408 take 84 on tiles of 256, 95 on those of 128.
 // Smaller ones lose what the cache holds from call to call (8 of 64 groups of 6 MB: 14.3 -> 16.5), and
 // weights that more row tiles read lose it within the call (8 groups, 2048 rows, K 4096 F 7168 int8
 // 89 -> 103).
-// And at most 16 rows with few columns, by tiles of 64 weight rows (us; the contraction split / tiles of 32 rows):
-//   16 bits: 64 (4 groups of 8 rows, K 1024 F 512) 6.4 / 6.5, 256 (one of 16, K 4096 F 4096, 128) 14.8 / 15.4,
-//     192 (8 of 64, 8 rows, K 2048 F 768) 13.6 / 11.3;  8 bits: 128 (one of 16, K 4096 N 8192) 9.6 / 11.3,
-//     256 (4 of 16, K 2048 N 4096) 9.0 / 7.8.
-//   fp32: 192 (8 of 8, K 2048 F 768) 15.5 / 29, 256 (16 of 64, K 1024 F 512) 14.4 / 17.8, 512 (8 of 8, K 2048
-//     F 2048) 36.6 / 30.6.
+// And fp32, at most 16 rows with few columns, by tiles of 64 weight rows (us; the contraction split over waves /
+// tiles of 32 rows): 64 (4 groups, 8 rows, K 1024 F 512) 9.1 / 13.6, 192 (8 of 8, K 2048 F 768) 15.5 / 24.5, 256
+// (16 of 64, K 1024 F 512) 14.4 / 16.1, 512 (8 of 8, K 2048 F 2048) 36.6 / 30.6.
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
   const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
   constexpr int64_t kWide = EPI == EPI_PLAIN ? 1 : 2;  // weight rows a column
   auto tiles = [&](int64_t r) { return ((p.T + r - 1) / r + groups) * ((kWide * p.F + r - 1) / r); };
-  if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= (IN == IN_F32 ? 256 : 128)) return launch_glu_few<IN, EL, EPI>(p, s);
+  if constexpr (IN == IN_F32)
+    if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= 256) return launch_glu_few<EPI>(p, s);
   const bool once = rows <= 96 && groups * kWide * p.F * p.K * in_bytes(IN) > kLastLevelCache;
   const bool large = IN == IN_F32  ? tiles(256) >= 2048
                      : IN == IN_I8 ? tiles(256) >= 160 && (rows > 96 || (rows > 24 && once))
                                    : tiles(256) >= 160 && rows > 96;
   if (!large) {
+    const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((kWide * p.F + 63) / 64);
     if constexpr (IN == IN_F32) {
-      const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((kWide * p.F + 63) / 64);
+      if (tiles32 <= 384) return launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s);
       if (rows <= 32 || tiles32 <= 896) return launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
       return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
     } else {
       if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128, 128>(p, once, s);
-      if constexpr (IN == IN_I8) return launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
+      if constexpr (IN == IN_I8)
+        return tiles32 <= 384 ? launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s)
+                              : launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
+      else if (tiles32 <= 224) return launch_glu_mid<IN, EL, EPI, 32, 32, 2>(p, false, s);
       else if (rows <= 8 || tiles(64) <= 256) return launch_glu_mid<IN, EL, EPI, 32, 32>(p, once, s);
       else return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
     }
