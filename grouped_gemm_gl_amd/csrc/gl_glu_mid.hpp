@@ -10,7 +10,7 @@
 // by 16 columns of either half, so h_g and h_u are in the same lane.
 //
 // Bound by the weights' bytes in flight: 64 groups, 4099 rows, K 2048 F 1400, fp16, 172 us for 734 MB
-// (4.3 TB/s, tiles of 128); 32 of 64 rows, K 1408 N 2048, int8, 14.2 us for 73 MB (5.1 TB/s, 32 by 64).  A
+// (4.3 TB/s, tiles of 128); 32 of 64 rows, K 1408 N 2048, int8, 13.6 us for 73 MB (5.4 TB/s, 32 by 64).  A
 // ring of five stages was slower, of three (fp32, three workgroups a CU) 5% slower at 333 rows and up to 7%
 // faster at more.
 #pragma once
