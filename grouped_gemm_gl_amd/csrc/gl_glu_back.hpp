@@ -4,11 +4,10 @@
 //
 // Both are out[i][j] = sum_p A(i, p) B(p, j) with j contiguous in B and out; A is dh, contiguous in
 // p for dx and in i for dW.  Tiles of TI x TJ outputs: 64 x 64 (4 waves, two workgroups a CU), dx also
-// 32 x 64 (4 waves, three; or with the contraction in two parts 8, one), or 128 x 128 (8 waves); stages of the contraction (64 values of 16 bits, 32 of
-// 32) go straight to a ring of STAGES in LDS, STAGES - 1 ahead, one barrier a stage (as in
-// glu_mid_kernel).  An operand whose tile
-// index is contiguous is staged as it lies, contraction row after contraction row, and turned on
-// the way out of LDS: 16-bit values by the transposing read, which hands a lane 4 contraction values
+// 32 x 64 (4 waves, three; or with the contraction in two parts 8, one), or 128 x 128 (8 waves);
+// stages of the contraction (64 values of 16 bits, 32 of 32) go straight to a ring of STAGES in LDS,
+// STAGES - 1 ahead, one barrier a stage (as in glu_mid_kernel).  An operand whose tile index is
+// contiguous is staged as it lies, contraction row after contraction row, and turned on the way out of LDS: 16-bit values by the transposing read, which hands a lane 4 contraction values
 // of one column, 32-bit ones by single-word reads.  16-byte slots are permuted by the row so that
 // the rows a read touches lie in different banks.
 //

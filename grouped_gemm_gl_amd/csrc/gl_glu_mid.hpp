@@ -1,7 +1,8 @@
 // Grouped products with a gated or scaled epilogue on small tiles, where 256-row tiles would be
 // too few to fill the chip: 32 rows by 32 weight rows (2 waves, five workgroups a CU) or by 64 (4
-// waves, three), either also with the contraction in two parts (twice the waves and LDS), 64 by 64 (4 waves, two) or 128 by 128 (8 waves, one), half of the weight rows the gate's and half the other's of the same columns
-// (plain: neighbouring columns).
+// waves, three), either also with the contraction in two parts (twice the waves and LDS), 64 by 64
+// (4 waves, two) or 128 by 128 (8 waves, one); half of the weight rows the gate's and half the
+// other's of the same columns (plain: neighbouring columns).
 //
 // Stages of 128 bytes of every row go straight to a ring of kStages in LDS, kStages - 1 ahead, and
 // one barrier a stage does for both sides: after it every wave's loads of the stage are there,
@@ -263,10 +264,13 @@ inline hipError_t launch_glu_mid(const GluParams &p, bool once, hipStream_t s) {
   const int64_t groups = p.T < p.G ? p.T : p.G;
   const int64_t items = ((p.T + ROWS - 1) / ROWS + groups) * ((p.F + kCols - 1) / kCols);
   const dim3 grid((unsigned)(items < 8192 ? items : 8192)), block(PARTS * M::kThreads);
-  if (once)
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, true, PARTS>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, false, PARTS>), grid, block, 0, s, p);
+  if constexpr (PARTS == 1) {  // (in two parts the weights are few)
+    if (once) {
+      hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, true, PARTS>), grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((glu_mid_kernel<IN, EL, EPI, ROWS, WEIGHT_ROWS, false, PARTS>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

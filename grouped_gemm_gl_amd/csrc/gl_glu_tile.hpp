@@ -578,6 +578,8 @@ inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged,
 // Measured (us; 64 / 128 / 256 rows):
 //   by rows a group, K 4096 F 7168, 8 groups, bf16:    16 rows 183 / 195 / 196   32 rows 217 / 189 / 208
 //                                                     128 rows 418 / 250 / 254  512 rows 1350 / 656 / 444
+//     (128 rows from 24 on: int8, small / 128: 64 of 1600, K 1408 N 2048 36.7 / 40.2, 64 of 4096 55 / 48.7, 4 of 130,
+//     K 4096 N 14336 49 / 40; bf16 64 of 1600, K 2048 F 768 81 / 89, 8 of 256, K 4096 F 4096 134 / 105)
 //   by tiles, one group, K 4096 F 4096: 512 rows (96 tiles of 256) 66 / 39 / 70   1024 (160) 130 / 76 / 71
 //     K 1024 F 1024: 512 rows (80 tiles of 128, 24 of 256) 8.8 / 12.8 / 23        2048 (272, 72) 19 / 15 / 25
 //   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
@@ -634,7 +636,8 @@ inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
       else return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
     }
   }
-  const int ragged = once ? kRaggedOnce : rows <= 256 ? kRaggedTiles : kFullTiles;  // 8 groups of 256 rows: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
+  // 8 groups of 256 rows, K 4096 F 7168: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
+  const int ragged = once ? kRaggedOnce : rows <= 256 ? kRaggedTiles : kFullTiles;
   if constexpr (EPI != EPI_PLAIN) {
     if (p.act == ACT_GELU) return launch_glu_tile<IN, EL, EPI, ACT_GELU>(p, tiles(256), ragged, s);
     if (p.act == ACT_GELU_TANH) return launch_glu_tile<IN, EL, EPI, ACT_GELU_TANH>(p, tiles(256), ragged, s);
