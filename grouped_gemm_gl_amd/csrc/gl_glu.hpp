@@ -33,7 +33,8 @@ template <bool SLOPE, int ACT>
 __device__ __forceinline__ float activate(float v, float &slope) {
   auto times = [](float v, float p) { return p == 0.f ? 0.f : v * p; };
   if constexpr (ACT == ACT_GELU) {
-    const float p = 0.5f + 0.5f * erff(v * 0.70710678118654752f);
+    // Phi by erfc: 1 + erf cancels where v is negative (4% off at -5, 0 from -5.6 on)
+    const float p = 0.5f * erfcf(v * -0.70710678118654752f);
     if (SLOPE) slope = p + times(v, 0.3989422804014327f * __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f));
     return times(v, p);
   } else if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)

@@ -6,7 +6,7 @@ from __future__ import annotations
 import math
 
 import numpy as np
-from scipy.special import erf as _erf
+from scipy.special import erfc as _erfc
 
 ACTS = ("silu", "gelu", "gelu_tanh")
 
@@ -16,12 +16,17 @@ def _sigmoid(v):
         return 1.0 / (1.0 + np.exp(-v))
 
 
+def _phi(v):
+    """The normal distribution (by erfc: 1 + erf cancels where v is negative)."""
+    return 0.5 * _erfc(-v / math.sqrt(2.0))
+
+
 def act(name, v):
     v = np.asarray(v, np.float64)
     if name == "silu":
         return v * _sigmoid(v)
     if name == "gelu":
-        return 0.5 * v * (1.0 + _erf(v / math.sqrt(2.0)))
+        return v * _phi(v)
     return 0.5 * v * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (v + 0.044715 * v ** 3)))
 
 
@@ -32,7 +37,7 @@ def slope(name, v):
         s = _sigmoid(v)
         return s * (1.0 + v * (1.0 - s))
     if name == "gelu":
-        return 0.5 * (1.0 + _erf(v / math.sqrt(2.0))) + v * np.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
+        return _phi(v) + v * np.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
     c = math.sqrt(2.0 / math.pi)
     t = np.tanh(c * (v + 0.044715 * v ** 3))
     return 0.5 * (1.0 + t) + 0.5 * v * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * v * v)
