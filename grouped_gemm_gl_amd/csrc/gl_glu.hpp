@@ -26,6 +26,25 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
 }
 
+// Phi(v), the normal distribution, given e = exp(-v^2 / 2): for v < 0 it is e t P(t) with
+// t = 1 / (1 + 0.35 |v|), and 1 - Phi(-v) for the others.  P, of degree 8, is the least relative error's
+// for v down to -13.5, where e leaves fp32 (3e-8; in fp32 arithmetic 3e-7 without e's own).  0.5 + 0.5
+// erf(v / sqrt 2) cancels where v is negative: 4% off at -5, 0 from -5.6 on.
+__device__ __forceinline__ float normal_cdf(float v, float e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35f, 1.f));
+  float p = -0.02912587672472f;
+  p = fmaf(p, t, 0.143872290849686f);
+  p = fmaf(p, t, -0.255504667758942f);
+  p = fmaf(p, t, 0.158929407596588f);
+  p = fmaf(p, t, -0.0229372195899487f);
+  p = fmaf(p, t, 0.105432972311974f);
+  p = fmaf(p, t, 0.119852431118488f);
+  p = fmaf(p, t, 0.139859080314636f);
+  p = fmaf(p, t, 0.139621570706368f);
+  const float q = p * t * e;
+  return v < 0.f ? q : 1.f - q;
+}
+
 // act(v) = v p, and with SLOPE act'(v) = p + v p'.  Infinities get the limits (0 and slope 0, or
 // v and slope 1) and NaN stays NaN: where p or p' is 0 in fp32, so is its product with v, an
 // infinite v's too.
@@ -33,9 +52,9 @@ template <bool SLOPE, int ACT>
 __device__ __forceinline__ float activate(float v, float &slope) {
   auto times = [](float v, float p) { return p == 0.f ? 0.f : v * p; };
   if constexpr (ACT == ACT_GELU) {
-    // Phi by erfc: 1 + erf cancels where v is negative (4% off at -5, 0 from -5.6 on)
-    const float p = 0.5f * erfcf(v * -0.70710678118654752f);
-    if (SLOPE) slope = p + times(v, 0.3989422804014327f * __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f));
+    const float e = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);  // exp(-v^2 / 2)
+    const float p = normal_cdf(v, e);
+    if (SLOPE) slope = p + times(v, 0.3989422804014327f * e);
     return times(v, p);
   } else if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh(z / 2)) / 2 is sigmoid(z)
     // each step with one literal: two would hold a register each

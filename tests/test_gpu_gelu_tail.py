@@ -1,11 +1,12 @@
 """GELU's negative tail in the gated layer: v Phi(v) and its slope relative to their own size, for gates
 from -9 to -3, where Phi is 1e-19 to 1e-3.
 
-Tolerances, with t = 2^-23.  Phi's argument is v times a constant, both rounded, so off by t
-relative; Phi's relative change is at most (v^2 + 1) times its argument's (the normal density
-over Phi is at most |v| + 1 / |v|); erfc itself is within 16 t.  The density's exponent v^2 / 2 is
-off by at most 3 roundings, 0.75 v^2 t, exp2 and the factors by 4 t.  Two or three products by exact
-values follow.  Together (v^2 + 21) t of Phi + |v| density, and the output's own rounding."""
+Tolerances, with t = 2^-23.  If Phi comes from erfc: its argument is v times a constant, both rounded, so
+off by t relative, Phi's relative change is at most v^2 + 1 times that (the normal density over Phi
+is at most |v| + 1 / |v|), and erfc itself is within 16 t.  If it comes from exp(-v^2 / 2) times a
+polynomial of 1 / (1 + c |v|): the exponent is off by at most 3 roundings, 0.75 v^2 t, exp2, the
+reciprocal and the polynomial by 6 t.  The density likewise.  Two or three products by exact
+values follow.  Either way at most (v^2 + 21) t of Phi + |v| density, and the output's own rounding."""
 import numpy as np
 import pytest
 import torch
