@@ -254,14 +254,25 @@ __device__ __forceinline__ ColumnTerms<IN, EL> column_terms(const GluParams &p, 
   return c;
 }
 
+// A row's scale as scale and after, whose product it is: (sum scale) channel after leaves fp32's range
+// only where the whole product does (a sum is 0 or of 1 .. 2^31, so only scales past 2^96 overflow with
+// it, and those leave 2^64 for the end).  The two scales' own product may leave it earlier, and 0 times
+// an infinity is NaN.  The last factor is a power of two, exact, in the addition of the bias.
+struct RowScale {
+  float scale, after;
+  __device__ __forceinline__ explicit RowScale(float s = 0.f)
+      : scale(fabsf(s) > 0x1p96f ? s * 0x1p-64f : s), after(fabsf(s) > 0x1p96f ? 0x1p64f : 1.f) {}
+};
+
 template <int IN, int EL>
-__device__ __forceinline__ float4 finish(typename Operand<IN>::acc_t s, float row_scale, const ColumnTerms<IN, EL> &c) {
+__device__ __forceinline__ float4 finish(typename Operand<IN>::acc_t s, const RowScale &r, const ColumnTerms<IN, EL> &c) {
   const float4 b = Quad<EL>::value(c.bias);
-  if constexpr (IN == IN_I8)
-    return make_float4((float)s[0] * (row_scale * c.scale[0]) + b.x, (float)s[1] * (row_scale * c.scale[1]) + b.y,
-                       (float)s[2] * (row_scale * c.scale[2]) + b.z, (float)s[3] * (row_scale * c.scale[3]) + b.w);
-  else
+  if constexpr (IN == IN_I8) {
+    auto one = [&](int i, float bias) { return fmaf((float)s[i] * r.scale * c.scale[i], r.after, bias); };
+    return make_float4(one(0, b.x), one(1, b.y), one(2, b.z), one(3, b.w));
+  } else {
     return make_float4(s[0] + b.x, s[1] + b.y, s[2] + b.z, s[3] + b.w);
+  }
 }
 
 template <bool SLOPE, int ACT>

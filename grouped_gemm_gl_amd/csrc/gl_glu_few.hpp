@@ -124,8 +124,8 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
       const int64_t row = row0 + r;
       const int c = 4 * q;
       if (c < cols) {
-        const float4 v0 = finish<IN, EL>(acc[0], 0.f, column_terms<IN, EL, EPI>(p, g, col0 + c));
-        const float4 v1 = finish<IN, EL>(acc[1], 0.f, column_terms<IN, EL, EPI>(p, g, second + c));
+        const float4 v0 = finish<IN, EL>(acc[0], RowScale(), column_terms<IN, EL, EPI>(p, g, col0 + c));
+        const float4 v1 = finish<IN, EL>(acc[1], RowScale(), column_terms<IN, EL, EPI>(p, g, second + c));
         with_activation(p.act, [&](auto act) { gated4<EL, EPI, decltype(act)::value>(p, row, col0 + c, v0, v1); });
       }
     }

@@ -237,7 +237,7 @@ __global__ __launch_bounds__((PARTS * MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) 
           const int rl = i * 32 + wm * 16 + fr;
           if (rl >= rows) break;
           const int64_t row = row0 + rl;
-          const float rs = IN == IN_I8 ? p.x_scale[row] : 0.f;
+          const RowScale rs(IN == IN_I8 ? p.x_scale[row] : 0.f);
           const float4 v0 = finish<IN, EL>(acc[0][i], rs, t0), v1 = finish<IN, EL>(acc[1][i], rs, t1);
           if constexpr (EPI == EPI_PLAIN) {
             put4<EL>(p.out, row * p.F + col0 + c, v0);

@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     const int width1 = kGated ? width : (int)min64(kHalf, p.F - col0 - kHalf);
     const int64_t second = kGated ? p.F + col0 : col0 + kHalf;  // the second set's first column
     ColumnTerms<IN, EL> ct[2][4];
-    float rs[2][2];
+    RowScale rs[2][2];
     if constexpr (!kTurnB) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          rs[a][i] = IN == IN_I8 ? p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, max(t.rows, 1) - 1)] : 0.f;
+          if (IN == IN_I8) rs[a][i] = RowScale(p.x_scale[t.row0 + min(a * kHalf + i * 64 + wm * 16 + er, max(t.rows, 1) - 1)]);
     }
     // dW is the group's own matrix; with accumulate, a group without rows is not touched
     void *const out = EPI == EPI_DW ? p.out ? (char *)p.out + (int64_t)t.g * p.N * p.F * elem_bytes(EL) : p.out_ptrs[t.g] : p.out;

@@ -469,7 +469,8 @@ int gl_quantize_int8(int64_t rows, int64_t cols, gl_dtype dtype, const void *src
  * and gl_glu_forward_int8: the same h [T, 2F] through the gate, a = act(h[:, :F]) * h[:, F:].
  *   x int8 [T, K], x_scale float [T]; w / w_ptrs int8 [G, N, K] or G x [N, K] (N = 2F, the
  *                gate's rows first), w_scale / w_scale_ptrs float [G, N] or G x [N], in the
- *                weights' form; codes may take the whole of [-128, 127], scales any value
+ *                weights' form; codes may take the whole of [-128, 127], scales any value (y leaves fp32's
+ *                range only where the formula does, and a sum of 0 under finite scales stays 0)
  *   out_dtype    GL_F32, GL_BF16 or GL_F16 for y / a and the bias / bias_ptrs (or none)
  *   y [y_rows, N] / a [a_rows, F], at least T rows: rows >= T are never written
  * The sums are exact in int32; from there on fp32, one rounding at the end.  K a multiple of 16
