@@ -115,6 +115,7 @@ __global__ __launch_bounds__((PARTS * MidTile<TI, TJ>::kThreads), 2) void glu_ba
       for (int i = 0; i < M::kBlocks; ++i) acc[h][i] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < M::kStages - 1; ++s) issue(s);
+    ChunkSums<IN, 2 * M::kBlocks> sums;
     for (int s = 0; s < nk; ++s) {
       __builtin_amdgcn_sched_barrier(0);
       gemm::wait_vm<(M::kStages - 2) * M::kPieces>();
@@ -154,7 +155,9 @@ __global__ __launch_bounds__((PARTS * MidTile<TI, TJ>::kThreads), 2) void glu_ba
           acc[1][i] = Op::mma(fb[1][c], fa[i][c], acc[1][i]);
         }
       }
+      sums.step(s, kFp32Chain / 32, &acc[0][0]);
     }
+    sums.end(&acc[0][0]);
     if constexpr (PARTS == 2) add_parts<2 * M::kBlocks>(lds, part, wave, lane, &acc[0][0]);
     void *out = WGRAD && !p.out ? p.out_ptrs[g] : p.out;
     const int64_t out0 = WGRAD ? (p.out ? (int64_t)g * p.N * p.K : 0) + i0 * p.K : (g_off + i0) * p.K;

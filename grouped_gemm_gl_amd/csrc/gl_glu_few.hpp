@@ -107,12 +107,15 @@ __global__ __launch_bounds__(kFewThreads) void glu_few_kernel(GluParams p) {
     uint32_t at = wave * 128;
     load(u0, at);
     load(u1, at + step);
-    for (; at < kb; at += 2 * step) {
+    ChunkSums<IN, 2> sums;
+    for (int n = 0; at < kb; at += 2 * step, ++n) {
       multiply(u0);
       load(u0, at + 2 * step);
       multiply(u1);
       load(u1, at + 3 * step);
+      sums.step(n, kFp32Chain / 64, acc);
     }
+    sums.end(acc);
     part[wave][0][lane] = acc[0];
     part[wave][1][lane] = acc[1];
     __syncthreads();

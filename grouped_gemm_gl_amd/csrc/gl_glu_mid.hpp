@@ -199,6 +199,7 @@ __global__ __launch_bounds__((PARTS * MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) 
       for (int i = 0; i < M::kBlocks; ++i) acc[h][i] = acc_t{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < M::kStages - 1; ++s) issue(s);
+    ChunkSums<IN, 2 * M::kBlocks> sums;
     for (int s = 0; s < nk; ++s) {
       __builtin_amdgcn_sched_barrier(0);
       gemm::wait_vm<(M::kStages - 2) * M::kPieces>();
@@ -224,7 +225,9 @@ __global__ __launch_bounds__((PARTS * MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) 
         acc[0][i] = Op::mma(b[0][1], a1, acc[0][i]);
         acc[1][i] = Op::mma(b[1][1], a1, acc[1][i]);
       }
+      sums.step(s, kFp32Chain / 32, &acc[0][0]);
     }
+    sums.end(&acc[0][0]);
     if constexpr (PARTS == 2) add_parts<2 * M::kBlocks>(lds, part, wave, lane, &acc[0][0]);
     const int c = wn * 16 + fq * 4;
     const bool in0 = c < left && part == 0, in1 = EPI == EPI_PLAIN ? c + M::kColsHalf < left : in0;

@@ -420,7 +420,8 @@ int gl_grouped_mlp_backward(int num_groups, int64_t in_features, int64_t ffn_fea
  * Sums, activation and product are fp32 (a is not computed from the rounded h, as
  * gl_swiglu_forward would); h and a are each rounded once.  K and F multiples of 8 (16-bit) or 4
  * (fp32), K and 2F at most 2^20; every tensor, each group's too, 16-byte aligned.  fp32 products
- * run on the matrix cores and differ from gl_forward's in the last bits.  The workspace is the
+ * run on the matrix cores and differ from gl_forward's in the last bits (chains of 256 values and then
+ * their sums; from about 2048 tiles of 256 rows on one chain each).  The workspace is the
  * one of gl_offsets; h and a do not overlap any other buffer.
  */
 enum { GL_GLU_SILU = 0, GL_GLU_GELU = 1, GL_GLU_GELU_TANH = 2 };
