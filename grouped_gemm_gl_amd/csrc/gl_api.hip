@@ -755,6 +755,7 @@ int int8_impl(const char *who, bool gated, int G, int64_t K, int64_t F, int64_t 
   GL_TRY(check_buf(y, T, gated ? "a" : "y"));
   if (T == 0) return ok();
   if (!x_scale || ((uintptr_t)x_scale & 3u)) return fail(GL_ERR_ARG, "%s: x_scale NULL or not 4-byte aligned", who);
+  if (y == (const void *)x) return fail(GL_ERR_ARG, "%s: the output must not be x", who);
   gl::GluParams p{};
   p.x = (const char *)x; p.w = (const char *)w; p.w_ptrs = (const char *const *)w_ptrs;
   p.bias = bias; p.bias_ptrs = bias_ptrs;
@@ -784,6 +785,7 @@ int gl_glu_forward(int num_groups, int64_t in_features, int64_t ffn_features, in
   if (h) GL_TRY(check_buf(h, T, "h"));
   if (T == 0) return ok();
   if (h == a) return fail(GL_ERR_ARG, "%s: h and a must be different buffers", who);
+  if (a == x || h == x) return fail(GL_ERR_ARG, "%s: neither h nor a may be x", who);
   gl::GluParams p{};
   p.x = (const char *)x; p.w = (const char *)w; p.w_ptrs = (const char *const *)w_ptrs;
   p.bias = bias; p.bias_ptrs = bias_ptrs; p.out = a; p.h = h;
@@ -810,8 +812,10 @@ int gl_glu_backward(int num_groups, int64_t in_features, int64_t ffn_features, i
   GL_TRY(check_buf(da, T, "da"));
   GL_TRY(check_buf(dh, T, "dh"));
   if (a) GL_TRY(check_buf(a, T, "a"));
-  if (T > 0 && (a == dh || (a && a == da))) return fail(GL_ERR_ARG, "%s: a must be a buffer of its own", who);
-  if (T > 0 && dh == da) return fail(GL_ERR_ARG, "%s: dh must not be da", who);
+  // (dx in x's, h's or da's place: those are read no more when dx is written)
+  if (T > 0 && a && (a == dh || a == da || a == h || a == x || a == dx))
+    return fail(GL_ERR_ARG, "%s: a must be a buffer of its own", who);
+  if (T > 0 && (dh == da || dh == x || dh == dx)) return fail(GL_ERR_ARG, "%s: dh must not be da, x or dx", who);
   gl::BackParams bp{};
   bp.a = (const char *)dh; bp.b = (const char *)w; bp.b_ptrs = (const char *const *)w_ptrs; bp.x = (const char *)x;
   bp.ws = workspace; bp.G = G; bp.T = T; bp.K = K; bp.N = 2 * F;
