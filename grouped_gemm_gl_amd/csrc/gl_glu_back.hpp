@@ -65,7 +65,7 @@ __global__ __launch_bounds__((PARTS * MidTile<TI, TJ>::kThreads), 2) void glu_ba
     const int64_t i0 = (int64_t)it * TI, j0 = (int64_t)jt * TJ;
     const int64_t contr = WGRAD ? g_rows : p.N;  // values of the contraction
     const int rows = (int)min64(TI, (WGRAD ? p.N : g_rows) - i0), cols = (int)min64(TJ, p.K - j0);
-    if (!device_check(rows > 0 && cols > 0 && g_off >= 0 && g_off + g_rows <= p.T, p.ws)) continue;
+    if (!device_check(rows > 0 && cols > 0 && g_off >= 0 && g_rows >= 0 && g_off + g_rows <= p.T, p.ws)) continue;
     const char *a = WGRAD ? p.a + g_off * nbytes + i0 * E : p.a + (g_off + i0) * nbytes;
     const char *b = WGRAD ? p.x + g_off * kbytes
                           : p.b ? p.b + (int64_t)g * p.N * kbytes : p.b_ptrs[g];

@@ -219,7 +219,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
       e.w = 0;
       good = mt > 0 && local >= 0 && it < mt && jt < tiles_j && rows > 0 && r0 >= 0 && r0 + rows <= p.T;
     }
-    if (GL_DEVICE_CHECKS && !device_check(good, p.ws)) e = make_int4(0, 0, 0, 0);  // a first tile without rows: nothing stored
+    // a failed check: a tile without rows, of which nothing is stored; dW's has the matrix's rows, and -1 of the
+    // contraction says so
+    if (GL_DEVICE_CHECKS && !device_check(good, p.ws)) e = make_int4(0, 0, 0, EPI == EPI_DW ? -1 : 0);
     places[lane] = e;
     TileStore<EL>::order();
   };
@@ -487,7 +489,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) 
     }
     // dW is the group's own matrix; with accumulate, a group without rows is not touched
     void *const out = EPI == EPI_DW ? p.out ? (char *)p.out + (int64_t)t.g * p.N * p.F * elem_bytes(EL) : p.out_ptrs[t.g] : p.out;
-    const bool untouched = EPI == EPI_DW && p.accumulate && t.len == 0;
+    const bool untouched = EPI == EPI_DW && ((p.accumulate && t.len == 0) || (GL_DEVICE_CHECKS && t.len < 0));
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
