@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "gl_gemm_tile.hpp"
+#include "gl_glu_choice.hpp"
 #include "gl_vec.hpp"
 
 namespace gl {
@@ -84,8 +85,7 @@ __device__ __forceinline__ void with_activation(int act, F f) {
 // Lane l holds bytes of row l % 16 of either operand, the quarters l / 16 of the wave holding
 // different contraction values, the same in both; the sum comes as four consecutive rows of
 // the first operand, 4 (l / 16) .., of column l % 16, a row of the second.
-enum { IN_BF16 = 0, IN_F32 = 1, IN_F16 = 2, IN_I8 = 3 };
-constexpr int in_bytes(int in) { return in == IN_F32 ? 4 : in == IN_I8 ? 1 : 2; }
+// (IN_BF16 .. IN_I8: gl_glu_choice.hpp)
 
 template <int IN>
 struct Operand {

@@ -197,68 +197,40 @@ inline hipError_t launch_glu_back_tile(const BackParams &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tiles.  fp32: dW those of 64 (of 128 up to twice as slow, at most a tenth faster) with a ring of
-// three, three workgroups a CU, because a group's rows are few stages (4 groups, 333 rows, K 1024 F 1024
-// 34.4 us with a ring of four, 30.3 of three; one of 4096 rows 167 and 169); dx 32 x 64 up to 896 of them, for
-// which 768 are under way at once (47 us on tiles of 64, 32 on these; one of 4096 rows, 2064 of them, 153 and
-// 165), up to 384 with the contraction in two parts (240: those 32 -> 27; 864: 66 -> 84).  (The grouped calls' fp32 kernel works on the vector units: both products 386 us, here 57.)
-// 16 bits, dx: up to 256 tiles of 32 x 64 those, in two parts (144: one group, 256 rows, K 1024 F 1024 13.3 us
-// on tiles of 64, 11.8 in one part, 9.7 in two; 544: 2 of 1024 rows 35.8 and 37.8 with dW), and else as
-// measured for bf16 (us; tiles of 64 / 128 / 256), (groups, rows, K, F):
-//   dx by tiles of 256:  16 (1, 256, 2048, 2048) 25 / 41 / 88     64 (4, 1024, 2048, 2048) 50 / 41 / 87
-//                       144 (2, 4096, 2048, 2048) 116 / 89 / 89  272 (1, 4096, 4096, 4096) 439 / 318 / 220
-//      and rows a group: 16 (64, 1024, 1024, 512) 36 / 34 / 27    64 (64, 4096, 2048, 768) 119 / 103 / 130
-//      by tiles of 128: 144 (16, 256, 1024, 512) 9.9 / 11.9      192 (4, 1024, 2048, 2048) 50 / 41
-//   dW by tiles of 256:  32 (1, 8192, 1024, 1024) 81 / 92 / 196  128 (1, 2048, 2048, 2048) 75 / 59 / 63
-//                       256 (16, 256, 1024, 512) 32 / 25 / 17   1024 (16, 1024, 2048, 1024) 107 / 87 / 44
-// What passes the last-level cache's 256 MB does not stay there: weights that one or two row tiles a group read
-// and weight gradients then go past it (64 groups, 4099 rows, K 2048 F 1400 fp16, 734 MB each: dx 211 -> 172,
-// dW 213 -> 185; 8 of 1024, K 4096 F 7168 dx 331 -> 282, dW 280 -> 262;
-// fp32, 8 of 16, K 4096 F 4096 dx 223 -> 156, dW 333 -> 298).  Smaller weight gradients are left
-// where their next reader finds them, though they too are written faster (1 of 512, K 2048 F 2048, 17 MB,
-// 27.4 -> 25.8).
+// The instances of choose_glu_back (gl_glu_choice.hpp).
 template <int IN, int EL>
 inline hipError_t launch_glu_back(const BackParams &p, bool wgrad, bool out_f32, hipStream_t s) {
-  const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
-  const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((p.K + 63) / 64);
+  const BackChoice c = choose_glu_back(IN, wgrad, out_f32, p.G, p.T, p.K, p.N);
   if constexpr (IN == IN_F32) {
     if (wgrad)
-      return p.G * p.N * p.K * 4 > kLastLevelCache ? launch_glu_back_tile<IN, EL, true, 64, 64, 3, true>(p, s)
-                                                   : launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
-    if (tiles32 <= 384) return launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s);
-    const bool once = rows <= 96 && groups * p.K * p.N * 4 > kLastLevelCache;
-    if (rows <= 32 || tiles32 <= 896)
-      return once ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, true>(p, s)
-                  : launch_glu_back_tile<IN, EL, false, 32, 64>(p, s);
-    return once ? launch_glu_back_tile<IN, EL, false, 64, 64, 4, true>(p, s)
-                : launch_glu_back_tile<IN, EL, false, 64>(p, s);
+      return c.once ? launch_glu_back_tile<IN, EL, true, 64, 64, 3, true>(p, s)
+                    : launch_glu_back_tile<IN, EL, true, 64, 64, 3>(p, s);
+    if (c.parts == 2) return launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s);
+    if (c.rows == 32)
+      return c.once ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, true>(p, s)
+                    : launch_glu_back_tile<IN, EL, false, 32, 64>(p, s);
+    return c.once ? launch_glu_back_tile<IN, EL, false, 64, 64, 4, true>(p, s)
+                  : launch_glu_back_tile<IN, EL, false, 64>(p, s);
   } else {
-    auto tiles = [&](int64_t r) {
-      return (wgrad ? groups * ((p.N + r - 1) / r) : (p.T + r - 1) / r + groups) * ((p.K + r - 1) / r);
-    };
     GluParams q{};
     q.x = p.a; q.ws = p.ws; q.G = p.G; q.T = p.T; q.F = p.K; q.out = p.out; q.out_ptrs = p.out_ptrs;
     if (!wgrad) {
-      const bool large = groups * p.K * p.N * in_bytes(IN) > kLastLevelCache;  // weights
-      if (tiles(256) >= 160 && (rows <= 24 || rows > 96)) {
+      if (c.rows == 256) {
         q.w = p.b; q.w_ptrs = p.b_ptrs; q.K = p.N;
-        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, tiles(256),
-                                                         rows > 256 ? kFullTiles : large ? kRaggedOnce : kRaggedTiles, s);
+        return launch_glu_tile<IN, EL, EPI_DX, ACT_SILU>(q, c.items, c.tiles, s);
       }
-      if (tiles(128) >= 192)
-        return large && rows <= 96 ? launch_glu_back_tile<IN, EL, false, 128, 128, 4, true>(p, s)
-                                   : launch_glu_back_tile<IN, EL, false, 128>(p, s);
-      return tiles32 <= 256 ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s)
-                            : launch_glu_back_tile<IN, EL, false, 64>(p, s);
+      if (c.rows == 128)
+        return c.once ? launch_glu_back_tile<IN, EL, false, 128, 128, 4, true>(p, s)
+                      : launch_glu_back_tile<IN, EL, false, 128>(p, s);
+      return c.rows == 32 ? launch_glu_back_tile<IN, EL, false, 32, 64, 4, false, 2>(p, s)
+                          : launch_glu_back_tile<IN, EL, false, 64>(p, s);
     }
-    if (tiles(256) >= 128) {
+    if (c.rows == 256) {
       q.w = p.x; q.N = p.N; q.accumulate = p.accumulate;
-      const int64_t items = (int64_t)p.G * ((p.N + 255) / 256) * ((p.K + 255) / 256);
-      const int stores = p.G * p.N * p.K * (out_f32 ? 4 : in_bytes(IN)) > kLastLevelCache ? kWrittenOnce : kFullTiles;
-      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, items, stores, s)
-                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, items, stores, s);
+      return out_f32 ? launch_glu_tile<IN, EL_F32, EPI_DW, ACT_SILU>(q, c.items, c.tiles, s)
+                     : launch_glu_tile<IN, EL, EPI_DW, ACT_SILU>(q, c.items, c.tiles, s);
     }
-    if (tiles(128) >= 192)
+    if (c.rows == 128)
       return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 128>(p, s) : launch_glu_back_tile<IN, EL, true, 128>(p, s);
     return out_f32 ? launch_glu_back_tile<IN, EL_F32, true, 64>(p, s) : launch_glu_back_tile<IN, EL, true, 64>(p, s);
   }

@@ -45,6 +45,7 @@
 #pragma once
 
 #include "gl_gemm_tile.hpp"
+#include "gl_glu_choice.hpp"
 #include "gl_glu_mid.hpp"
 
 namespace gl {
@@ -141,8 +142,6 @@ struct TilePlace {
 // RAGGED: row blocks past a tile's rows are neither read from LDS nor multiplied, which costs full
 // tiles a tenth of their speed in branches.  kRaggedOnce: and the weights are loaded as data that is
 // read once.  kWrittenOnce: full tiles whose outputs are stored as data that is not read soon.
-enum { kFullTiles = 0, kRaggedTiles = 1, kRaggedOnce = 2, kWrittenOnce = 3 };
-constexpr int64_t kLastLevelCache = (int64_t)256 << 20;
 template <int IN, int EL, int EPI, int ACT, int RAGGED>
 __global__ __launch_bounds__(kTileThreads, 2) void glu_tile_kernel(GluParams p) {
   using Op = Operand<IN>;
@@ -574,77 +573,32 @@ inline hipError_t launch_glu_tile(const GluParams &p, int64_t items, int ragged,
   return hipGetLastError();
 }
 
-// Which kernel, by the rows of a group that has any (on average: the splits are on the device) and
-// the most tiles there can be.  The tiles of 256 rows multiply at the rate of the matrix cores, those
-// of 128 and 64 are enough for the chip in smaller problems and waste less on groups of few rows.
-// Measured (us; 64 / 128 / 256 rows):
-//   by rows a group, K 4096 F 7168, 8 groups, bf16:    16 rows 183 / 195 / 196   32 rows 217 / 189 / 208
-//                                                     128 rows 418 / 250 / 254  512 rows 1350 / 656 / 444
-//     (128 rows from 24 on: int8, small / 128: 64 of 1600, K 1408 N 2048 36.7 / 40.2, 64 of 4096 55 / 48.7, 4 of 130,
-//     K 4096 N 14336 49 / 40; bf16 64 of 1600, K 2048 F 768 81 / 89, 8 of 256, K 4096 F 4096 134 / 105)
-//   by tiles, one group, K 4096 F 4096: 512 rows (96 tiles of 256) 66 / 39 / 70   1024 (160) 130 / 76 / 71
-//     K 1024 F 1024: 512 rows (80 tiles of 128, 24 of 256) 8.8 / 12.8 / 23        2048 (272, 72) 19 / 15 / 25
-//   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
-//     4 groups, 333 rows, K 1024 F 2048 37 / 69 / 216;  8 groups, 16384 rows, K 4096 F 7168
-//     (4032 tiles of 256) 16504 / 14747 / 14029
-// Among the small tiles (rows by weight rows; us):
-//   16 bits, 64 x 64 / 32 x 32: at most 256 tiles of 64: 2 groups, 64 rows, K 4096 F 2048 23.6 / 15.8, one of
-//     300, K 1024 F 1024 8.3 / 7.6 (at 1 of 128, K 4096 F 4096, 384 tiles, 23.2 / 25.8).  At most 8 rows
-//     a group: 64 of 256, K 4096 F 768 170 / 134, 8 of 16, K 4096 F 7168 156 / 136, but K 2048 72 / 76 and 81 / 84
-//     (64 of 1024, K 2048 F 768 76 / 86).
-//   8-bit integers, 64 x 64 / 32 x 64: 64 of 32 rows, K 1408 N 2048 16.1 / 13.5; 64 of 1024 37.8 / 34.4; one of
-//     512, K 2048 N 1024 8.6 / 7.7; one of 32, K 4096 N 4096 10.8 / 11.2.
-//   fp32, 64 x 64 / 32 x 64: up to 896 tiles of 32, for which 768 are under way at once: 8 of 600, K 2048 F 1024
-//     (864) 71 / 60, but 4 of 333, K 1024 F 2048 (960) 37 / 41.  64 of 64, K 1024 F 512 39 / 34; one of 256,
-//     K 4096 F 4096 (1152) 137 / 165.
-//   The contraction in one / two parts, by tiles of 32 x 64: 16 bits (on 32 x 32) 216 (8 of 64 groups, 8 rows, K 2048
-//     F 768) 11.2 / 10.4, 96 (one of 64, K 2048 F 1024) 9.1 / 7.7, 256 (2 of 64, K 4096 F 2048) 16.0 / 17.5;  8-bit
-//     integers 128 (one of 32, K 4096 N 4096) 11.1 / 8.6, 320 (8 of 64, K 2048 N 2048) 7.9 / 7.1, 1056 (64 of 32, K 1408
-//     N 2048) 13.5 / 19.3;  fp32 320 (8 of 40, K 2048 F 1024) 35 / 26, 544 (one of 512, K 1024 F 1024) 24.6 / 28.0.
-//     Weights of so few tiles are past the cache only where K is very long: they are not marked as read once.
-// Weights of more than the 256 MB of the last-level cache that about one row tile of each group reads
-// are loaded as data that is read once: 64 groups, 4099 rows, K 2048 F 1400, fp16 (734 MB of weights),
-// tiles of 128 180 -> 172; with it 8-bit integers of F 1408 take 84 on tiles of 256, 95 on those of 128.
-// Smaller ones lose what the cache holds from call to call (8 of 64 groups of 6 MB: 14.3 -> 16.5), and
-// weights that more row tiles read lose it within the call (8 groups, 2048 rows, K 4096 F 7168 int8
-// 89 -> 103).
-// And fp32, at most 16 rows with few columns, by tiles of 64 weight rows (us; the contraction split over waves /
-// tiles of 32 rows): 64 (4 groups, 8 rows, K 1024 F 512) 9.1 / 13.6, 192 (8 of 8, K 2048 F 768) 15.5 / 24.5, 256
-// (16 of 64, K 1024 F 512) 14.4 / 16.1, 512 (8 of 8, K 2048 F 2048) 36.6 / 30.6.
+// The instances of choose_glu (gl_glu_choice.hpp).
 template <int IN, int EL, int EPI>
 inline hipError_t launch_glu(const GluParams &p, hipStream_t s) {
-  const int64_t groups = p.T < p.G ? p.T : p.G, rows = p.T / groups;
-  constexpr int64_t kWide = EPI == EPI_PLAIN ? 1 : 2;  // weight rows a column
-  auto tiles = [&](int64_t r) { return ((p.T + r - 1) / r + groups) * ((kWide * p.F + r - 1) / r); };
+  const GluChoice c = choose_glu(IN, EPI == EPI_PLAIN, p.G, p.T, p.K, p.F);
   if constexpr (IN == IN_F32)
-    if (p.T <= 16 && groups * ((kWide * p.F + 63) / 64) <= 256) return launch_glu_few<EPI>(p, s);
-  const bool once = rows <= 96 && groups * kWide * p.F * p.K * in_bytes(IN) > kLastLevelCache;
-  const bool large = IN == IN_F32  ? tiles(256) >= 2048
-                     : IN == IN_I8 ? tiles(256) >= 160 && (rows > 96 || (rows > 24 && once))
-                                   : tiles(256) >= 160 && rows > 96;
-  if (!large) {
-    const int64_t tiles32 = ((p.T + 31) / 32 + groups) * ((kWide * p.F + 63) / 64);
+    if (c.kernel == GluChoice::kFew) return launch_glu_few<EPI>(p, s);
+  if (c.kernel == GluChoice::kMid) {
     if constexpr (IN == IN_F32) {
-      if (tiles32 <= 384) return launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s);
-      if (rows <= 32 || tiles32 <= 896) return launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
-      return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
+      if (c.parts == 2) return launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s);
+      return c.rows == 32 ? launch_glu_mid<IN, EL, EPI, 32, 64>(p, c.once, s)
+                          : launch_glu_mid<IN, EL, EPI, 64, 64>(p, c.once, s);
     } else {
-      if (rows > 24 && tiles(128) >= 256) return launch_glu_mid<IN, EL, EPI, 128, 128>(p, once, s);
+      if (c.rows == 128) return launch_glu_mid<IN, EL, EPI, 128, 128>(p, c.once, s);
       if constexpr (IN == IN_I8)
-        return tiles32 <= 384 ? launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s)
-                              : launch_glu_mid<IN, EL, EPI, 32, 64>(p, once, s);
-      else if (tiles32 <= 224) return launch_glu_mid<IN, EL, EPI, 32, 32, 2>(p, false, s);
-      else if (rows <= 8 || tiles(64) <= 256) return launch_glu_mid<IN, EL, EPI, 32, 32>(p, once, s);
-      else return launch_glu_mid<IN, EL, EPI, 64, 64>(p, once, s);
+        return c.parts == 2 ? launch_glu_mid<IN, EL, EPI, 32, 64, 2>(p, false, s)
+                            : launch_glu_mid<IN, EL, EPI, 32, 64>(p, c.once, s);
+      else if (c.parts == 2) return launch_glu_mid<IN, EL, EPI, 32, 32, 2>(p, false, s);
+      else if (c.rows == 32) return launch_glu_mid<IN, EL, EPI, 32, 32>(p, c.once, s);
+      else return launch_glu_mid<IN, EL, EPI, 64, 64>(p, c.once, s);
     }
   }
-  // 8 groups of 256 rows, K 4096 F 7168: 297 us skipping what is past the rows, 306 not; of 512: 472 and 460
-  const int ragged = once ? kRaggedOnce : rows <= 256 ? kRaggedTiles : kFullTiles;
   if constexpr (EPI != EPI_PLAIN) {
-    if (p.act == ACT_GELU) return launch_glu_tile<IN, EL, EPI, ACT_GELU>(p, tiles(256), ragged, s);
-    if (p.act == ACT_GELU_TANH) return launch_glu_tile<IN, EL, EPI, ACT_GELU_TANH>(p, tiles(256), ragged, s);
+    if (p.act == ACT_GELU) return launch_glu_tile<IN, EL, EPI, ACT_GELU>(p, c.items, c.ragged, s);
+    if (p.act == ACT_GELU_TANH) return launch_glu_tile<IN, EL, EPI, ACT_GELU_TANH>(p, c.items, c.ragged, s);
   }
-  return launch_glu_tile<IN, EL, EPI, ACT_SILU>(p, tiles(256), ragged, s);
+  return launch_glu_tile<IN, EL, EPI, ACT_SILU>(p, c.items, c.ragged, s);
 }
 
 }  // namespace gl

@@ -28,9 +28,15 @@ def new(*s):
     return torch.empty(*s, device=DEV)
 
 
-# the contraction over waves; in two parts; tiles of 32 by 64; of 64 by 64
-@pytest.mark.parametrize("T,K,F", [(8, 1 << 15, 64), (40, 1 << 14, 64), (100, 1 << 14, 4096), (300, 1 << 14, 4096)], ids=str)
-def test_forward(T, K, F):
+# kernel: T, K, F
+FORWARD = {"few": (8, 1 << 15, 64), "32x64 parts": (40, 1 << 14, 64), "32x64": (100, 1 << 14, 4096),
+           "64x64": (300, 1 << 14, 4096)}
+DX = {"32x64 parts": (40, 64, 1 << 13), "32x64": (100, 6400, 1 << 13), "64x64": (300, 5760, 1 << 13)}
+
+
+@pytest.mark.parametrize("kernel", FORWARD)
+def test_forward(kernel):
+    T, K, F = FORWARD[kernel]
     x, w, h = torch.full((T, K), 2.0 ** -14, device=DEV), torch.full((1, 2 * F, K), 2.0 ** -13, device=DEV), new(T, 2 * F)
     x[:, 0], w[:, :, 0] = 1, 1
     gl.gl_glu_forward(x, w, new(T, F), workspace(T), h=h)
@@ -39,10 +45,9 @@ def test_forward(T, K, F):
     assert off <= limit(K), off
 
 
-# dx in two parts; tiles of 32 by 64; of 64 by 64
-@pytest.mark.parametrize("T,K", [(40, 64), (100, 6400), (300, 5760)])
-def test_dx(T, K):
-    F = 1 << 13
+@pytest.mark.parametrize("kernel", DX)
+def test_dx(kernel):
+    T, K, F = DX[kernel]
     h = torch.full((T, 2 * F), 2.0 ** -13, device=DEV)  # the other half; dh of the gate's half is it times 1
     h[:, :F], h[:, F] = 30, 1  # SiLU's slope at 30 is 1
     w = torch.zeros(1, 2 * F, K, device=DEV)

@@ -17,7 +17,8 @@ from oracle import gated
 from test_gpu_glu import TYPES, check, half_step
 
 pytestmark = pytest.mark.gpu
-DEV = "cuda"
+DEV, K = "cuda", 64
+SIZES = [(1, 64), (70, 520), (1000, 4096)]  # in 16 bits the contraction in two parts, twice, and tiles of 256
 
 
 def gates(F, dtype):
@@ -39,10 +40,9 @@ def workspace(T):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,F", [(1, 64), (70, 520), (600, 4096)])
+@pytest.mark.parametrize("T,F", SIZES)
 def test_forward(T, F, dtype):
-    """No tokens' part: the gate is the bias, the other half 1; the largest in 16 bits by tiles of 256."""
-    K = 64
+    """No tokens' part: the gate is the bias, the other half 1."""
     v = gates(F, dtype)
     b = torch.cat([v, torch.ones(F, dtype=dtype)])[None].to(DEV)
     x, w = torch.zeros(T, K, dtype=dtype, device=DEV), torch.ones(1, 2 * F, K, dtype=dtype, device=DEV)
@@ -55,9 +55,8 @@ def test_forward(T, F, dtype):
 
 @pytest.mark.parametrize("kept", [False, True])
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,F", [(1, 64), (70, 520), (600, 4096)])
+@pytest.mark.parametrize("T,F", SIZES)
 def test_backward(T, F, dtype, kept):
-    K = 64
     v = gates(F, dtype)
     b = torch.cat([v, torch.ones(F, dtype=dtype)])[None].to(DEV)
     x, w = torch.zeros(T, K, dtype=dtype, device=DEV), torch.ones(1, 2 * F, K, dtype=dtype, device=DEV)

@@ -13,7 +13,7 @@ from oracle import gated
 from test_gpu_glu import check, glu_limits, half_step
 
 pytestmark = pytest.mark.gpu
-DEV, F32, BF = "cuda", torch.float32, torch.bfloat16
+DEV, F32, BF, K = "cuda", torch.float32, torch.bfloat16, 128
 # with each other: products of 1e-42 .. 1e76, and ordinary results from scales far apart
 SCALES = [1.0, 1e-12, 1e-30, -1e-38, 1e-44, 1e20, -1e25, 1e30, 3e38, 0.0, 2.0 ** 96, 2.0 ** 97, 2.0 ** -126]
 SUMS = [0, 1, -127, 127 * 127, 100 * 127 * 127]
@@ -46,12 +46,17 @@ def reference(host):
     return h + (0.0 if b is None else b), 3 * 2.0 ** -24 * (np.abs(h) + (0.0 if b is None else np.abs(b))) + 2.0 ** -150
 
 
-# the contraction in two parts; tiles of 32 by 64; of 128 rows; of 256
-@pytest.mark.parametrize("T,N", [(13, 72), (26, 8192), (300, 16384), (1030, 9000)])
+# kernel: rows and weight rows
+SIZES = {"32x64 parts": (13, 72), "32x64": (13, 16384), "128x128": (26, 16384), "256 ragged": (200, 24000),
+         "256 full": (1030, 9000)}
+
+
+@pytest.mark.parametrize("kernel", SIZES)
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("out", [F32, BF])
-def test_product(T, N, bias, out):
-    host, (x, xs, w, ws, b), space = problem(T, N, 128, bias, out)
+def test_product(kernel, bias, out):
+    T, N = SIZES[kernel]
+    host, (x, xs, w, ws, b), space = problem(T, N, K, bias, out)
     y = torch.empty(T, N, dtype=out, device=DEV)
     gl.gl_forward_int8(x, xs, w, ws, y, space, bias=b)
     ref, e = reference(host)
@@ -68,7 +73,6 @@ def test_product(T, N, bias, out):
 @pytest.mark.parametrize("T,F", [(13, 40), (1030, 4104)])
 def test_gated_product(T, F):
     """Gates whose sums are 0 under scales whose product overflows: what is left is the bias."""
-    K = 128
     g = torch.Generator().manual_seed(F)
     x, w = (torch.randint(-127, 128, s, generator=g, dtype=torch.int8) for s in ((T, K), (1, 2 * F, K)))
     w[0, :F] = 0
