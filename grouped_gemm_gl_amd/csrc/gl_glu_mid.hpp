@@ -65,13 +65,7 @@ __device__ __forceinline__ void read_turned(const uint32_t (&at)[B], i32x4_t (&o
   typedef __attribute__((ext_vector_type(2))) int i32x2_t;
   i32x2_t v[B][4];
 #define GL_TR(n) "ds_read_b64_tr_b16 %" #n ", "
-  if constexpr (B == 1) {
-    asm volatile(GL_TR(0) "%4\n\t" GL_TR(1) "%4 offset:%c5\n\t" GL_TR(2) "%4 offset:%c6\n\t" GL_TR(3) "%4 offset:%c7\n\t"
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3])
-                 : "v"(at[0]), "n"(4 * ROW), "n"(32 * ROW), "n"(36 * ROW)
-                 : "memory");
-  } else if constexpr (B == 2) {
+  if constexpr (B == 2) {
     asm volatile(GL_TR(0) "%8\n\t" GL_TR(1) "%8 offset:%c10\n\t" GL_TR(2) "%8 offset:%c11\n\t" GL_TR(3) "%8 offset:%c12\n\t"
                  GL_TR(4) "%9\n\t" GL_TR(5) "%9 offset:%c10\n\t" GL_TR(6) "%9 offset:%c11\n\t" GL_TR(7) "%9 offset:%c12\n\t"
                  "s_waitcnt lgkmcnt(0)"
