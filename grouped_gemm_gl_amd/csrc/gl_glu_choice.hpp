@@ -35,6 +35,12 @@ struct GluChoice {
 //   fp32, 32 cycles a matrix instruction: what counts is that no CU waits for another's tile.
 //     4 groups, 333 rows, K 1024 F 2048 37 / 69 / 216;  8 groups, 16384 rows, K 4096 F 7168
 //     (4032 tiles of 256) 16504 / 14747 / 14029
+//     (Few rows on many wide experts lose by it: 64 of 64 rows, K 2048 F 7168 706 on tiles of 64 with weights read
+//     once, 782 on those of 256; 64 of 2048 1662 / 1850; 64 of 4096, K 2048 F 4096 1497 / 1709.)
+//   8-bit integers, 25 to 96 rows a group and weights past the cache, 128 / 256: 64 groups, K 2048 F 1408, 28 rows
+//     78 / 69, 64 rows 89 / 80, 90 rows 105 / 86;  128 groups, K 2048 F 768 85 / 73, 102 / 89, 120 / 107;  8 groups,
+//     K 4096 F 7168 102 / 100, 115 / 106, 129 / 117, but at 48 rows 102 / 109;  16 groups, K 4096 F 4096 111 / 119,
+//     130 / 122, 132 / 155.
 // Among the small tiles (rows by weight rows; us):
 //   16 bits, 64 x 64 / 32 x 32: at most 256 tiles of 64: 2 groups, 64 rows, K 4096 F 2048 23.6 / 15.8, one of
 //     300, K 1024 F 1024 8.3 / 7.6 (at 1 of 128, K 4096 F 4096, 384 tiles, 23.2 / 25.8).  At most 8 rows
@@ -44,11 +50,15 @@ struct GluChoice {
 //     512, K 2048 N 1024 8.6 / 7.7; one of 32, K 4096 N 4096 10.8 / 11.2.
 //   fp32, 64 x 64 / 32 x 64: up to 896 tiles of 32, for which 768 are under way at once: 8 of 600, K 2048 F 1024
 //     (864) 71 / 60, but 4 of 333, K 1024 F 2048 (960) 37 / 41.  64 of 64, K 1024 F 512 39 / 34; one of 256,
-//     K 4096 F 4096 (1152) 137 / 165.
+//     K 4096 F 4096 (1152) 137 / 165.  4 of 333 rows, 780 / 900 / 990 / 1200 tiles: K 1024 37 / 32, 38 / 38, 38 / 43,
+//     58 / 49;  K 4096 135 / 109, 135 / 131, 137 / 169, 212 / 185.
 //   The contraction in one / two parts, by tiles of 32 x 64: 16 bits (on 32 x 32) 216 (8 of 64 groups, 8 rows, K 2048
 //     F 768) 11.2 / 10.4, 96 (one of 64, K 2048 F 1024) 9.1 / 7.7, 256 (2 of 64, K 4096 F 2048) 16.0 / 17.5;  8-bit
 //     integers 128 (one of 32, K 4096 N 4096) 11.1 / 8.6, 320 (8 of 64, K 2048 N 2048) 7.9 / 7.1, 1056 (64 of 32, K 1408
 //     N 2048) 13.5 / 19.3;  fp32 320 (8 of 40, K 2048 F 1024) 35 / 26, 544 (one of 512, K 1024 F 1024) 24.6 / 28.0.
+//     (8 groups of 64 rows, 16 bits, 190 / 220 / 260 / 320 tiles: K 1024 7.0 / 6.1, 7.1 / 6.2, 7.1 / 6.2, 7.5 / 6.5;
+//     K 2048 11.0 / 10.4, 11.3 / 11.4, 12.2 / 11.9, 13.9 / 13.3;  K 4096 18.5 / 18.8, 18.9 / 19.2, 21.3 / 20.7, 24.0 /
+//     22.7;  fp32, 4 of 333 rows, K 1024, 240 / 300 / 390 tiles 16.7 / 14.7, 22.9 / 27.3, 23.8 / 28.0.)
 //     Weights of so few tiles are past the cache only where K is very long: they are not marked as read once.
 // Weights of more than the 256 MB of the last-level cache that about one row tile of each group reads
 // are loaded as data that is read once: 64 groups, 4099 rows, K 2048 F 1400, fp16 (734 MB of weights),

@@ -11,9 +11,9 @@
 // by 16 columns of either half, so h_g and h_u are in the same lane.
 //
 // Bound by the weights' bytes in flight: 64 groups, 4099 rows, K 2048 F 1400, fp16, 172 us for 734 MB
-// (4.3 TB/s, tiles of 128); 32 of 64 rows, K 1408 N 2048, int8, 13.6 us for 73 MB (5.4 TB/s, 32 by 64).  A
-// ring of five stages was slower, of three (fp32, three workgroups a CU) 5% slower at 333 rows and up to 7%
-// faster at more.
+// (4.3 TB/s from HBM, tiles of 128); 32 of 64 rows, K 1408 N 2048, int8, 13.6 us for 73 MB (5.4 TB/s, most of it
+// from the last-level cache, 32 by 64).  A ring of five stages was slower, of three (fp32, three workgroups a CU) 5%
+// slower at 333 rows and up to 7% faster at more.
 #pragma once
 
 #include "gl_gemm_tile.hpp"
@@ -124,7 +124,7 @@ __device__ __forceinline__ void add_parts(char *lds, int part, int wave, int lan
   }
 }
 
-// ONCE: the weights are loaded as data that is read once; PARTS of the contraction (see launch_glu).
+// ONCE: the weights are loaded as data that is read once; PARTS of the contraction (see choose_glu).
 template <int IN, int EL, int EPI, int ROWS, int WEIGHT_ROWS, bool ONCE, int PARTS>
 __global__ __launch_bounds__((PARTS * MidTile<ROWS, WEIGHT_ROWS>::kThreads), 2) void glu_mid_kernel(GluParams p) {
   using Op = Operand<IN>;

@@ -40,8 +40,11 @@
 // (read_turned, which waits for itself: there a phase's loads go out before its reads).
 //
 // Bound by the matrix cores: 8 groups, 16384 rows, K 4096 F 7168 bf16 1425 us, 1350 TFLOP/s (with h 1475), int8
-// 782 us, 2460 TOP/s; a library product of that size reaches 1438 and 2313.  dx and dW 1640 and 1660 us, 1170
-// and 1160 TFLOP/s, by the reads of the turned operands.  Without the lag of the second wave group 1651.
+// 760-790 us, 2430-2530 TOP/s; a library product of that size reaches 1438 and 2313.  dx and dW 1640-1720 and
+// 1660-1690 us, 1120-1170 and 1140-1160 TFLOP/s, by the number of their reads: a turned fragment is four reads where
+// the others are two, and a phase waits for its own.  Matrix cores busy 70% and 59% of the CUs' cycles (83%
+// forward, 80% the gradient), LDS 27% and 24% (34%, 32%), conflicts in 1% and 4% of those.  Without the lag of the
+// second wave group 1651.
 #pragma once
 
 #include "gl_gemm_tile.hpp"
