@@ -94,9 +94,9 @@ inline GluChoice choose_glu(int in, bool plain, int64_t G, int64_t T, int64_t K,
 }
 
 struct BackChoice {
-  int rows, cols, stages, parts;  // the tile (256: gl_glu_tile.hpp's), the ring's stages, parts of the contraction
-  bool once;                      // below 256: dx's weights or dW are past the cache
-  int tiles;                      // 256: the form
+  int rows, cols, parts;  // the tile (256: gl_glu_tile.hpp's), parts of the contraction
+  bool once;              // below 256: dx's weights or dW are past the cache
+  int tiles;              // 256: the form
   int64_t items;
 };
 
@@ -123,12 +123,12 @@ struct BackChoice {
 inline BackChoice choose_glu_back(int in, bool wgrad, bool out_f32, int64_t G, int64_t T, int64_t K, int64_t N) {
   const int64_t groups = T < G ? T : G, rows = T / groups;
   const int64_t tiles32 = ((T + 31) / 32 + groups) * ((K + 63) / 64);
-  auto tile = [](int r, int c, int stages, int parts, bool once) { return BackChoice{r, c, stages, parts, once, 0, 0}; };
+  auto tile = [](int r, int c, int parts, bool once) { return BackChoice{r, c, parts, once, 0, 0}; };
   if (in == IN_F32) {
-    if (wgrad) return tile(64, 64, 3, 1, G * N * K * 4 > kLastLevelCache);
-    if (tiles32 <= 384) return tile(32, 64, 4, 2, false);
+    if (wgrad) return tile(64, 64, 1, G * N * K * 4 > kLastLevelCache);
+    if (tiles32 <= 384) return tile(32, 64, 2, false);
     const bool once = rows <= 96 && groups * K * N * 4 > kLastLevelCache;
-    return rows <= 32 || tiles32 <= 896 ? tile(32, 64, 4, 1, once) : tile(64, 64, 4, 1, once);
+    return rows <= 32 || tiles32 <= 896 ? tile(32, 64, 1, once) : tile(64, 64, 1, once);
   }
   auto tiles = [&](int64_t r) {
     return (wgrad ? groups * ((N + r - 1) / r) : (T + r - 1) / r + groups) * ((K + r - 1) / r);
@@ -136,14 +136,14 @@ inline BackChoice choose_glu_back(int in, bool wgrad, bool out_f32, int64_t G, i
   if (!wgrad) {
     const bool large = groups * K * N * in_bytes(in) > kLastLevelCache;  // weights
     if (tiles(256) >= 160 && (rows <= 24 || rows > 96))
-      return {256, 256, 0, 1, false, rows > 256 ? kFullTiles : large ? kRaggedOnce : kRaggedTiles, tiles(256)};
-    if (tiles(128) >= 192) return tile(128, 128, 4, 1, large && rows <= 96);
-    return tiles32 <= 256 ? tile(32, 64, 4, 2, false) : tile(64, 64, 4, 1, false);
+      return {256, 256, 1, false, rows > 256 ? kFullTiles : large ? kRaggedOnce : kRaggedTiles, tiles(256)};
+    if (tiles(128) >= 192) return tile(128, 128, 1, large && rows <= 96);
+    return tiles32 <= 256 ? tile(32, 64, 2, false) : tile(64, 64, 1, false);
   }
   if (tiles(256) >= 128)
-    return {256, 256, 0, 1, false, G * N * K * (out_f32 ? 4 : in_bytes(in)) > kLastLevelCache ? kWrittenOnce : kFullTiles,
+    return {256, 256, 1, false, G * N * K * (out_f32 ? 4 : in_bytes(in)) > kLastLevelCache ? kWrittenOnce : kFullTiles,
             G * ((N + 255) / 256) * ((K + 255) / 256)};
-  return tiles(128) >= 192 ? tile(128, 128, 4, 1, false) : tile(64, 64, 4, 1, false);
+  return tiles(128) >= 192 ? tile(128, 128, 1, false) : tile(64, 64, 1, false);
 }
 
 }  // namespace gl
