@@ -852,6 +852,8 @@ def gl_glu_backward(x: Tensor, w: Grouped, da: Tensor, dh: Tensor, dx: Optional[
     _matrix(h, T, N, dt, "h")
     _matrix(a, T, F, dt, "a")
     _matrix(dx, T, K, dt, "dx", more=True)
+    if not isinstance(dw, Tensor) and len(dw) != G:
+        raise ValueError(f"dw must be a tensor or a list of {G}")
     wd = (dw if isinstance(dw, Tensor) else dw[0]).dtype
     if wd not in _DT:
         raise ValueError(f"unsupported dtype {wd}")

@@ -1,8 +1,9 @@
-"""One buffer given for two of the gated layer's, where one would be overwritten while it is still
-read, or by the other: refused before anything is enqueued."""
+"""Refusals of the gated layer: one buffer given for two, where one would be overwritten while it is still
+read, or by the other, and an empty list.  All before anything is enqueued."""
 import os
 
 import pytest
+import torch
 
 import grouped_gemm_gl_amd as gl
 from test_abi_gated import A, B, C_, GLU, GLU_B, INT8
@@ -31,3 +32,9 @@ def test_int8_products():
     v = list({**INT8, "y": INT8["x"]}.values())
     assert gl.load().gl_forward_int8(*v, None) == -1 and gl.load().gl_last_error()
     assert gl.load().gl_glu_forward_int8(*v[:5], 0, *v[5:], None) == -1 and gl.load().gl_last_error()
+
+
+def test_backward_refuses_an_empty_list_of_gradients():
+    t = lambda *s: torch.empty(*s)  # noqa: E731
+    with pytest.raises(ValueError, match="dw"):
+        gl.gl_glu_backward(t(3, 64), t(2, 32, 64), t(3, 16), t(3, 32), None, [], torch.empty(1 << 26, dtype=torch.uint8))
