@@ -37,4 +37,4 @@ def test_int8_products():
 def test_backward_refuses_an_empty_list_of_gradients():
     t = lambda *s: torch.empty(*s)  # noqa: E731
     with pytest.raises(ValueError, match="dw"):
-        gl.gl_glu_backward(t(3, 64), t(2, 32, 64), t(3, 16), t(3, 32), None, [], torch.empty(1 << 26, dtype=torch.uint8))
+        gl.gl_glu_backward(t(3, 64), t(2, 32, 64), t(3, 16), t(3, 32), None, [], torch.empty(gl.gl_workspace_size(2), dtype=torch.uint8))
